@@ -1,0 +1,62 @@
+/*
+ * moe_serving.h — C ABI of the serving operators around the routed expert path on MI355X (gfx950):
+ *
+ *   moe_rmsnorm             residual addition and root-mean-square norm in front of the layer, with
+ *                           bf16 rows and/or E4M3 codes out
+ *   moe_quantize_fp8_block  E4M3 codes of bf16 rows with one scale per 128 columns
+ *
+ * The conventions of moe_mi355x.h hold here as well: device pointers owned by the caller and 16-byte
+ * aligned, row-major contiguous layouts, bf16 as uint16_t bit patterns, no allocation, no
+ * synchronisation, work on `stream` only, launches that depend on host scalars only (so that every
+ * call can be captured in a HIP graph), host-checkable arguments checked before anything is enqueued.
+ */
+#ifndef MOE_SERVING_H
+#define MOE_SERVING_H
+
+#include "../moe_mi355x.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Columns under one scale of the block-scaled E4M3 format (weights: 128 x 128 blocks). */
+#define MOE_FP8_BLOCK 128
+
+/* E4M3 quantisation, shared by the operators below.  For the values v of one scale group (a row, or
+ * 128 consecutive columns of a row; the last group of a row may be shorter), in fp32:
+ *   amax = max |v|; scale = a / 448, f = 448 / a with a = max(amax, 2^-100) (the floor keeps f finite);
+ *   code = e4m3(v * f), round to nearest even; an all-zero group has scale 1 and zero codes.
+ * A NaN gives a NaN code and does not enter amax.  An infinity makes its group's scale infinite (its
+ * own code NaN, the other codes 0). */
+
+/* Residual addition and root-mean-square norm of `rows` rows of `k` columns:
+ *   h = bf16(x + residual)            (h = x without a residual)
+ *   y = (h * weight) * (1 / sqrt(mean(h^2) + eps)), in fp32
+ *   x            bf16 [rows, k]
+ *   residual     bf16 [rows, k] or NULL
+ *   weight       bf16 [k]
+ *   residual_out bf16 [rows, k]: h; required with a residual, NULL without.  May be `residual` itself
+ *                (the usual update in place) or `x`.
+ *   y_out        bf16 [rows, k] or NULL: y rounded once to bf16; may be `x`
+ *   q            uint8 [rows, k] or NULL: E4M3 codes of the fp32 y (not of its bf16 rounding)
+ *   scale        fp32, with q: [rows] (scale_block 0, what moe_grouped_gemm_fp8 reads) or
+ *                [rows, ceil(k/128)] (scale_block 128, what moe_grouped_gemm_fp8_block reads)
+ * The norm is taken of the rounded h, the value that later layers read back, so that it can be
+ * recomputed from residual_out bit for bit.  Sums of squares are fp32: a row whose sum of squares
+ * passes the fp32 range comes out as zeros.  eps >= 0; with eps 0 a row of zeros gives NaN.
+ * At least one of y_out and q.  k % 8 == 0, with q k % 16 == 0; k <= 2^20.  rows == 0 enqueues nothing. */
+moe_status moe_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps,
+                       int64_t rows, int32_t k, uint16_t* residual_out, uint16_t* y_out, uint8_t* q, float* scale,
+                       int32_t scale_block, moe_stream stream);
+
+/* E4M3 codes of bf16 rows with one scale per 128 columns.
+ *   x bf16 [rows, k], q uint8 [rows, k], scale fp32 [rows, ceil(k/128)].  With sorted_ids (i32 [rows])
+ *   only rows r with sorted_ids[r] in [0, num_pairs) are written (the real sorted rows of Hs); NULL
+ *   writes every row.  k % 16 == 0.  rows == 0 enqueues nothing. */
+moe_status moe_quantize_fp8_block(const uint16_t* x, int64_t rows, int32_t k, const int32_t* sorted_ids,
+                                  int64_t num_pairs, uint8_t* q, float* scale, moe_stream stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* MOE_SERVING_H */

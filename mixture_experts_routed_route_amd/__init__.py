@@ -9,3 +9,4 @@ from ._lib import (LIB_PATH, MOE_OP_DOWN, MOE_OP_GATE_UP_SILU, MOE_OP_GATHER, MO
                    MoeError, lib)
 from .layer import Buffers, MoeLayer
 from .ops import *  # noqa: F401,F403
+from .serving import *  # noqa: F401,F403

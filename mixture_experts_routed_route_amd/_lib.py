@@ -1,4 +1,5 @@
-"""ctypes view of the C ABI in ``include/moe_mi355x.h`` and ``include/moe_probes.h``
+"""ctypes view of the C ABI in ``include/moe_mi355x.h``, ``include/moe_probes.h`` and
+``include/serving/moe_serving.h``
 (``_lib/libmoe_mi355x.so``).
 
 No fallback: if the library is missing, loading raises and nothing runs.
@@ -15,7 +16,7 @@ MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_ELAUNCH = 0, -1, -2, -3
 MOE_W_BF16, MOE_W_INT4_GPTQ, MOE_W_FP8 = 0, 1, 2
 MOE_OP_GATE_UP_SILU, MOE_OP_DOWN, MOE_OP_GATHER = 0, 1, 2
 
-# every symbol the header declares: name -> (restype, argtypes)
+# every symbol moe_mi355x.h and moe_probes.h declare: name -> (restype, argtypes)
 SIGNATURES = {
     "moe_last_error": (c_char_p, []),
     "moe_abi_version": (c_int32, []),
@@ -66,6 +67,14 @@ SIGNATURES = {
     "moe_probe_mfma_bf16": (c_int32, [c_int64, c_void_p, c_int32, c_void_p]),
 }
 
+# every symbol serving/moe_serving.h declares
+SERVING_SIGNATURES = {
+    "moe_rmsnorm": (c_int32, [c_void_p, c_void_p, c_void_p, c_float, c_int64, c_int32, c_void_p, c_void_p, c_void_p,
+                              c_void_p, c_int32, c_void_p]),
+    "moe_quantize_fp8_block": (c_int32, [c_void_p, c_int64, c_int32, c_void_p, c_int64, c_void_p, c_void_p,
+                                         c_void_p]),
+}
+
 
 class MoeWeight(ctypes.Structure):
     """struct moe_weight of the header."""
@@ -83,7 +92,7 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"HIP library not built ({LIB_PATH}); run "
                                "`python -m mixture_experts_routed_route_amd.build`")
         L = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in SIGNATURES.items():
+        for name, (res, args) in {**SIGNATURES, **SERVING_SIGNATURES}.items():
             f = getattr(L, name)
             f.restype = res
             f.argtypes = args

@@ -2,6 +2,7 @@
 // checks, pure host helpers, and the launches of the gfx950 kernels.
 #include "../../include/moe_mi355x.h"
 #include "../../include/moe_probes.h"
+#include "../../include/serving/moe_serving.h"
 
 #include <hip/hip_runtime.h>
 
@@ -697,6 +698,50 @@ moe_status moe_combine(const uint16_t* ys, const int32_t* inv_sorted, const floa
                  "%s: slot-major combine needs ys_rows >= num_tokens*top_k", who);
     return launched(who, moe::launch_combine(ys, inv_sorted, topk_w, out, num_tokens, top_k, hidden, ys_rows,
                                              static_cast<hipStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ serving operators (moe_serving.h)
+moe_status moe_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps,
+                       int64_t rows, int32_t k, uint16_t* residual_out, uint16_t* y_out, uint8_t* q, float* scale,
+                       int32_t scale_block, moe_stream stream) {
+    const char* who = "moe_rmsnorm";
+    REQUIRE(rows >= 0, "%s: rows %lld is negative", who, static_cast<long long>(rows));
+    REQUIRE(k >= 8 && k % 8 == 0 && k <= (1 << 20), "%s: k %d must be a positive multiple of 8, at most 2^20", who, k);
+    REQUIRE(eps >= 0.0f, "%s: eps must not be negative or NaN", who);
+    REQUIRE(y_out != nullptr || q != nullptr, "%s: one of y_out and q is needed", who);
+    REQUIRE((residual == nullptr) == (residual_out == nullptr), "%s: residual and residual_out go together", who);
+    REQUIRE(residual_out == nullptr || residual_out != y_out, "%s: residual_out and y_out are one buffer", who);
+    REQUIRE(scale_block == 0 || scale_block == MOE_FP8_BLOCK, "%s: scale_block %d not 0 or %d", who, scale_block,
+            MOE_FP8_BLOCK);
+    REQUIRE((q == nullptr) == (scale == nullptr), "%s: q and scale go together", who);
+    if (q) REQUIRE(k % 16 == 0, "%s: k %d must be a multiple of 16 with q", who, k);
+    if (rows == 0) return ok();
+    REQUIRE_PTR(who, x);
+    REQUIRE_PTR(who, weight);
+    if (residual) REQUIRE_PTR(who, residual);
+    if (residual_out) REQUIRE_PTR(who, residual_out);
+    if (y_out) REQUIRE_PTR(who, y_out);
+    if (q) {
+        REQUIRE_PTR(who, q);
+        REQUIRE_PTR(who, scale);
+    }
+    return launched(who, moe::launch_rmsnorm(x, residual, weight, eps, rows, k, residual_out, y_out, q, scale,
+                                             scale_block, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_quantize_fp8_block(const uint16_t* x, int64_t rows, int32_t k, const int32_t* sorted_ids,
+                                  int64_t num_pairs, uint8_t* q, float* scale, moe_stream stream) {
+    const char* who = "moe_quantize_fp8_block";
+    REQUIRE(k >= 16 && k % 16 == 0, "%s: k %d must be a positive multiple of 16", who, k);
+    REQUIRE(rows >= 0, "%s: rows %lld is negative", who, static_cast<long long>(rows));
+    REQUIRE(num_pairs >= 0 && num_pairs < INT32_MAX, "%s: num_pairs out of range", who);
+    if (rows == 0) return ok();
+    REQUIRE_PTR(who, x);
+    REQUIRE_PTR(who, q);
+    REQUIRE_PTR(who, scale);
+    if (sorted_ids) REQUIRE_PTR(who, sorted_ids);
+    return launched(who, moe::launch_quantize_fp8_block(x, rows, k, sorted_ids, static_cast<int>(num_pairs), q, scale,
+                                                        static_cast<hipStream_t>(stream)));
 }
 
 // ------------------------------------------------------------------ ceiling probes (moe_probes.h)

@@ -95,6 +95,12 @@ hipError_t launch_lora_gather_fold(const uint16_t* x, int64_t x_rows, uint16_t* 
                                    const uint64_t* b_tab, const float* s_tab, int n_tab, int n_ad, int k_in, int n_out,
                                    int max_rank, uint16_t* xa, hipStream_t s);
 
+// rmsnorm.hip: residual addition, norm and E4M3 output; block quantisation
+hipError_t launch_rmsnorm(const uint16_t* x, const uint16_t* r, const uint16_t* w, float eps, int64_t rows, int K,
+                          uint16_t* h_out, uint16_t* y, uint8_t* q, float* scale, int scale_block, hipStream_t s);
+hipError_t launch_quantize_fp8_block(const uint16_t* x, int64_t rows, int K, const int32_t* sorted_ids, int P,
+                                     uint8_t* q, float* scale, hipStream_t s);
+
 // probes.hip (ceiling probes, not steps of the path)
 hipError_t launch_probe_stream_read(const void* src, int64_t bytes, uint32_t* sink, int blocks, hipStream_t s);
 hipError_t launch_probe_mfma_bf16(int64_t iters, float* sink, int blocks, hipStream_t s);

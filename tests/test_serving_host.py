@@ -1,0 +1,162 @@
+"""Serving operators, CPU side: the library exports what serving/moe_serving.h declares, the C ABI and
+the binding refuse invalid calls before anything is enqueued, and the oracle's functions are pinned
+to closed forms and to torch."""
+import ctypes
+import os
+import re
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_routed_route_amd as m
+import oracle
+from _util import ROOT
+from moe_synth import f32_to_bf16_bits
+
+HEADER = os.path.join(ROOT, "include", "serving", "moe_serving.h")
+
+
+@pytest.fixture(scope="module")
+def L():
+    from mixture_experts_routed_route_amd import _lib
+    if not os.path.exists(_lib.LIB_PATH):
+        from mixture_experts_routed_route_amd.build import build
+        build()
+    return _lib.lib()
+
+
+def test_exports_every_declared_symbol(L):
+    from mixture_experts_routed_route_amd import _lib
+    src = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = set(re.findall(r"^(?:moe_status|int64_t|int32_t)\s+(moe_\w+)\s*\(", src, flags=re.M))
+    assert names == set(_lib.SERVING_SIGNATURES)
+    for n in names:
+        assert hasattr(L, n), f"{n} not exported"
+
+
+def _rc(L, name, *args):
+    rc = getattr(L, name)(*args)
+    return rc, L.moe_last_error().decode()
+
+
+FAKE = ctypes.c_void_p(1 << 20)   # never dereferenced: every call below fails validation or has no rows
+OFF = ctypes.c_void_p((1 << 20) + 8)
+
+
+# moe_rmsnorm(x, residual, weight, eps, rows, k, residual_out, y, q, scale, scale_block, stream)
+RMSNORM_BAD = [
+    ((FAKE, None, FAKE, 1e-6, 4, 20, None, FAKE, None, None, 0, None), "k 20"),
+    ((FAKE, None, FAKE, 1e-6, 4, 0, None, FAKE, None, None, 0, None), "k 0"),
+    ((FAKE, None, FAKE, 1e-6, 4, (1 << 20) + 8, None, FAKE, None, None, 0, None), "2^20"),
+    ((FAKE, None, FAKE, 1e-6, 4, 24, None, None, FAKE, FAKE, 0, None), "multiple of 16"),
+    ((FAKE, None, FAKE, 1e-6, -1, 64, None, FAKE, None, None, 0, None), "negative"),
+    ((FAKE, None, FAKE, -1.0, 4, 64, None, FAKE, None, None, 0, None), "eps"),
+    ((FAKE, None, FAKE, float("nan"), 4, 64, None, FAKE, None, None, 0, None), "eps"),
+    ((FAKE, None, FAKE, 1e-6, 4, 64, None, None, None, None, 0, None), "one of y_out and q"),
+    ((FAKE, FAKE, FAKE, 1e-6, 4, 64, None, FAKE, None, None, 0, None), "go together"),
+    ((FAKE, None, FAKE, 1e-6, 4, 64, FAKE, FAKE, None, None, 0, None), "go together"),
+    ((FAKE, FAKE, FAKE, 1e-6, 4, 64, FAKE, FAKE, None, None, 0, None), "one buffer"),
+    ((FAKE, None, FAKE, 1e-6, 4, 64, None, None, FAKE, None, 0, None), "go together"),
+    ((FAKE, None, FAKE, 1e-6, 4, 64, None, None, FAKE, FAKE, 64, None), "scale_block"),
+    ((None, None, FAKE, 1e-6, 4, 64, None, FAKE, None, None, 0, None), "x is NULL"),
+    ((OFF, None, FAKE, 1e-6, 4, 64, None, FAKE, None, None, 0, None), "aligned"),
+    ((FAKE, None, None, 1e-6, 4, 64, None, FAKE, None, None, 0, None), "weight is NULL"),
+]
+
+
+@pytest.mark.parametrize("args,word", RMSNORM_BAD, ids=[str(i) for i in range(len(RMSNORM_BAD))])
+def test_rmsnorm_refusals(L, args, word):
+    rc, msg = _rc(L, "moe_rmsnorm", *args)
+    assert rc == -1 and word in msg, msg
+
+
+def test_rmsnorm_and_quantize_without_rows_enqueue_nothing(L):
+    assert L.moe_rmsnorm(None, None, None, 1e-6, 0, 64, None, FAKE, None, None, 0, None) == 0
+    assert L.moe_quantize_fp8_block(None, 0, 64, None, 0, None, None, None) == 0
+
+
+def test_quantize_block_refusals(L):
+    for args, word in [((FAKE, 4, 24, None, 0, FAKE, FAKE, None), "multiple of 16"),
+                       ((FAKE, -1, 32, None, 0, FAKE, FAKE, None), "negative"),
+                       ((FAKE, 4, 32, None, -1, FAKE, FAKE, None), "num_pairs"),
+                       ((None, 4, 32, None, 0, FAKE, FAKE, None), "x is NULL"),
+                       ((FAKE, 4, 32, OFF, 8, FAKE, FAKE, None), "aligned"),
+                       ((FAKE, 4, 32, None, 0, FAKE, None, None), "scale is NULL")]:
+        rc, msg = _rc(L, "moe_quantize_fp8_block", *args)
+        assert rc == -1 and word in msg, msg
+
+
+# ------------------------------------------------------------------------------------- the binding
+def bf(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def u8(*shape):
+    return torch.zeros(shape, dtype=torch.uint8)
+
+
+def test_rmsnorm_binding_refuses_mismatched_buffers():
+    x, w = bf(4, 256), bf(256)
+    for kw, word in [(dict(weight=bf(128)), "weight"), (dict(residual=bf(4, 128)), "residual is"),
+                     (dict(residual_out=bf(4, 256)), "without residual"), (dict(y=bf(3, 256)), "y is"),
+                     (dict(q=u8(4, 256)), "go together"), (dict(q=u8(4, 255), scale=torch.zeros(4)), "q is"),
+                     (dict(q=u8(4, 256), scale=torch.zeros(3)), "scale is"),
+                     (dict(q=u8(4, 256), scale=torch.zeros(4, 3)), "scale is"),
+                     (dict(q=u8(4, 256), scale=torch.zeros(4, 1)), "scale is")]:
+        args = {"weight": w, **kw}
+        with pytest.raises(ValueError, match=word):
+            m.moe_rmsnorm(x, args.pop("weight"), 1e-6, **args)
+    with pytest.raises(ValueError, match="rows, k"):
+        m.moe_rmsnorm(bf(256), w)
+    with pytest.raises(ValueError, match="HIP device"):
+        m.moe_rmsnorm(x, w)
+
+
+def test_quantize_block_binding_refuses_mismatched_buffers():
+    for q, s, word in [(u8(4, 128), torch.zeros(4, 2), "q is"), (u8(4, 256), torch.zeros(4), "scale is"),
+                       (u8(4, 256), torch.zeros(4, 3), "scale is")]:
+        with pytest.raises(ValueError, match=word):
+            m.moe_quantize_fp8_block(bf(4, 256), q, s)
+    r = m.Routing.allocate(4, 2, 2, 16, "cpu")
+    rows = r.max_pad + 16
+    with pytest.raises(ValueError, match="sorted_ids"):
+        m.moe_quantize_fp8_block(bf(rows, 128), u8(rows, 128), torch.zeros(rows, 1), r)
+
+
+# -------------------------------------------------------------------------------------- the oracle
+def test_oracle_rmsnorm_closed_form():
+    """A row of one value v has mean square v^2: y = w * sign(v) without eps; x + residual rounds to
+    bf16 before the norm (256 + 1 is halfway between bf16 values 256 and 258: ties to even, 256)."""
+    x = f32_to_bf16_bits(np.array([[2.0] * 8, [-3.0] * 8, [256.0] * 8], np.float32))
+    r = f32_to_bf16_bits(np.array([[0.0] * 8, [0.0] * 8, [1.0] * 8], np.float32))
+    w = f32_to_bf16_bits(np.arange(1, 9, dtype=np.float32))
+    h, y = oracle.rmsnorm(x, w, 0.0, r)
+    assert (h[2] == 256.0).all()
+    np.testing.assert_allclose(y, np.array([1.0, -1.0, 1.0])[:, None] * np.arange(1, 9), rtol=1e-15)
+    _, y = oracle.rmsnorm(np.zeros((1, 8), np.uint16), w, 1e-6)
+    assert (y == 0).all()
+
+
+def test_oracle_block_quantisation_matches_torch():
+    rng = np.random.default_rng(5)
+    x = torch.from_numpy(rng.standard_normal((7, 272)).astype(np.float32)).bfloat16().float()
+    x[3, 128:256] = 0
+    q, s = oracle.quantize_blocks_fp8(x.numpy())
+    assert s.shape == (7, 3) and (s[3, 1] == 1) and (q[3, 128:256] == 0).all()
+    for r in range(7):
+        for b in range(3):
+            part = x[r, 128 * b: 128 * b + 128]
+            amax = part.abs().max()
+            f = torch.tensor(448.0) / amax if amax > 0 else torch.tensor(1.0)
+            want = (part * f).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+            assert np.array_equal(want, q[r, 128 * b: 128 * b + 128])
+            if amax > 0:
+                assert s[r, b] == (amax / 448.0).item()
+
+
+def test_oracle_block_quantisation_floor():
+    x = np.zeros((1, 128), np.float32)
+    x[0, 0] = 2.0 ** -120
+    q, s = oracle.quantize_blocks_fp8(x)
+    assert s[0, 0] == np.float32(2.0 ** -100) / np.float32(448) and not (q & 0x7F).any()
