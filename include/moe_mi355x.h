@@ -19,6 +19,9 @@
  *   moe_lora_gather_fold  the same fold on slot-major rows (decode, no sorting)
  *   moe_combine       top-k weighted sum of the expert outputs per token
  *
+ * serving/moe_serving.h declares the serving operators around the path (the norm in front of it,
+ * block-scaled fp8, the whole layer for a few tokens).
+ *
  * Sources (cited by page and item; the pages are Rust host code of four
  * projects):  ferrum-kernels `src/backend/cuda/moe.rs` (route_topk_softmax,
  * moe_build_pairs_by_token, moe_align_block_size[_pair_ids], moe_combine,
@@ -180,8 +183,10 @@ moe_status moe_route_align(const float* logits, int32_t num_tokens, int32_t num_
  *                    consecutive k (ferrum triton_fused_moe.rs, TritonStackedGptqWeight).
  *   MOE_W_FP8:       data = uint8 OCP FP8 E4M3 codes [E, N, K] (K contiguous);
  *                    scales = fp32 [E, N]; W[n,k] = value(code) * scales[e, n].  Used by
- *                    moe_grouped_gemm_fp8 only. */
-typedef enum { MOE_W_BF16 = 0, MOE_W_INT4_GPTQ = 1, MOE_W_FP8 = 2 } moe_wtype;
+ *                    moe_grouped_gemm_fp8 and moe_few_tokens only.
+ *   MOE_W_FP8_BLOCK: data as MOE_W_FP8; scales = fp32 [E, ceil(N/128), ceil(K/128)], one per
+ *                    128 x 128 block.  Used by the operators of serving/moe_serving.h only. */
+typedef enum { MOE_W_BF16 = 0, MOE_W_INT4_GPTQ = 1, MOE_W_FP8 = 2, MOE_W_FP8_BLOCK = 3 } moe_wtype;
 typedef struct moe_weight {
     int32_t type;            /* moe_wtype */
     int32_t group_size;      /* G (int4 only): multiple of 32, divides K */

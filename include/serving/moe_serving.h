@@ -4,6 +4,7 @@
  *   moe_rmsnorm             residual addition and root-mean-square norm in front of the layer, with
  *                           bf16 rows and/or E4M3 codes out
  *   moe_quantize_fp8_block  E4M3 codes of bf16 rows with one scale per 128 columns
+ *   moe_few_tokens          the whole routed layer for at most 32 tokens, in two launches
  *
  * The conventions of moe_mi355x.h hold here as well: device pointers owned by the caller and 16-byte
  * aligned, row-major contiguous layouts, bf16 as uint16_t bit patterns, no allocation, no
@@ -55,6 +56,37 @@ moe_status moe_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16
  *   writes every row.  k % 16 == 0.  rows == 0 enqueues nothing. */
 moe_status moe_quantize_fp8_block(const uint16_t* x, int64_t rows, int32_t k, const int32_t* sorted_ids,
                                   int64_t num_pairs, uint8_t* q, float* scale, moe_stream stream);
+
+/* The whole routed layer for a few tokens (moe_route, gate/up + SiLU, down and moe_combine), without
+ * a sorted layout, in two launches:
+ *   ids, w = moe_route(logits)                 bit for bit
+ *   h[t,j] = bf16(silu(x[t] Wg[e]^T) * (x[t] Wu[e]^T)), e = ids[t,j], from fp32 sums
+ *   out[t] = bf16(sum_j w[t,j] * (h[t,j] Wd[e]^T)), fp32, the expert outputs not rounded in between
+ *   logits   fp32 [num_tokens, num_experts], finite
+ *   x        bf16 [num_tokens, hidden]
+ *   w_gate, w_up  weights with N = inter, K = hidden; w_down with N = hidden, K = inter.  One type for
+ *            all three: MOE_W_BF16, MOE_W_INT4_GPTQ (one group size), MOE_W_FP8 or MOE_W_FP8_BLOCK.
+ *            Activations stay bf16 with every type (fp8 weights are not multiplied by quantised
+ *            activations, as moe_grouped_gemm_fp8 does).
+ *   topk_ids i32 [num_tokens, top_k], topk_w fp32 [num_tokens, top_k]   out
+ *   out      bf16 [num_tokens, hidden]
+ *   workspace  >= moe_few_tokens_workspace_bytes(...) bytes, zero-filled once before its first use;
+ *            every call leaves its counters at zero again.  Calls that share one must not overlap
+ *            (streams, or replays of graphs captured with it).  One made for more tokens, or the
+ *            larger of two layers' sizes, serves both.
+ * Results do not depend on the order in which workgroups finish.  num_tokens <= 32, top_k <= 32,
+ * num_experts <= 256, hidden <= 65536 (MOE_EUNSUPPORTED above); hidden and inter multiples of 8 (bf16),
+ * 16 (fp8), 64 and the group size (int4); each expert matrix under 2 GiB (MOE_EUNSUPPORTED).
+ * num_tokens == 0 enqueues nothing. */
+moe_status moe_few_tokens(const float* logits, const uint16_t* x, const moe_weight* w_gate, const moe_weight* w_up,
+                          const moe_weight* w_down, int32_t num_tokens, int32_t num_experts, int32_t top_k,
+                          int32_t hidden, int32_t inter, int32_t renormalize, int32_t* topk_ids, float* topk_w,
+                          uint16_t* out, void* workspace, int64_t workspace_bytes, moe_stream stream);
+
+/* Bytes of workspace for up to num_tokens tokens (wtype: the moe_wtype of the weights); -1 on invalid
+ * arguments. */
+int64_t moe_few_tokens_workspace_bytes(int32_t num_tokens, int32_t num_experts, int32_t top_k, int32_t hidden,
+                                       int32_t inter, int32_t wtype);
 
 #ifdef __cplusplus
 }

@@ -13,7 +13,7 @@ from ctypes import POINTER, c_char_p, c_float, c_int32, c_int64, c_uint64, c_voi
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libmoe_mi355x.so")
 
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_ELAUNCH = 0, -1, -2, -3
-MOE_W_BF16, MOE_W_INT4_GPTQ, MOE_W_FP8 = 0, 1, 2
+MOE_W_BF16, MOE_W_INT4_GPTQ, MOE_W_FP8, MOE_W_FP8_BLOCK = 0, 1, 2, 3
 MOE_OP_GATE_UP_SILU, MOE_OP_DOWN, MOE_OP_GATHER = 0, 1, 2
 
 # every symbol moe_mi355x.h and moe_probes.h declare: name -> (restype, argtypes)
@@ -73,6 +73,9 @@ SERVING_SIGNATURES = {
                               c_void_p, c_int32, c_void_p]),
     "moe_quantize_fp8_block": (c_int32, [c_void_p, c_int64, c_int32, c_void_p, c_int64, c_void_p, c_void_p,
                                          c_void_p]),
+    "moe_few_tokens_workspace_bytes": (c_int64, [c_int32] * 6),
+    "moe_few_tokens": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32,
+                                 c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p]),
 }
 
 

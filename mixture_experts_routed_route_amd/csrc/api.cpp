@@ -12,6 +12,7 @@
 #include <cstring>
 #include <string>
 
+#include "few_tokens.h"
 #include "launchers.h"
 
 namespace {
@@ -742,6 +743,89 @@ moe_status moe_quantize_fp8_block(const uint16_t* x, int64_t rows, int32_t k, co
     if (sorted_ids) REQUIRE_PTR(who, sorted_ids);
     return launched(who, moe::launch_quantize_fp8_block(x, rows, k, sorted_ids, static_cast<int>(num_pairs), q, scale,
                                                         static_cast<hipStream_t>(stream)));
+}
+
+int64_t moe_few_tokens_workspace_bytes(int32_t num_tokens, int32_t num_experts, int32_t top_k, int32_t hidden,
+                                       int32_t inter, int32_t wtype) {
+    if (num_tokens < 0 || num_tokens > moe::kFewTokens || num_experts < 1 || num_experts > 256 || top_k < 1 ||
+        top_k > moe::kFewTopK || top_k > num_experts || hidden < 8 || hidden > moe::kFewMaxHidden || inter < 8 ||
+        wtype < MOE_W_BF16 || wtype > MOE_W_FP8_BLOCK)
+        return -1;
+    return moe::few_layout(num_tokens, num_experts, top_k, hidden, inter, wtype == MOE_W_INT4_GPTQ).bytes;
+}
+
+moe_status moe_few_tokens(const float* logits, const uint16_t* x, const moe_weight* w_gate, const moe_weight* w_up,
+                          const moe_weight* w_down, int32_t num_tokens, int32_t num_experts, int32_t top_k,
+                          int32_t hidden, int32_t inter, int32_t renormalize, int32_t* topk_ids, float* topk_w,
+                          uint16_t* out, void* workspace, int64_t workspace_bytes, moe_stream stream) {
+    const char* who = "moe_few_tokens";
+    REQUIRE(num_tokens >= 0, "%s: num_tokens %d is negative", who, num_tokens);
+    REQUIRE(num_experts >= 1, "%s: num_experts %d < 1", who, num_experts);
+    REQUIRE(top_k >= 1 && top_k <= num_experts, "%s: top_k %d not in [1, num_experts=%d]", who, top_k, num_experts);
+    if (num_tokens > moe::kFewTokens)
+        return fail(MOE_EUNSUPPORTED, "%s: num_tokens=%d > %d", who, num_tokens, moe::kFewTokens);
+    if (num_experts > 256) return fail(MOE_EUNSUPPORTED, "%s: num_experts=%d > 256", who, num_experts);
+    if (top_k > moe::kFewTopK) return fail(MOE_EUNSUPPORTED, "%s: top_k=%d > %d", who, top_k, moe::kFewTopK);
+    REQUIRE(w_gate && w_up && w_down, "%s: w_gate, w_up and w_down are required", who);
+    const int type = w_gate->type;
+    REQUIRE(type >= MOE_W_BF16 && type <= MOE_W_FP8_BLOCK, "%s: unknown weight type %d", who, type);
+    REQUIRE(w_up->type == type && w_down->type == type, "%s: the weights have different types", who);
+    int step = type == MOE_W_BF16 ? 8 : 16, group = 0;
+    double bytes = type == MOE_W_BF16 ? 2 : 1;  // per value
+    if (type == MOE_W_INT4_GPTQ) {
+        group = w_gate->group_size;
+        REQUIRE(group == 32 || group == 64 || group == 128 || group == 256,
+                "%s: group_size %d not in {32,64,128,256}", who, group);
+        REQUIRE(w_up->group_size == group && w_down->group_size == group, "%s: the group sizes differ", who);
+        step = group > 64 ? group : 64;
+        bytes = 0.5;
+    }
+    REQUIRE(hidden >= step && hidden % step == 0, "%s: hidden %d must be a positive multiple of %d", who, hidden, step);
+    REQUIRE(inter >= step && inter % step == 0, "%s: inter %d must be a positive multiple of %d", who, inter, step);
+    if (hidden > moe::kFewMaxHidden)
+        return fail(MOE_EUNSUPPORTED, "%s: hidden=%d > %d", who, hidden, moe::kFewMaxHidden);
+    // the kernels address each expert's matrix and h with 31-bit byte offsets
+    const double cells = static_cast<double>(hidden) * inter;
+    if (cells * bytes >= 2147483648.0 || static_cast<double>(num_tokens) * top_k * inter * 2 >= 2147483648.0)
+        return fail(MOE_EUNSUPPORTED, "%s: an expert matrix (%d x %d) or the activations exceed 2 GiB", who, inter,
+                    hidden);
+    if (num_tokens == 0) return ok();
+    const moe::FewLayout l = moe::few_layout(num_tokens, num_experts, top_k, hidden, inter, type == MOE_W_INT4_GPTQ);
+    REQUIRE_PTR(who, workspace);
+    REQUIRE(workspace_bytes >= l.bytes, "%s: workspace_bytes %lld < required %lld", who,
+            static_cast<long long>(workspace_bytes), static_cast<long long>(l.bytes));
+    REQUIRE_PTR(who, logits);
+    REQUIRE_PTR(who, x);
+    REQUIRE_PTR(who, topk_ids);
+    REQUIRE_PTR(who, topk_w);
+    REQUIRE_PTR(who, out);
+    moe::FewArgs a{};
+    const moe_weight* w[3] = {w_gate, w_up, w_down};
+    moe::FewWeight* f[3] = {&a.gate, &a.up, &a.down};
+    for (int i = 0; i < 3; ++i) {
+        REQUIRE_PTR(who, w[i]->data);
+        if (type != MOE_W_BF16) REQUIRE_PTR(who, w[i]->scales);
+        if (type == MOE_W_INT4_GPTQ) REQUIRE_PTR(who, w[i]->qzeros);
+        *f[i] = {w[i]->data, w[i]->scales, w[i]->qzeros};
+    }
+    a.logits = logits;
+    a.x = x;
+    a.ids = topk_ids;
+    a.w = topk_w;
+    a.out = out;
+    char* ws = static_cast<char*>(workspace);
+    a.cnt = reinterpret_cast<int32_t*>(ws);
+    a.part = reinterpret_cast<float*>(ws + l.part_at);
+    a.hs = reinterpret_cast<uint16_t*>(ws + l.hs_at);
+    a.T = num_tokens;
+    a.E = num_experts;
+    a.top_k = top_k;
+    a.H = hidden;
+    a.I = inter;
+    a.renorm = renormalize ? 1 : 0;
+    a.splits = l.splits;
+    a.group = group;
+    return launched(who, moe::launch_few_tokens(type, a, static_cast<hipStream_t>(stream)));
 }
 
 // ------------------------------------------------------------------ ceiling probes (moe_probes.h)

@@ -1,25 +1,48 @@
 """PyTorch-facing binding of the serving operators (``include/serving/moe_serving.h``): the norm in
-front of the layer and block-scaled E4M3 quantisation.
+front of the layer, block-scaled E4M3 quantisation, and the whole layer for a few tokens.
 
 As in ``ops``: argument checks and marshalling only; every step runs in the HIP library on the
 tensors' device and its current stream.
 """
 from __future__ import annotations
 
-from typing import Optional
+import ctypes
+from dataclasses import dataclass
+from typing import Optional, Tuple
 
 import torch
 
-from ._lib import check, lib
-from .ops import Routing, _dev, _need, _numel_at_least
+from ._lib import MOE_W_FP8_BLOCK, MoeWeight, check, lib
+from .ops import Fp8Weight, GptqWeight, Routing, _dev, _need, _numel_at_least
 
-__all__ = ["FP8_BLOCK", "moe_rmsnorm", "moe_quantize_fp8_block"]
+__all__ = ["FP8_BLOCK", "FEW_TOKENS", "Fp8BlockWeight", "FewTokensPlan", "moe_rmsnorm", "moe_quantize_fp8_block",
+           "few_tokens_plan", "moe_few_tokens"]
 
 FP8_BLOCK = 128   # columns under one scale (weights: 128 x 128 blocks)
+FEW_TOKENS = 32   # most tokens of moe_few_tokens
 
 
 def _blocks(n: int) -> int:
     return -(-n // FP8_BLOCK)
+
+
+@dataclass
+class Fp8BlockWeight:
+    """FP8 E4M3 expert weights with one fp32 scale per 128 x 128 block: codes ``[E, N, K]`` uint8,
+    scales ``[E, ceil(N/128), ceil(K/128)]``."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    @property
+    def shape(self) -> Tuple[int, int, int]:
+        return tuple(self.codes.shape)
+
+    def struct(self) -> MoeWeight:
+        E, N, K = self.codes.shape
+        _need(tuple(self.scales.shape) == (E, _blocks(N), _blocks(K)),
+              f"scales is {tuple(self.scales.shape)}; needs {(E, _blocks(N), _blocks(K))}")
+        return MoeWeight(MOE_W_FP8_BLOCK, 0, _dev(self.codes, torch.uint8, "codes"),
+                         _dev(self.scales, torch.float32, "scales"), None)
 
 
 def _launch(name: str, device: torch.device, *args) -> None:
@@ -92,3 +115,96 @@ def moe_quantize_fp8_block(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor
             _ptr(routing.sorted_ids, torch.int32, "sorted_ids", x) if routing is not None else None,
             routing.num_pairs if routing is not None else 0, _ptr(q, torch.uint8, "q", x),
             _ptr(scale, torch.float32, "scale", x))
+
+
+# ----------------------------------------------------------------------------- the layer for a few tokens
+@dataclass
+class FewTokensPlan:
+    """What ``moe_few_tokens`` keeps between calls: the checked weights and the workspace (calls on one
+    plan must not overlap: one plan per stream that runs the layer)."""
+    gate: object
+    up: object
+    down: object
+    E: int
+    H: int
+    I: int
+    top_k: int
+    max_tokens: int
+    renormalize: bool
+    workspace: torch.Tensor
+    structs: Tuple[MoeWeight, MoeWeight, MoeWeight]
+
+    @property
+    def device(self) -> torch.device:
+        return self.workspace.device
+
+
+def _weight_tensors(w):
+    return [t for t in vars(w).values() if isinstance(t, torch.Tensor)]
+
+
+def _check_weight(w, who: str) -> None:
+    """The scales' shapes (the kernels read them by the matrix sizes)."""
+    E, N, K = w.shape
+    if isinstance(w, GptqWeight):
+        G = int(w.group_size)
+        _need(G > 0 and K % G == 0 and N % 8 == 0, f"{who}: K={K} is not a multiple of group_size {G}, or N={N} of 8")
+        want = {"scales": (E, K // G, N), "qzeros": (E, K // G, N // 8)}
+    elif isinstance(w, Fp8Weight):
+        want = {"scales": (E, N)}
+    else:
+        want = {}
+    for name, shape in want.items():
+        _need(tuple(getattr(w, name).shape) == shape, f"{who}: {name} is {tuple(getattr(w, name).shape)}; needs {shape}")
+
+
+def few_tokens_plan(gate, up, down, top_k: int, max_tokens: int = FEW_TOKENS,
+                    renormalize: bool = True) -> FewTokensPlan:
+    """Check the expert weights of a layer (gate and up ``[E, I, H]``, down ``[E, H, I]``; all bf16, GPTQ
+    int4, fp8 with channel scales or fp8 with block scales) once and make the workspace for calls of up
+    to ``max_tokens`` tokens."""
+    who = "few_tokens_plan"
+    E, I, H = gate.shape
+    _need(type(gate) is type(up) is type(down), f"{who}: gate, up and down must have one type")
+    _need(tuple(up.shape) == (E, I, H) and tuple(down.shape) == (E, H, I),
+          f"{who}: gate is {(E, I, H)}, up {tuple(up.shape)}, down {tuple(down.shape)}")
+    _need(0 <= max_tokens <= FEW_TOKENS, f"{who}: max_tokens {max_tokens} not in [0, {FEW_TOKENS}]")
+    for w in (gate, up, down):
+        _check_weight(w, who)
+    structs = tuple(w.struct() for w in (gate, up, down))
+    device = _weight_tensors(gate)[0].device
+    _need(all(t.device == device for w in (gate, up, down) for t in _weight_tensors(w)),
+          f"{who}: the weights are on more than one device")
+    n = int(lib().moe_few_tokens_workspace_bytes(max_tokens, E, top_k, H, I, structs[0].type))
+    _need(n >= 0, f"{who}: unsupported sizes (E={E}, top_k={top_k}, hidden={H}, inter={I})")
+    return FewTokensPlan(gate, up, down, E, H, I, top_k, max_tokens, bool(renormalize),
+                         torch.zeros(n, dtype=torch.uint8, device=device), structs)
+
+
+def moe_few_tokens(plan: FewTokensPlan, logits: torch.Tensor, x: torch.Tensor,
+                   topk_ids: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None,
+                   out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """The whole routed layer for ``x`` [T, H] bf16 and router ``logits`` [T, E] fp32, T <= the plan's
+    ``max_tokens``, in two launches.  Returns (out [T, H] bf16, topk_ids [T, k] int32, topk_w [T, k]
+    fp32).  Activations stay bf16 whatever the weights' type."""
+    who = "moe_few_tokens"
+    _need(x.dim() == 2 and x.shape[1] == plan.H, f"{who}: x is {tuple(x.shape)}; its width must be {plan.H}")
+    T, k = x.shape[0], plan.top_k
+    _need(T <= plan.max_tokens, f"{who}: {T} tokens; the plan holds {plan.max_tokens}")
+    _need(tuple(logits.shape) == (T, plan.E), f"{who}: logits is {tuple(logits.shape)}; needs {(T, plan.E)}")
+    _need(x.device == plan.device, f"{who}: x is on {x.device}, the plan on {plan.device}")
+    if out is None:
+        out = torch.empty_like(x)
+    if topk_ids is None:
+        topk_ids = torch.empty((T, k), dtype=torch.int32, device=x.device)
+    if topk_w is None:
+        topk_w = torch.empty((T, k), dtype=torch.float32, device=x.device)
+    _need(out.shape == x.shape, f"{who}: out is {tuple(out.shape)}; needs {tuple(x.shape)}")
+    _numel_at_least(topk_ids, T * k, f"{who}: topk_ids")
+    _numel_at_least(topk_w, T * k, f"{who}: topk_w")
+    g, u, d = plan.structs
+    _launch(who, x.device, _ptr(logits, torch.float32, "logits", x), _dev(x, torch.bfloat16, "x"), ctypes.byref(g),
+            ctypes.byref(u), ctypes.byref(d), T, plan.E, k, plan.H, plan.I, int(plan.renormalize),
+            _ptr(topk_ids, torch.int32, "topk_ids", x), _ptr(topk_w, torch.float32, "topk_w", x),
+            _ptr(out, torch.bfloat16, "out", x), plan.workspace.data_ptr(), plan.workspace.numel())
+    return out, topk_ids, topk_w

@@ -8,9 +8,10 @@ from __future__ import annotations
 
 import numpy as np
 
-from .moe_oracle import bf16_bits_to_f64, e4m3_round, round_bf16
+from .moe_oracle import bf16_bits_to_f64, e4m3_round, e4m3_to_f64, round_bf16, route, silu
 
-__all__ = ["rmsnorm", "block_amax", "quantize_blocks_fp8", "spread_blocks", "FP8_BLOCK"]
+__all__ = ["rmsnorm", "block_amax", "quantize_blocks_fp8", "spread_blocks", "FP8_BLOCK",
+           "fp8_block_matrix", "few_tokens"]
 
 FP8_BLOCK = 128
 _FLOOR = np.float32(2.0 ** -100)
@@ -49,3 +50,35 @@ def quantize_blocks_fp8(x: np.ndarray):
     scale = np.where(amax > 0, a / np.float32(448.0), one).astype(np.float32)
     factor = np.where(amax > 0, np.float32(448.0) / a, one).astype(np.float32)
     return e4m3_round((xf * spread_blocks(factor, xf.shape[1])).astype(np.float32)), scale
+
+
+def fp8_block_matrix(w, e: int) -> np.ndarray:
+    """Expert e's [N, K] matrix: value(code) * scale of its 128 x 128 block."""
+    v = e4m3_to_f64(w["codes"][e])
+    rows = np.repeat(np.asarray(w["scales"][e], np.float64), FP8_BLOCK, axis=0)[: v.shape[0]]
+    return v * spread_blocks(rows, v.shape[1])
+
+
+def few_tokens(logits: np.ndarray, x_bits: np.ndarray, gate, up, down, top_k: int, renormalize: bool = True):
+    """The routed layer without rounding in between.  gate, up, down: expert id -> [N, K] fp64 matrix.
+
+    Returns (out, ids, w, spread, noise): ``spread[t, n] = sum_j w_j sum_k |h_k| |Wd[n, k]|``, what a relative
+    error of h can move out by at most, and ``noise[t, n]``, what one unit of relative fp32 error in the
+    products of the first stage can move it by: h = silu(g) u with |silu'| <= 1.1, so
+    |dh| <= 1.1 |u| sum |x||Wg| + |silu(g)| sum |x||Wu|."""
+    x = bf16_bits_to_f64(x_bits)
+    ids, w = route(logits, top_k, renormalize)
+    H = x.shape[1]
+    out, spread, noise = (np.zeros((x.shape[0], H)) for _ in range(3))
+    mats = {int(e): (gate(int(e)), up(int(e)), down(int(e))) for e in np.unique(ids)}
+    for t in range(x.shape[0]):
+        for j in range(top_k):
+            wg, wu, wd = mats[int(ids[t, j])]
+            g, u = wg @ x[t], wu @ x[t]
+            h = silu(g) * u
+            dh = 1.1 * np.abs(u) * (np.abs(wg) @ np.abs(x[t])) + np.abs(silu(g)) * (np.abs(wu) @ np.abs(x[t]))
+            wt = float(w[t, j])
+            out[t] += wt * (wd @ h)
+            spread[t] += wt * (np.abs(wd) @ np.abs(h))
+            noise[t] += wt * (np.abs(wd) @ dh)
+    return out, ids, w, spread, noise

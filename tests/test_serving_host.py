@@ -160,3 +160,87 @@ def test_oracle_block_quantisation_floor():
     x[0, 0] = 2.0 ** -120
     q, s = oracle.quantize_blocks_fp8(x)
     assert s[0, 0] == np.float32(2.0 ** -100) / np.float32(448) and not (q & 0x7F).any()
+
+
+# ------------------------------------------------------------------------ the layer for a few tokens
+def mw(type_=0, group=0, data=FAKE, scales=FAKE, qzeros=FAKE):
+    from mixture_experts_routed_route_amd._lib import MoeWeight
+    return MoeWeight(type_, group, data, scales, qzeros)
+
+
+def few(L, g=None, u=None, d=None, T=4, E=8, k=2, H=256, I=128, logits=FAKE, x=FAKE, ids=FAKE, w=FAKE, out=FAKE,
+        ws=FAKE, nbytes=1 << 40):
+    g, u, d = g or mw(), u or mw(), d or mw()
+    return _rc(L, "moe_few_tokens", logits, x, ctypes.byref(g), ctypes.byref(u), ctypes.byref(d), T, E, k, H, I, 1,
+               ids, w, out, ws, nbytes, None)
+
+
+def test_few_tokens_refusals(L):
+    assert few(L, T=0)[0] == 0      # nothing to do, nothing enqueued
+    for kw, code, word in [
+            (dict(T=-1), -1, "num_tokens"), (dict(T=33), -2, "33"), (dict(E=0), -1, "num_experts"),
+            (dict(E=257, k=2), -2, "256"), (dict(k=0), -1, "top_k"), (dict(k=9), -1, "top_k"), (dict(E=64, k=33), -2, "32"),
+            (dict(H=252), -1, "hidden"), (dict(I=4), -1, "inter"), (dict(H=65544), -2, "65536"),
+            (dict(H=32768, I=32768), -2, "2 GiB"), (dict(g=mw(1, 128)), -1, "different types"),
+            (dict(g=mw(9), u=mw(9), d=mw(9)), -1, "type 9"),
+            (dict(g=mw(1, 48), u=mw(1, 48), d=mw(1, 48)), -1, "group_size 48"),
+            (dict(g=mw(1, 64), u=mw(1, 128), d=mw(1, 64)), -1, "group sizes"),
+            (dict(g=mw(1, 256), u=mw(1, 256), d=mw(1, 256), I=128), -1, "inter"),
+            (dict(g=mw(2), u=mw(2), d=mw(2), H=264), -1, "hidden"),
+            (dict(nbytes=100), -1, "workspace_bytes"), (dict(ws=None), -1, "workspace is NULL"), (dict(ws=OFF), -1, "aligned"),
+            (dict(x=None), -1, "x is NULL"), (dict(logits=OFF), -1, "aligned"), (dict(out=None), -1, "out is NULL"),
+            (dict(ids=None), -1, "topk_ids"), (dict(w=OFF), -1, "topk_w"), (dict(d=mw(data=None)), -1, "data is NULL"),
+            (dict(g=mw(3, scales=None), u=mw(3), d=mw(3)), -1, "scales is NULL"),
+            (dict(g=mw(1, 64, qzeros=None), u=mw(1, 64), d=mw(1, 64)), -1, "qzeros is NULL")]:
+        rc, msg = few(L, **kw)
+        assert rc == code and word in msg, (kw, rc, msg)
+
+
+def test_few_tokens_workspace_size_covers_fewer_tokens(L):
+    f = L.moe_few_tokens_workspace_bytes
+    for E, k, H, I, t in [(64, 6, 2048, 1408, 1), (8, 2, 4096, 14336, 0), (256, 8, 8, 8, 0), (4, 4, 65536, 64, 3)]:
+        sizes = [f(T, E, k, H, I, t) for T in range(33)]
+        assert sizes[0] > 0 and all(a <= b for a, b in zip(sizes, sizes[1:]))
+        assert sizes[32] >= 32 * k * I * 2
+    for bad in [(33, 8, 2, 64, 64, 0), (1, 257, 2, 64, 64, 0), (1, 8, 9, 64, 64, 0), (1, 8, 2, 65544, 64, 0),
+                (1, 8, 2, 64, 64, 4), (-1, 8, 2, 64, 64, 0)]:
+        assert f(*bad) == -1
+
+
+def test_few_tokens_plan_refuses_mismatched_weights(L):
+    def w(*s):
+        return m.Bf16Weight(bf(*s))
+
+    def f8(n, k, scales):
+        return m.Fp8BlockWeight(u8(4, n, k), torch.zeros(scales))
+    for args, word in [((w(4, 32, 64), w(4, 32, 64), w(4, 64, 40)), "down"),
+                       ((w(4, 32, 64), w(4, 40, 64), w(4, 64, 32)), "up"),
+                       ((w(4, 32, 64), f8(32, 64, (4, 1, 1)), w(4, 64, 32)), "one type"),
+                       ((f8(32, 64, (4, 1, 2)),) * 2 + (f8(64, 32, (4, 1, 1)),), "scales"),
+                       ((m.Fp8Weight(u8(4, 32, 64), torch.zeros(4, 31)),) * 2 + (m.Fp8Weight(u8(4, 64, 32), torch.zeros(4, 64)),), "scales")]:
+        with pytest.raises(ValueError, match=word):
+            m.few_tokens_plan(*args, 2)
+    q = m.GptqWeight(torch.zeros(4, 16, 64, dtype=torch.int32), torch.zeros(4, 2, 64, dtype=torch.float16),
+                     torch.zeros(4, 2, 7, dtype=torch.int32), 64)
+    with pytest.raises(ValueError, match="qzeros"):
+        m.few_tokens_plan(q, q, m.GptqWeight(torch.zeros(4, 8, 128, dtype=torch.int32), torch.zeros(4, 1, 128, dtype=torch.float16),
+                                             torch.zeros(4, 1, 16, dtype=torch.int32), 64), 2)
+    with pytest.raises(ValueError, match="max_tokens"):
+        m.few_tokens_plan(w(4, 32, 64), w(4, 32, 64), w(4, 64, 32), 2, 33)
+
+
+def test_oracle_few_tokens_matches_dense_layer():
+    """Against oracle.moe_layer (which sorts and combines) on the same inputs, and block scales of one
+    against unscaled codes."""
+    from moe_synth import MoeConfig, make_inputs
+    cfg = MoeConfig("t", T=6, H=64, I=40, E=5, top_k=2, block_size=16, seed=4)
+    d = make_inputs(cfg)
+    out, ids, w, spread, _ = oracle.few_tokens(d["logits"], d["x"], *[lambda e, k=k: oracle.expert_matrix(d[k], e) for k in ("wg", "wu", "wd")], 2)
+    ref = oracle.moe_layer(d)
+    assert np.array_equal(ids, ref["ids"]) and np.array_equal(w, ref["w"])
+    np.testing.assert_allclose(out, ref["out"], rtol=1e-11, atol=1e-13)
+    assert (spread >= np.abs(out) * (1 - 1e-12)).all()
+    codes = np.arange(256, dtype=np.uint8).reshape(1, 1, 256) & 0x77
+    one = {"codes": codes, "scales": np.array([[[1.0, 2.0]]], np.float32)}
+    v = oracle.e4m3_to_f64(codes[0])
+    assert np.array_equal(oracle.fp8_block_matrix(one, 0), np.concatenate([v[:, :128], 2 * v[:, 128:]], axis=1))
