@@ -4,6 +4,7 @@
  *   moe_rmsnorm             residual addition and root-mean-square norm in front of the layer, with
  *                           bf16 rows and/or E4M3 codes out
  *   moe_quantize_fp8_block  E4M3 codes of bf16 rows with one scale per 128 columns
+ *   moe_grouped_gemm_fp8_block  the grouped expert products on block-scaled E4M3 operands
  *   moe_few_tokens          the whole routed layer for at most 32 tokens, in two launches
  *
  * The conventions of moe_mi355x.h hold here as well: device pointers owned by the caller and 16-byte
@@ -56,6 +57,26 @@ moe_status moe_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16
  *   writes every row.  k % 16 == 0.  rows == 0 enqueues nothing. */
 moe_status moe_quantize_fp8_block(const uint16_t* x, int64_t rows, int32_t k, const int32_t* sorted_ids,
                                   int64_t num_pairs, uint8_t* q, float* scale, moe_stream stream);
+
+/* The grouped expert GEMMs on block-scaled E4M3 operands; arguments as for moe_grouped_gemm_fp8, except
+ *   a_scale   fp32 [rows of a, ceil(K/128)]: one scale per 128 k of a row (moe_rmsnorm or
+ *             moe_quantize_fp8_block outputs)
+ *   w0, w1    MOE_W_FP8_BLOCK weights (gate and up, or down)
+ *   acc[r, n] = sum over blocks b of a_scale[row, b] * scales[e, n/128, b] *
+ *               sum_{k in b} a(row, k) W(n, k)      (exact fp8 products, fp32 sums)
+ *   c         bf16 [max_pad, N]: silu(gate acc) * up acc (MOE_OP_GATE_UP_SILU) or acc (MOE_OP_DOWN); or NULL
+ *   q         uint8 [max_pad, N], q_scale fp32 [max_pad, ceil(N/128)], instead of c and with
+ *             MOE_OP_GATE_UP_SILU only: E4M3 codes of the unrounded silu(gate) * up with one scale per
+ *             128 columns, what MOE_OP_DOWN reads next (moe_quantize_fp8_block of c, without its
+ *             rounding to bf16 and without the launch)
+ * Exactly one of c and q.  Sentinel and padding rows are not written.  K % 16 == 0; N % 8 == 0, with q
+ * N % 16 == 0.  a (its rows: num_pairs/top_k for gate/up, max_pad for down) and each expert's matrix must
+ * each be under 4 GiB (else MOE_EUNSUPPORTED).  workspace: as for moe_grouped_gemm (the same buffer). */
+moe_status moe_grouped_gemm_fp8_block(int32_t op, const uint8_t* a, const float* a_scale, const moe_weight* w0,
+                                      const moe_weight* w1, uint16_t* c, uint8_t* q, float* q_scale,
+                                      const int32_t* sorted_ids, const int32_t* expert_offsets, int64_t num_pairs,
+                                      int32_t top_k, int32_t num_experts, int32_t n, int32_t k, int32_t block_size,
+                                      int64_t max_pad, void* workspace, int64_t workspace_bytes, moe_stream stream);
 
 /* The whole routed layer for a few tokens (moe_route, gate/up + SiLU, down and moe_combine), without
  * a sorted layout, in two launches:

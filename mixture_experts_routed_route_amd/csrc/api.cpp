@@ -745,6 +745,71 @@ moe_status moe_quantize_fp8_block(const uint16_t* x, int64_t rows, int32_t k, co
                                                         static_cast<hipStream_t>(stream)));
 }
 
+moe_status moe_grouped_gemm_fp8_block(int32_t op, const uint8_t* a, const float* a_scale, const moe_weight* w0,
+                                      const moe_weight* w1, uint16_t* c, uint8_t* q, float* q_scale,
+                                      const int32_t* sorted_ids, const int32_t* expert_offsets, int64_t num_pairs,
+                                      int32_t top_k, int32_t num_experts, int32_t n, int32_t k, int32_t block_size,
+                                      int64_t max_pad, void* workspace, int64_t workspace_bytes, moe_stream stream) {
+    const char* who = "moe_grouped_gemm_fp8_block";
+    REQUIRE(op == MOE_OP_GATE_UP_SILU || op == MOE_OP_DOWN, "%s: op %d not GATE_UP_SILU or DOWN", who, op);
+    const bool gate_up = op == MOE_OP_GATE_UP_SILU;
+    REQUIRE(num_pairs >= 0 && num_pairs < INT32_MAX, "%s: num_pairs out of range", who);
+    REQUIRE(top_k >= 1, "%s: top_k %d < 1", who, top_k);
+    REQUIRE(num_pairs % top_k == 0, "%s: num_pairs %lld is not a multiple of top_k %d", who,
+            static_cast<long long>(num_pairs), top_k);
+    REQUIRE(num_experts >= 1, "%s: num_experts %d < 1", who, num_experts);
+    if (num_experts > 256) return fail(MOE_EUNSUPPORTED, "%s: num_experts=%d > 256", who, num_experts);
+    REQUIRE(valid_block_size(block_size), "%s: block_size %d not in {16,32,64,128}", who, block_size);
+    REQUIRE((c != nullptr) != (q != nullptr), "%s: exactly one of c and q is needed", who);
+    REQUIRE((q == nullptr) == (q_scale == nullptr), "%s: q and q_scale go together", who);
+    REQUIRE(q == nullptr || gate_up, "%s: q is for GATE_UP_SILU", who);
+    const int step = q ? 16 : 8;
+    REQUIRE(n >= step && n % step == 0, "%s: n %d must be a positive multiple of %d", who, n, step);
+    REQUIRE(k >= 16 && k % 16 == 0, "%s: k %d must be a positive multiple of 16", who, k);
+    REQUIRE(max_pad >= max_padded(num_pairs, num_experts, block_size) && max_pad % block_size == 0 &&
+                max_pad < INT32_MAX,
+            "%s: max_pad %lld must be >= %lld and a multiple of block_size", who, static_cast<long long>(max_pad),
+            static_cast<long long>(max_padded(num_pairs, num_experts, block_size)));
+    REQUIRE(w0 != nullptr, "%s: w0 is NULL", who);
+    if (gate_up) REQUIRE(w1 != nullptr, "%s: MOE_OP_GATE_UP_SILU needs w1 (up)", who);
+    else REQUIRE(w1 == nullptr, "%s: op %d takes no w1", who, op);
+    REQUIRE(w0->type == MOE_W_FP8_BLOCK, "%s: w0 must be MOE_W_FP8_BLOCK (type %d)", who, w0->type);
+    if (w1) REQUIRE(w1->type == MOE_W_FP8_BLOCK, "%s: w1 must be MOE_W_FP8_BLOCK (type %d)", who, w1->type);
+    if (workspace != nullptr) {
+        const int64_t need = moe_grouped_gemm_workspace_bytes();
+        REQUIRE_PTR(who, workspace);
+        REQUIRE(workspace_bytes >= need, "%s: workspace_bytes %lld < required %lld", who,
+                static_cast<long long>(workspace_bytes), static_cast<long long>(need));
+    }
+    if (num_pairs == 0) return ok();
+    REQUIRE_PTR(who, a);
+    REQUIRE_PTR(who, a_scale);
+    if (c) REQUIRE_PTR(who, c);
+    if (q) {
+        REQUIRE_PTR(who, q);
+        REQUIRE_PTR(who, q_scale);
+    }
+    REQUIRE_PTR(who, sorted_ids);
+    REQUIRE_PTR(who, expert_offsets);
+    REQUIRE_PTR(who, w0->data);
+    REQUIRE_PTR(who, w0->scales);
+    if (w1) {
+        REQUIRE_PTR(who, w1->data);
+        REQUIRE_PTR(who, w1->scales);
+    }
+    // the kernel addresses a's rows and each expert matrix with 32-bit byte offsets
+    const int64_t a_rows = gate_up ? num_pairs / top_k : max_pad;
+    if (a_rows * k > INT64_C(0xffffffff) || static_cast<int64_t>(n) * k > INT64_C(0xffffffff))
+        return fail(MOE_EUNSUPPORTED, "%s: a (%lld rows) or an expert matrix (%d x %d) exceeds 4 GiB", who,
+                    static_cast<long long>(a_rows), n, k);
+    return launched(who, moe::launch_gemm_fp8_block(
+                             gate_up, a, a_scale, static_cast<const uint8_t*>(w0->data),
+                             static_cast<const float*>(w0->scales), w1 ? static_cast<const uint8_t*>(w1->data) : nullptr,
+                             w1 ? static_cast<const float*>(w1->scales) : nullptr, c, q, q_scale, sorted_ids,
+                             expert_offsets, static_cast<int>(num_pairs), top_k, num_experts, n, k,
+                             static_cast<int>(max_pad), workspace, workspace_bytes, static_cast<hipStream_t>(stream)));
+}
+
 int64_t moe_few_tokens_workspace_bytes(int32_t num_tokens, int32_t num_experts, int32_t top_k, int32_t hidden,
                                        int32_t inter, int32_t wtype) {
     if (num_tokens < 0 || num_tokens > moe::kFewTokens || num_experts < 1 || num_experts > 256 || top_k < 1 ||

@@ -31,6 +31,7 @@
 // Rows past N or T, k past K and tokens that are not the expert's are read through bounds-checked
 // buffer loads with an offset past the end: zeros, and no memory traffic.
 #include "few_tokens.h"
+#include "fp8_quant.h"
 #include "int4_dequant.h"
 #include "launchers.h"
 #include "route_common.h"
@@ -148,18 +149,6 @@ struct Panel {
     __amdgpu_buffer_rsrc_t abuf;
 };
 
-// two codes of a word as a bf16 pair (exact)
-__device__ __forceinline__ uint32_t fp8_pair(uint32_t w, bool hi) {
-    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-    const bf16x2_t v = hi ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true)
-                          : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false);
-    return __builtin_bit_cast(uint32_t, v);
-}
-
-__device__ __forceinline__ bf16x8 fp8_frag(uint32_t w0, uint32_t w1) {
-    return as_bf16x8(u32x4{fp8_pair(w0, false), fp8_pair(w0, true), fp8_pair(w1, false), fp8_pair(w1, true)});
-}
-
 // [E, N, K] weights, K contiguous.  A load instruction takes 16 bytes of 4 consecutive k chunks of 16
 // rows; U of them per column set are in flight before the first is used.
 template <int KIND, int CPL, int TF, int U>
@@ -214,8 +203,8 @@ __device__ __forceinline__ void panel_rows(const Panel& p, const int (&arow)[TF]
                 if constexpr (KIND == kBf16) {
                     w[0] = as_bf16x8(b[u][j]);
                 } else {
-                    w[0] = fp8_frag(b[u][j][0], b[u][j][1]);
-                    w[FR - 1] = fp8_frag(b[u][j][2], b[u][j][3]);
+                    w[0] = fp8_to_bf16(b[u][j][0], b[u][j][1]);
+                    w[FR - 1] = fp8_to_bf16(b[u][j][2], b[u][j][3]);
                 }
 #pragma unroll
                 for (int f = 0; f < TF; ++f) {

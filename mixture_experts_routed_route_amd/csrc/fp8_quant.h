@@ -44,6 +44,19 @@ __device__ __forceinline__ float row16_max(float v) {
     return fmaxf(v, ror(v, std::integral_constant<int, 8>{}));
 }
 
+// two codes of a word (its low or high half) as a pair of bf16 values; exact
+__device__ __forceinline__ uint32_t fp8_pair(uint32_t w, bool hi) {
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    const bf16x2_t v = hi ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true)
+                          : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false);
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+// eight codes as a bf16 MFMA operand
+__device__ __forceinline__ bf16x8 fp8_to_bf16(uint32_t w0, uint32_t w1) {
+    return __builtin_bit_cast(bf16x8, u32x4{fp8_pair(w0, false), fp8_pair(w0, true), fp8_pair(w1, false), fp8_pair(w1, true)});
+}
+
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 

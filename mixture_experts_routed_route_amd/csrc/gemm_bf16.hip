@@ -68,7 +68,7 @@
 // K stage through the last stage's LDS buffer; the other forms fetch the fragments from memory.
 #include <type_traits>
 
-#include "device_common.h"
+#include "fp8_quant.h"
 #include "launchers.h"
 
 namespace moe {
@@ -157,12 +157,108 @@ struct Fp8Scales {
     const float* w1;
 };
 
+// block-scaled fp8 form: one scale per 128 k of an activation row ([rows of A, ceil(K/128)]) and per
+// 128 x 128 block of a weight matrix ([E, ceil(N/128), ceil(K/128)]); with q, gate/up writes E4M3 codes
+// and their scales per 128 columns instead of bf16
+struct BlockScales {
+    const float* a;
+    const float* w0;
+    const float* w1;
+    uint8_t* q;   // [max_pad, N]
+    float* qs;    // [max_pad, ceil(N/128)]
+};
+
 // LORA: 0 no LoRA epilogue (gate/up, or with GATE_UP false the down projection); 1 one adapter (every
 // folded row is adapter 0; down: only at rank == BK, folded from LDS); 2 any adapters (the rows of one
 // fragment may belong to different adapters: one pass per adapter present; down: any rank).  The
 // one-adapter form is the common case and keeps the lean epilogue, which the loop of the general
 // form would cost registers in the main loop.
-template <bool GATE_UP, int BM, int BK, int STAGES, int NW, int LORA = 0, bool FP8 = false>
+// Epilogue of the block-scaled form, whose accumulators hold one token row per lane: value v of block
+// [i][j] is row wm * 64 + i * 32 + fr, column j * 32 + (v / 4) * 8 + fc * 4 + v % 4 of the wave's columns.
+// Four consecutive values are four adjacent columns; the two half waves swap quads, so that a lane ends
+// with eight adjacent columns of its row (16 bytes of bf16, 8 of codes): lane fc = 0 those of quads 0 and
+// 2 of a block (columns 0.. and 16..), fc = 1 those of 1 and 3.
+//
+// Codes (gate/up): the tile's 128 columns n0 .. are one block of 128 of h = SiLU(g) * u.  A
+// lane's maximum over its own columns, the other half wave's (one exchange) and the other column wave's
+// (through s_qm) give the row's scale, and h leaves as codes, never as bf16 rows.
+template <bool GATE_UP, bool CODES, int FI, int BM>
+__device__ __forceinline__ void store_rows(f32x16 (&acc)[FI][4], uint16_t* C, uint8_t* q, float* qs, const int* s_row,
+                                           float (*s_qm)[BM], int N, int n0, int r0, int wm, int wn, int lane) {
+    constexpr int NO = GATE_UP ? 2 : 4;  // output column blocks of this wave
+    const int fr = lane & 31, fc = lane >> 5;
+    const int c0 = n0 + wn * 32 * NO;
+    if constexpr (GATE_UP) {
+#pragma unroll
+        for (int i = 0; i < FI; ++i)
+#pragma unroll
+            for (int j = 0; j < NO; ++j)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[i][j][v] = silu_mul(acc[i][j][v], acc[i][j + 2][v]);
+    }
+    // eight adjacent columns from quads 2 p and 2 p + 1 of a block: the swap hands the lower half wave the
+    // other half's columns 4..7 of quad pair member 2 p, and the upper one columns 0..3 of member 2 p + 1
+    auto eight = [&](const f32x16& b, int p, float (&o)[8]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(b[8 * p + x]),
+                                                            __float_as_uint(b[8 * p + 4 + x]), false, false);
+            o[x] = __uint_as_float(r[0]);
+            o[4 + x] = __uint_as_float(r[1]);
+        }
+    };
+    float f[FI];
+    if constexpr (CODES) {
+#pragma unroll
+        for (int i = 0; i < FI; ++i) {
+            float top = 0.f;
+#pragma unroll
+            for (int j = 0; j < NO; ++j)
+#pragma unroll
+                for (int v = 0; v < 16; ++v)  // columns past N are no part of the block
+                    if (c0 + j * 32 + (v >> 2) * 8 + fc * 4 < N) top = fmaxf(top, fabsf(acc[i][j][v]));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            if (fc == 0) s_qm[wn][wm * 64 + i * 32 + fr] = top;
+        }
+        // orders LDS only (loads of the next tile stay in flight)
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+#pragma unroll
+        for (int i = 0; i < FI; ++i) {
+            const int rl = wm * 64 + i * 32 + fr;
+            const Fp8Scale sc = fp8_scale(fmaxf(s_qm[0][rl], s_qm[1][rl]));
+            f[i] = sc.factor;
+            if (wn == 0 && fc == 0 && s_row[rl] >= 0)
+                qs[static_cast<size_t>(r0 + rl) * ((N + kFp8Block - 1) / kFp8Block) + n0 / kFp8Block] = sc.scale;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < FI; ++i) {
+        const int rl = wm * 64 + i * 32 + fr;
+        const bool ok = s_row[rl] >= 0;
+        const size_t row = static_cast<size_t>(r0 + rl) * N;
+#pragma unroll
+        for (int j = 0; j < NO; ++j)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                float o[8];
+                eight(acc[i][j], p, o);
+                const int col = c0 + j * 32 + p * 16 + fc * 8;
+                if (!ok || col >= N) continue;
+                if constexpr (CODES)
+                    *reinterpret_cast<uint2*>(q + row + col) =
+                        make_uint2(fp8_codes4(o[0] * f[i], o[1] * f[i], o[2] * f[i], o[3] * f[i]),
+                                   fp8_codes4(o[4] * f[i], o[5] * f[i], o[6] * f[i], o[7] * f[i]));
+                else
+                    *reinterpret_cast<u32x4*>(C + row + col) = u32x4{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
+                                                                    pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7])};
+            }
+    }
+}
+
+// BLK (with FP8): the block-scaled form, 1 with bf16 out on the fp8 MFMA, 2 with codes out on the bf16 one.
+template <bool GATE_UP, int BM, int BK, int STAGES, int NW, int LORA = 0, bool FP8 = false, int BLK = 0>
 __global__ __launch_bounds__(64 * NW, 1) void gemm_bf16_kernel(const Elem<FP8>* __restrict__ A,
                                                           const Elem<FP8>* __restrict__ W0,
                                                           const Elem<FP8>* __restrict__ W1,
@@ -171,8 +267,10 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm_bf16_kernel(const Elem<FP8>* 
                                                           const int32_t* __restrict__ offsets, int P, int top_k,
                                                           int E, int N, int K, int max_pad, int n_tiles,
                                                           float* __restrict__ sk_part, int32_t* __restrict__ sk_cnt,
-                                                          int sk_on, int a_tok, GateUpLora lora, Fp8Scales f8) {
+                                                          int sk_on, int a_tok, GateUpLora lora,
+                                                          std::conditional_t<BLK != 0, BlockScales, Fp8Scales> f8) {
     static_assert(!(LORA && FP8), "no LoRA epilogue in the fp8 form");
+    static_assert(!BLK || (FP8 && BK == kFp8Block), "block scales: a stage is one block of k");
     using TE = Elem<FP8>;
     constexpr int ES = sizeof(TE);
     using F = Cfg<GATE_UP, BM, BK, STAGES, NW, ES>;
@@ -183,7 +281,9 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm_bf16_kernel(const Elem<FP8>* 
     __shared__ int s_lo[kMaxE], s_hi[kMaxE], s_tb[kMaxE + 1];  // expert span, first row tile
     __shared__ int s_row[2][BM];                                  // A source row per tile row
     __shared__ int s_rad[LORA ? 2 : 1][LORA ? BM : 1];            // LoRA: adapter id per tile row (-1: none)
-    __shared__ float s_as[FP8 ? 2 : 1][FP8 ? BM : 1];             // fp8: dequantisation scale per tile row
+    __shared__ float s_as[FP8 && !BLK ? 2 : 1][FP8 && !BLK ? BM : 1];  // fp8: dequantisation scale per tile row
+    __shared__ float s_sk[BLK ? STAGES : 1][BLK ? BM : 1];        // block scales: a stage's scale per tile row
+    __shared__ __attribute__((aligned(16))) float s_qm[BLK ? 2 : 1][BLK ? BM : 1];  // max |h| per row and column half
     __shared__ int s_h[2];                                        // rows up to the last token
     __shared__ int s_arrived;                                     // split tile: the other side's count
     __shared__ int s_pf[STAGES == 2 ? BM : 1];                    // next segment's sorted ids
@@ -291,7 +391,7 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm_bf16_kernel(const Elem<FP8>* 
                 }
             }
             s_row[buf][i] = src;
-            if constexpr (FP8) s_as[buf][i] = src >= 0 ? f8.a[src] : 0.f;
+            if constexpr (FP8 && !BLK) s_as[buf][i] = src >= 0 ? f8.a[src] : 0.f;
             if constexpr (LORA) {
                 // the token's adapter (atlas: a mixed batch's adapter comes from the per-row map); 0
                 // without a map; -1 for rows without a token or with an id outside [0, n_ad)
@@ -323,11 +423,20 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm_bf16_kernel(const Elem<FP8>* 
     Src a_o[NBLK][F::A_INST], b_o[NBLK][F::B_INST];
     const TE* b_base0 = W0;     // the tile's expert matrices (uniform)
     const TE* b_base1 = W1;
+    // block scales: blocks along K, and the first of this lane's activation row's (every issuing wave
+    // loads the scales of 64 tile rows; with more issuing waves than rows / 64, some of them twice)
+    const int kblocks = BLK ? (K + BK - 1) / BK : 0;
+    const int srow_w = (wave % (BM / 64)) * 64;
+    const float* sk_src = nullptr;
     auto block_wave = [&](int j) __attribute__((always_inline)) { return wave + j * (NW / 2); };
     auto set_sources = [&](int bf, int e_, int r0_, int n0_) __attribute__((always_inline)) {
         b_base0 = W0 + static_cast<size_t>(e_) * N * K;
         b_base1 = GATE_UP ? W1 + static_cast<size_t>(e_) * N * K : b_base0;
         if (!issuer) return;
+        if constexpr (BLK) {
+            const int src = s_row[bf][srow_w + lane];
+            sk_src = f8.a + static_cast<size_t>(src >= 0 ? src : ((GATE_UP || a_tok) ? 0 : r0_)) * kblocks;
+        }
 #pragma unroll
         for (int j = 0; j < NBLK; ++j) {
             const int bw = block_wave(j);
@@ -372,6 +481,8 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm_bf16_kernel(const Elem<FP8>* 
     auto issue_at = [&](int t, int kbase, int parts = 3) __attribute__((always_inline)) {  // 1: A rows, 2: B rows
         if (!issuer) return;
         const int k0 = (kbase + t) * BK;
+        if constexpr (BLK)
+            if (parts & 1) dma4(sk_src + kbase + t, lds_u32(s_sk[(sb + t) % STAGES]) + srow_w * 4);
         const uint32_t sbuf = static_cast<uint32_t>((sb + t) % STAGES) * (F::STAGE_ELEMS * ES);
         // B instruction q of block j: its 8 rows lie on one side of the gate/up boundary
         auto b_base = [&](int bw, int q) __attribute__((always_inline)) {
@@ -519,12 +630,13 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm_bf16_kernel(const Elem<FP8>* 
     // wave is past stage t-1, whose buffer is refilled with stage t+STAGES-1.
     auto ready = [&](int t) __attribute__((always_inline)) {
         const int ahead = min(STAGES - 2, nseg - 1 - t);
+        constexpr int LOADS = F::LOADS + (BLK ? 1 : 0);
         if constexpr (STAGES >= 4) {
-            if (ahead >= 2) wait_vmcnt<2 * F::LOADS>();
-            else if (ahead == 1) wait_vmcnt<F::LOADS>();
+            if (ahead >= 2) wait_vmcnt<2 * LOADS>();
+            else if (ahead == 1) wait_vmcnt<LOADS>();
             else wait_vmcnt<0>();
         } else if constexpr (STAGES == 3) {
-            if (ahead >= 1) wait_vmcnt<F::LOADS>();
+            if (ahead >= 1) wait_vmcnt<LOADS>();
             else wait_vmcnt<0>();
         } else {
             wait_vmcnt<0>();
@@ -562,7 +674,7 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm_bf16_kernel(const Elem<FP8>* 
                 if (src >= 0) atomicMax(&s_h[buf ^ 1], tid + 1);
                 // fp8: the rows' activation scales, straight into LDS as well (a row without a
                 // token takes row 0's, never used); the later stage waits cover the loads
-                if constexpr (FP8) dma4(f8.a + (src >= 0 ? src : 0), lds_u32(s_as[buf ^ 1]) + wave * 256);
+                if constexpr (FP8 && !BLK) dma4(f8.a + (src >= 0 ? src : 0), lds_u32(s_as[buf ^ 1]) + wave * 256);
                 // LoRA: the tokens' adapter ids, raw, straight into LDS (checked after the next
                 // barrier, below); without a map every row with a token is adapter 0
                 if constexpr (LORA) {
@@ -588,7 +700,74 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm_bf16_kernel(const Elem<FP8>* 
     // boundary, after the barrier), so queued MFMAs cover both LDS latency and barrier waits.
     // NF = A fragments of this wave that hold tokens; every wave still loads and meets the barriers.
     auto main_loop = [&](auto nf_c) __attribute__((always_inline)) {
-        if constexpr (NSET == 2) {
+        if constexpr (BLK) {
+            // Block scales: a stage is one block of 128 k, so each 32x32 block's product over the stage
+            // (from zero) enters the accumulator times sa[row] * sw, one multiply-add per value.  The
+            // MFMA operands are swapped (the weights as its rows, the tokens as its columns), so a lane
+            // holds one token row of the block and its factor is one register: no broadcast per value.
+            constexpr int NF = decltype(nf_c)::value;
+            const int nb = (n0 + (GATE_UP ? 0 : wn * BP / 2)) / kFp8Block;
+            const int nblocks = (N + kFp8Block - 1) / kFp8Block;
+            const size_t wblk = (static_cast<size_t>(e) * nblocks + min(nb, nblocks - 1)) * kblocks + kb;
+            const float* sw0p = uniform_ptr(f8.w0 + wblk);
+            const float* sw1p = GATE_UP ? uniform_ptr(f8.w1 + wblk) : nullptr;
+            for (int s = 0; s < nseg; ++s) {
+                const float sw0 = sw0p[s], sw1 = GATE_UP ? sw1p[s] : 0.f;
+                ready(s);
+                if (s == 0) pf_load();
+                else if (s == 1) pf_rows();
+                if (A_LATE && s + 1 < nseg) issue_at(s + 1, kb, 1);
+                if constexpr (NF > 0) {
+                    const TE* st = stage_ptr(s);
+                    const float* sk = s_sk[(sb + s) % STAGES] + wm * F::WM + fr;
+                    float f0[NF], f1[NF];
+#pragma unroll
+                    for (int i = 0; i < NF; ++i) {
+                        const float sa = sk[i * 32];
+                        f0[i] = sa * sw0;
+                        f1[i] = GATE_UP ? sa * sw1 : f0[i];
+                    }
+                    auto frag = [&](int off, int kk) __attribute__((always_inline)) {
+                        const int c0 = kk * 4 + fc * 2;
+                        const u32x4 lo = *reinterpret_cast<const u32x4*>(st + off + (c0 ^ fswz) * CE);
+                        const u32x4 hi = *reinterpret_cast<const u32x4*>(st + off + ((c0 + 1) ^ fswz) * CE);
+                        return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
+                                     (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+                    };
+                    i32x8 af[NF][2];
+#pragma unroll
+                    for (int i = 0; i < NF; ++i)
+#pragma unroll
+                        for (int kk = 0; kk < 2; ++kk) af[i][kk] = frag(a_off[i], kk);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const i32x8 b0 = frag(b_off[j], 0), b1 = frag(b_off[j], 1);
+#pragma unroll
+                        for (int i = 0; i < NF; ++i) {
+                            f32x16 d;
+#pragma unroll
+                            for (int v = 0; v < 16; ++v) d[v] = 0.f;
+                            if constexpr (BLK == 1) {
+                                d = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b0, af[i][0], d, 0, 0, 0, 127, 0, 127);
+                                d = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b1, af[i][1], d, 0, 0, 0, 127, 0, 127);
+                            } else {
+#pragma unroll
+                                for (int g = 0; g < 4; ++g)
+                                    d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fp8_to_bf16(b0[2 * g], b0[2 * g + 1]),
+                                                                                fp8_to_bf16(af[i][0][2 * g], af[i][0][2 * g + 1]), d, 0, 0, 0);
+#pragma unroll
+                                for (int g = 0; g < 4; ++g)
+                                    d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fp8_to_bf16(b1[2 * g], b1[2 * g + 1]),
+                                                                                fp8_to_bf16(af[i][1][2 * g], af[i][1][2 * g + 1]), d, 0, 0, 0);
+                            }
+                            const float f = GATE_UP && j >= 2 ? f1[i] : f0[i];
+#pragma unroll
+                            for (int v = 0; v < 16; ++v) acc[i][j][v] = fmaf(f, d[v], acc[i][j][v]);
+                        }
+                    }
+                }
+            }
+        } else if constexpr (NSET == 2) {
             ready(0);
             pf_load();
             read(nf_c, 0, 0, 0);
@@ -984,13 +1163,17 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm_bf16_kernel(const Elem<FP8>* 
         constexpr int NO = GATE_UP ? 2 : 4;  // output column blocks of this wave
         // fp8: the weight scales of this lane's accumulator column in each block (gate, up)
         float wsc[NO], wsu[NO];
-        if constexpr (FP8) {
+        if constexpr (FP8 && !BLK) {
 #pragma unroll
             for (int j = 0; j < NO; ++j) {
                 const int cj = min(n0 + (GATE_UP ? wn * 64 : wn * 128) + j * 32 + fr, N - 1);
                 wsc[j] = f8.w0[static_cast<size_t>(e) * N + cj];
                 if constexpr (GATE_UP) wsu[j] = f8.w1[static_cast<size_t>(e) * N + cj];
             }
+        }
+        if constexpr (BLK) {
+            if (store) store_rows<GATE_UP, BLK == 2, F::FI, BM>(acc, C, f8.q, f8.qs, s_row[buf], s_qm, N, n0, r0, wm, wn, lane);
+            store = false;
         }
         if (store)
 #pragma unroll
@@ -1002,15 +1185,15 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm_bf16_kernel(const Elem<FP8>* 
                 const bool ok = s_row[buf][row_l] >= 0;
                 uint16_t* crow = C + static_cast<size_t>(r0 + row_l) * N;
                 float sa0 = 1.f, sa1 = 1.f;  // fp8: the rows' activation scales
-                if constexpr (FP8) { sa0 = s_as[buf][rl]; sa1 = s_as[buf][rl + 1]; }
+                if constexpr (FP8 && !BLK) { sa0 = s_as[buf][rl]; sa1 = s_as[buf][rl + 1]; }
 #pragma unroll
                 for (int j = 0; j < NO; ++j) {
                     float h0, h1;  // values v (row rl) and v+1 (row rl+1) of this lane's column
                     float g0 = acc[i][j][v], g1 = acc[i][j][v + 1];
-                    if constexpr (FP8) { g0 = g0 * sa0 * wsc[j]; g1 = g1 * sa1 * wsc[j]; }
+                    if constexpr (FP8 && !BLK) { g0 = g0 * sa0 * wsc[j]; g1 = g1 * sa1 * wsc[j]; }
                     if constexpr (GATE_UP) {
                         float u0 = acc[i][j + 2][v], u1 = acc[i][j + 2][v + 1];
-                        if constexpr (FP8) { u0 = u0 * sa0 * wsu[j]; u1 = u1 * sa1 * wsu[j]; }
+                        if constexpr (FP8 && !BLK) { u0 = u0 * sa0 * wsu[j]; u1 = u1 * sa1 * wsu[j]; }
                         h0 = silu_mul(g0, u0);
                         h1 = silu_mul(g1, u1);
                     } else {
@@ -1058,11 +1241,12 @@ constexpr int64_t kSkPartBytes = 512LL * 2 * 64 * 4;    // largest partial: 512 
 constexpr int64_t kSkWorkspaceBytes = kSkCounterBytes + kSkMaxGrid * kSkPartBytes;
 static_assert(kSkMaxGrid * 4 <= kSkCounterBytes, "split-tail counters overflow their area");
 
-template <bool GATE_UP, int BM, int BK, int STAGES, int NW, int LORA = 0, bool FP8 = false>
+template <bool GATE_UP, int BM, int BK, int STAGES, int NW, int LORA = 0, bool FP8 = false, int BLK = 0>
 hipError_t launch_cfg(const Elem<FP8>* a, const Elem<FP8>* w0, const Elem<FP8>* w1, uint16_t* c,
                       const int32_t* sorted_ids, const int32_t* offsets, int P, int top_k, int E, int N, int K,
                       int max_pad, void* ws, int64_t ws_bytes, int a_tok, hipStream_t s,
-                      const GateUpLora& lora = GateUpLora{}, const Fp8Scales& f8 = Fp8Scales{}) {
+                      const GateUpLora& lora = GateUpLora{},
+                      const std::conditional_t<BLK != 0, BlockScales, Fp8Scales>& f8 = {}) {
     using F = Cfg<GATE_UP, BM, BK, STAGES, NW, sizeof(Elem<FP8>)>;
     static_assert(F::NT * F::FI * 64 * 4 <= kSkPartBytes, "partial accumulators larger than their workspace slot");
     const int n_tiles = (N + F::NCOL - 1) / F::NCOL;
@@ -1086,7 +1270,7 @@ hipError_t launch_cfg(const Elem<FP8>* a, const Elem<FP8>* w0, const Elem<FP8>* 
     }
     int32_t* cnt = sk ? static_cast<int32_t*>(ws) : nullptr;
     float* part = sk ? reinterpret_cast<float*>(static_cast<char*>(ws) + kSkCounterBytes) : nullptr;
-    gemm_bf16_kernel<GATE_UP, BM, BK, STAGES, NW, LORA, FP8><<<static_cast<int>(grid), F::NT, 0, s>>>(
+    gemm_bf16_kernel<GATE_UP, BM, BK, STAGES, NW, LORA, FP8, BLK><<<static_cast<int>(grid), F::NT, 0, s>>>(
         a, w0, w1, c, sorted_ids, offsets, P, top_k, E, N, K, max_pad, n_tiles, part, cnt, sk ? 1 : 0, a_tok, lora,
         f8);
     return hipGetLastError();
@@ -1142,6 +1326,24 @@ hipError_t launch_gemm_fp8(bool gate_up, const uint8_t* a, const float* a_scale,
     }
     if (big) return launch_cfg<false, 256, 128, 2, 8, 0, true>(a, w0, nullptr, c, sorted_ids, offsets, P, top_k, E, N, K, max_pad, ws, ws_bytes, 0, s, GateUpLora{}, f8);
     return launch_cfg<false, 128, 128, 3, 4, 0, true>(a, w0, nullptr, c, sorted_ids, offsets, P, top_k, E, N, K, max_pad, ws, ws_bytes, 0, s, GateUpLora{}, f8);
+}
+
+hipError_t launch_gemm_fp8_block(bool gate_up, const uint8_t* a, const float* a_scale, const uint8_t* w0,
+                                 const float* ws0, const uint8_t* w1, const float* ws1, uint16_t* c, uint8_t* q,
+                                 float* q_scale, const int32_t* sorted_ids, const int32_t* offsets, int P, int top_k,
+                                 int E, int N, int K, int max_pad, void* ws, int64_t ws_bytes, hipStream_t s) {
+    const BlockScales f8{a_scale, ws0, ws1, q, q_scale};
+    const bool big = static_cast<long long>(P) >= static_cast<long long>(MOE_GEMM_BIG_ROWS) * E;
+    if (q) {
+        if (big) return launch_cfg<true, 256, 128, 2, 8, 0, true, 2>(a, w0, w1, c, sorted_ids, offsets, P, top_k, E, N, K, max_pad, ws, ws_bytes, 1, s, GateUpLora{}, f8);
+        return launch_cfg<true, 128, 128, 3, 4, 0, true, 2>(a, w0, w1, c, sorted_ids, offsets, P, top_k, E, N, K, max_pad, ws, ws_bytes, 1, s, GateUpLora{}, f8);
+    }
+    if (gate_up) {
+        if (big) return launch_cfg<true, 256, 128, 2, 8, 0, true, 1>(a, w0, w1, c, sorted_ids, offsets, P, top_k, E, N, K, max_pad, ws, ws_bytes, 1, s, GateUpLora{}, f8);
+        return launch_cfg<true, 128, 128, 3, 4, 0, true, 1>(a, w0, w1, c, sorted_ids, offsets, P, top_k, E, N, K, max_pad, ws, ws_bytes, 1, s, GateUpLora{}, f8);
+    }
+    if (big) return launch_cfg<false, 256, 128, 2, 8, 0, true, 1>(a, w0, nullptr, c, sorted_ids, offsets, P, top_k, E, N, K, max_pad, ws, ws_bytes, 0, s, GateUpLora{}, f8);
+    return launch_cfg<false, 128, 128, 3, 4, 0, true, 1>(a, w0, nullptr, c, sorted_ids, offsets, P, top_k, E, N, K, max_pad, ws, ws_bytes, 0, s, GateUpLora{}, f8);
 }
 
 }  // namespace moe

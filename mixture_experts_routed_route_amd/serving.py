@@ -1,5 +1,6 @@
 """PyTorch-facing binding of the serving operators (``include/serving/moe_serving.h``): the norm in
-front of the layer, block-scaled E4M3 quantisation, and the whole layer for a few tokens.
+front of the layer, block-scaled E4M3 quantisation and grouped products, and the whole layer for a few
+tokens.
 
 As in ``ops``: argument checks and marshalling only; every step runs in the HIP library on the
 tensors' device and its current stream.
@@ -13,10 +14,10 @@ from typing import Optional, Tuple
 import torch
 
 from ._lib import MOE_W_FP8_BLOCK, MoeWeight, check, lib
-from .ops import Fp8Weight, GptqWeight, Routing, _dev, _need, _numel_at_least
+from .ops import Fp8Weight, GptqWeight, Routing, _check_gemm_shapes, _dev, _need, _numel_at_least
 
 __all__ = ["FP8_BLOCK", "FEW_TOKENS", "Fp8BlockWeight", "FewTokensPlan", "moe_rmsnorm", "moe_quantize_fp8_block",
-           "few_tokens_plan", "moe_few_tokens"]
+           "moe_grouped_gemm_fp8_block", "few_tokens_plan", "moe_few_tokens"]
 
 FP8_BLOCK = 128   # columns under one scale (weights: 128 x 128 blocks)
 FEW_TOKENS = 32   # most tokens of moe_few_tokens
@@ -115,6 +116,38 @@ def moe_quantize_fp8_block(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor
             _ptr(routing.sorted_ids, torch.int32, "sorted_ids", x) if routing is not None else None,
             routing.num_pairs if routing is not None else 0, _ptr(q, torch.uint8, "q", x),
             _ptr(scale, torch.float32, "scale", x))
+
+
+def moe_grouped_gemm_fp8_block(op: int, a: torch.Tensor, a_scale: torch.Tensor, w0: Fp8BlockWeight,
+                               w1: Optional[Fp8BlockWeight], routing: Routing, out: Optional[torch.Tensor] = None,
+                               q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                               workspace: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """op = MOE_OP_GATE_UP_SILU (a = x codes [T, K] by token) or MOE_OP_DOWN (a = Hs codes [max_pad, K]),
+    a_scale [rows, ceil(K/128)].  Returns ``out`` (bf16 [max_pad, N], allocated without one); with ``q``
+    (uint8 [max_pad, N]) and ``scale`` ([max_pad, ceil(N/128)]) the gate/up op writes E4M3 codes for the
+    down op instead, and returns None."""
+    who = "moe_grouped_gemm_fp8_block"
+    E, N, K = w0.shape
+    _need((q is None) == (scale is None), f"{who}: q and scale go together")
+    _need(q is None or out is None, f"{who}: out and q exclude each other")
+    mp = routing.max_pad
+    if q is None and out is None:
+        out = torch.empty((mp, N), dtype=torch.bfloat16, device=a.device)
+    _check_gemm_shapes(op, a, w0, w1, routing, out if q is None else q, who)
+    _need(a_scale.dim() == 2 and a_scale.shape[1] == _blocks(K) and a_scale.shape[0] >= a.shape[0],
+          f"{who}: a_scale is {tuple(a_scale.shape)}; needs [>= {a.shape[0]}, {_blocks(K)}]")
+    if scale is not None:
+        _need(scale.dim() == 2 and scale.shape[1] == _blocks(N) and scale.shape[0] >= mp,
+              f"{who}: scale is {tuple(scale.shape)}; needs [>= {mp}, {_blocks(N)}]")
+    s0 = w0.struct()
+    s1 = w1.struct() if w1 is not None else None
+    _launch(who, a.device, op, _dev(a, torch.uint8, "a"), _ptr(a_scale, torch.float32, "a_scale", a),
+            ctypes.byref(s0), ctypes.byref(s1) if s1 is not None else None, _ptr(out, torch.bfloat16, "out", a),
+            _ptr(q, torch.uint8, "q", a), _ptr(scale, torch.float32, "scale", a),
+            _ptr(routing.sorted_ids, torch.int32, "sorted_ids", a), _ptr(routing.offsets, torch.int32, "offsets", a),
+            routing.num_pairs, routing.top_k, routing.num_experts, N, K, routing.block_size, mp,
+            _ptr(workspace, torch.uint8, "workspace", a), workspace.numel() if workspace is not None else 0)
+    return out
 
 
 # ----------------------------------------------------------------------------- the layer for a few tokens

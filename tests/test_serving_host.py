@@ -244,3 +244,49 @@ def test_oracle_few_tokens_matches_dense_layer():
     one = {"codes": codes, "scales": np.array([[[1.0, 2.0]]], np.float32)}
     v = oracle.e4m3_to_f64(codes[0])
     assert np.array_equal(oracle.fp8_block_matrix(one, 0), np.concatenate([v[:, :128], 2 * v[:, 128:]], axis=1))
+
+
+# ----------------------------------------------------------------- grouped products with block scales
+def gemm(L, op=0, a=FAKE, sa=FAKE, w0=None, w1="same", c=FAKE, q=None, qs=None, ids=FAKE, off=FAKE, P=16, k_=2, E=4, n=128,
+         k=256, bs=16, mp=None, ws=None, wsb=0):
+    w0 = mw(3) if w0 is None else w0
+    w1 = w0 if w1 == "same" else w1
+    mp = -(-(P + E * (bs - 1)) // bs) * bs if mp is None else mp
+    return _rc(L, "moe_grouped_gemm_fp8_block", op, a, sa, ctypes.byref(w0), ctypes.byref(w1) if w1 is not None else None,
+               c, q, qs, ids, off, P, k_, E, n, k, bs, mp, ws, wsb, None)
+
+
+def test_gemm_fp8_block_refusals(L):
+    assert gemm(L, P=0, c=FAKE)[0] == 0   # no pairs: nothing enqueued
+    for kw, code, word in [
+            (dict(op=2), -1, "op 2"), (dict(c=None), -1, "exactly one"), (dict(q=FAKE, qs=FAKE), -1, "exactly one"),
+            (dict(c=None, q=FAKE), -1, "go together"), (dict(qs=FAKE), -1, "go together"),
+            (dict(op=1, w1=None, c=None, q=FAKE, qs=FAKE), -1, "GATE_UP_SILU"), (dict(op=1), -1, "no w1"), (dict(w1=None), -1, "needs w1"),
+            (dict(n=12), -1, "multiple of 8"), (dict(n=136, c=None, q=FAKE, qs=FAKE), -1, "multiple of 16"),
+            (dict(k=40), -1, "multiple of 16"), (dict(w0=mw(2)), -1, "MOE_W_FP8_BLOCK"), (dict(w1=mw(2)), -1, "MOE_W_FP8_BLOCK"),
+            (dict(E=257), -2, "256"), (dict(bs=48), -1, "block_size"), (dict(mp=16), -1, "max_pad"), (dict(P=15), -1, "multiple of top_k"),
+            (dict(n=65536, k=65536 + 16), -2, "4 GiB"), (dict(op=1, w1=None, P=2**26, k=128, n=8), -2, "4 GiB"),
+            (dict(ws=FAKE, wsb=8), -1, "workspace_bytes"), (dict(a=None), -1, "a is NULL"), (dict(sa=OFF), -1, "aligned"),
+            (dict(c=None, q=FAKE, qs=OFF), -1, "aligned"), (dict(ids=None), -1, "sorted_ids"), (dict(off=None), -1, "expert_offsets"),
+            (dict(w0=mw(3, scales=None)), -1, "scales is NULL")]:
+        rc, msg = gemm(L, **kw)
+        assert rc == code and word in msg, (kw, rc, msg)
+
+
+def test_gemm_fp8_block_binding_refuses_mismatched_buffers():
+    r = m.Routing.allocate(16, 2, 4, 16, "cpu")
+    w = m.Fp8BlockWeight(u8(4, 144, 272), torch.zeros(4, 2, 3))
+    sa = torch.zeros(8, 3)
+    for kw, word in [(dict(a_scale=torch.zeros(8, 2)), "a_scale"), (dict(a_scale=torch.zeros(7, 3)), "a_scale"),
+                     (dict(a=u8(7, 272)), "rows"), (dict(a=u8(8, 256)), "width must be K"),
+                     (dict(out=bf(r.max_pad - 1, 144)), "out is"), (dict(q=u8(r.max_pad, 144)), "go together"),
+                     (dict(q=u8(r.max_pad, 144), scale=torch.zeros(r.max_pad, 1)), "scale is"),
+                     (dict(q=u8(r.max_pad, 128), scale=torch.zeros(r.max_pad, 2)), "out is"),
+                     (dict(q=u8(r.max_pad, 144), scale=torch.zeros(r.max_pad, 2), out=bf(r.max_pad, 144)), "exclude"),
+                     (dict(w0=m.Fp8BlockWeight(u8(4, 144, 272), torch.zeros(4, 2, 2)), a_scale=sa), "scales is")]:
+        args = dict(op=0, a=u8(8, 272), a_scale=sa, w0=w, w1=w, routing=r)
+        args.update(kw)
+        if "w0" in kw:
+            args["w1"] = args["w0"]
+        with pytest.raises(ValueError, match=word):
+            m.moe_grouped_gemm_fp8_block(**args)
