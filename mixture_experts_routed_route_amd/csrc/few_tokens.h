@@ -8,11 +8,11 @@ namespace moe {
 
 constexpr int kFewTokens = 32;  // tokens: one bit each of an expert's mask
 constexpr int kFewTopK = 32;    // slots per token
-constexpr int kFewGrid = 512;   // workgroups of the first launch: two of eight waves per compute unit
-constexpr int kFewDownGrid = 512;  // workgroups the second launch aims at, by splitting the experts
+constexpr int kFewGrid = 256;   // workgroups of the first launch: one per compute unit
+constexpr int kFewDownGrid = 256;  // workgroups the second launch aims at, by splitting the experts
 constexpr int kFewMaxSplits = 16;
 constexpr int kFewMaxHidden = 65536;
-constexpr int kFewCounterBytes = kFewMaxHidden / 16 * 4;  // one counter per 16 output columns
+constexpr int kFewCounterBytes = kFewMaxHidden / 32 * 4;  // one counter per output panel (32 columns or more)
 
 struct FewWeight {
     const void* data;
@@ -43,7 +43,7 @@ struct FewLayout {
 
 inline FewLayout few_layout(int T, int E, int top_k, int H, int I, bool int4) {
     auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
-    const int ncol = int4 ? 64 : 16;
+    const int ncol = int4 ? 64 : 32;  // columns of a panel
     const int panels = (H + ncol - 1) / ncol;
     const int most = T * top_k < E ? T * top_k : E;
     int splits = (kFewDownGrid + panels - 1) / panels;

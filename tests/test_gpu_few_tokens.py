@@ -96,6 +96,9 @@ CASES = [
     # int4: every group size, one and two token fragments, few groups per wave
     *[C(f"int4_g{G}_T{T}", T, 512, 256, 8, 2, "int4_gptq", group_size=G, seed=G + T) for G in (32, 64, 128, 256) for T in (1, 19)],
     C("int4_one_unit", 3, 64, 64, 4, 2, "int4_gptq", group_size=64, seed=20), C("int4_mid", 16, 1024, 704, 16, 4, "int4_gptq", group_size=64, seed=21),
+    # rows of x that do not fit LDS beside the panel sums (and the widest that do)
+    *[C(f"{w}_x{H}_T{T}", T, H, 64, 4, 2, w, group_size=64, seed=H + T)
+      for w in ("bf16", "int4_gptq", "fp8_block") for T, H in ((16, 2688), (16, 4096), (8, 8192), (20, 1792), (32, 2048), (24, 4096))],
     # fp8: channel and block scales, widths that end inside a block
     *[C(f"{w}_T{T}", T, 384, 256, 8, 2, w, seed=T) for w in ("fp8", "fp8_block") for T in (1, 16, 23)],
     *[C(f"{w}_odd", 5, 400, 208, 6, 3, w, seed=30) for w in ("fp8", "fp8_block")],
