@@ -46,24 +46,38 @@ class Fp8BlockWeight:
                          _dev(self.scales, torch.float32, "scales"), None)
 
 
-def _launch(name: str, device: torch.device, *args) -> None:
-    """The call on ``device``'s current stream, with that device current (a launch goes to the
-    current device's code object, whatever device its stream belongs to)."""
+# the current stream's handle by device index: torch.cuda.current_stream builds a Stream object first, which
+# takes longer (1.9 us) than the rest of a call's marshalling
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(name: str, index: int, *args) -> None:
+    """The call on the current stream of device ``index``, with that device current (a launch goes to
+    the current device's code object, whatever device its stream belongs to)."""
     f = getattr(lib(), name)
-    if device.index is None or device.index == torch.cuda.current_device():
-        check(f(*args, torch.cuda.current_stream(device).cuda_stream))
+    if index == torch.cuda.current_device():
+        check(f(*args, _raw_stream(index)))
     else:
-        with torch.cuda.device(device):
-            check(f(*args, torch.cuda.current_stream(device).cuda_stream))
+        with torch.cuda.device(index):
+            check(f(*args, _raw_stream(index)))
 
 
-def _ptr(t: Optional[torch.Tensor], dtype: torch.dtype, name: str, like: torch.Tensor) -> Optional[int]:
-    """``t``'s address (None stays None), on the same device as ``like``."""
+def _ptr(t: Optional[torch.Tensor], dtype: torch.dtype, name: str, index: int) -> Optional[int]:
+    """``t``'s address (None stays None), a contiguous tensor on device ``index``."""
     if t is None:
         return None
-    p = _dev(t, dtype, name)
-    _need(t.device == like.device, f"{name} is on {t.device}, x on {like.device}")
-    return p
+    if t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    _dev(t, dtype, name)
+    raise ValueError(f"{name} is on {t.device}, the first argument on device {index}")
+
+
+def _index(t: torch.Tensor, dtype: torch.dtype, name: str) -> int:
+    """The device index of a call's leading tensor, checked."""
+    if not (t.is_cuda and t.dtype is dtype and t.is_contiguous()):
+        _dev(t, dtype, name)
+    return t.get_device()
 
 
 def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
@@ -78,26 +92,28 @@ def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residu
     [rows, ceil(k/128)]).  Returns ``y`` (None with codes only)."""
     who = "moe_rmsnorm"
     _need(x.dim() == 2, f"{who}: x is {tuple(x.shape)}; needs [rows, k]")
-    rows, k = x.shape
-    _need(weight.dim() == 1 and weight.shape[0] == k, f"{who}: weight is {tuple(weight.shape)}; needs ({k},)")
-    _need(residual is not None or residual_out is None, f"{who}: residual_out without residual")
-    if residual is not None and residual_out is None:
+    rows, k = shape = x.shape
+    _need(tuple(weight.shape) == (k,), f"{who}: weight is {tuple(weight.shape)}; needs ({k},)")
+    if residual is None:
+        _need(residual_out is None, f"{who}: residual_out without residual")
+    elif residual_out is None:
         residual_out = residual
     _need((q is None) == (scale is None), f"{who}: q and scale go together")
     if y is None and q is None:
         y = torch.empty_like(x)
     for t, name in ((residual, "residual"), (residual_out, "residual_out"), (y, "y"), (q, "q")):
-        _need(t is None or t.shape == x.shape, f"{who}: {name} is {tuple(t.shape) if t is not None else ()}; "
-                                               f"needs {(rows, k)}")
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{who}: {name} is {tuple(t.shape)}; needs {(rows, k)}")
     block = 0
     if scale is not None:
         block = FP8_BLOCK if scale.dim() == 2 else 0
         want = (rows, _blocks(k)) if block else (rows,)
         _need(tuple(scale.shape) == want, f"{who}: scale is {tuple(scale.shape)}; needs {(rows,)} or {(rows, _blocks(k))}")
     bf = torch.bfloat16
-    _launch(who, x.device, _dev(x, bf, "x"), _ptr(residual, bf, "residual", x), _ptr(weight, bf, "weight", x),
-            float(eps), rows, k, _ptr(residual_out, bf, "residual_out", x), _ptr(y, bf, "y", x),
-            _ptr(q, torch.uint8, "q", x), _ptr(scale, torch.float32, "scale", x), block)
+    i = _index(x, bf, "x")
+    _launch(who, i, x.data_ptr(), _ptr(residual, bf, "residual", i), _ptr(weight, bf, "weight", i),
+            eps, rows, k, _ptr(residual_out, bf, "residual_out", i), _ptr(y, bf, "y", i),
+            _ptr(q, torch.uint8, "q", i), _ptr(scale, torch.float32, "scale", i), block)
     return y
 
 
@@ -112,10 +128,11 @@ def moe_quantize_fp8_block(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor
     _need(tuple(scale.shape) == (rows, _blocks(k)), f"{who}: scale is {tuple(scale.shape)}; needs {(rows, _blocks(k))}")
     if routing is not None:
         _numel_at_least(routing.sorted_ids, rows, f"{who}: routing.sorted_ids")
-    _launch(who, x.device, _dev(x, torch.bfloat16, "x"), rows, k,
-            _ptr(routing.sorted_ids, torch.int32, "sorted_ids", x) if routing is not None else None,
-            routing.num_pairs if routing is not None else 0, _ptr(q, torch.uint8, "q", x),
-            _ptr(scale, torch.float32, "scale", x))
+    i = _index(x, torch.bfloat16, "x")
+    _launch(who, i, x.data_ptr(), rows, k,
+            _ptr(routing.sorted_ids, torch.int32, "sorted_ids", i) if routing is not None else None,
+            routing.num_pairs if routing is not None else 0, _ptr(q, torch.uint8, "q", i),
+            _ptr(scale, torch.float32, "scale", i))
 
 
 def moe_grouped_gemm_fp8_block(op: int, a: torch.Tensor, a_scale: torch.Tensor, w0: Fp8BlockWeight,
@@ -141,12 +158,13 @@ def moe_grouped_gemm_fp8_block(op: int, a: torch.Tensor, a_scale: torch.Tensor, 
               f"{who}: scale is {tuple(scale.shape)}; needs [>= {mp}, {_blocks(N)}]")
     s0 = w0.struct()
     s1 = w1.struct() if w1 is not None else None
-    _launch(who, a.device, op, _dev(a, torch.uint8, "a"), _ptr(a_scale, torch.float32, "a_scale", a),
-            ctypes.byref(s0), ctypes.byref(s1) if s1 is not None else None, _ptr(out, torch.bfloat16, "out", a),
-            _ptr(q, torch.uint8, "q", a), _ptr(scale, torch.float32, "scale", a),
-            _ptr(routing.sorted_ids, torch.int32, "sorted_ids", a), _ptr(routing.offsets, torch.int32, "offsets", a),
+    i = _index(a, torch.uint8, "a")
+    _launch(who, i, op, a.data_ptr(), _ptr(a_scale, torch.float32, "a_scale", i),
+            ctypes.byref(s0), ctypes.byref(s1) if s1 is not None else None, _ptr(out, torch.bfloat16, "out", i),
+            _ptr(q, torch.uint8, "q", i), _ptr(scale, torch.float32, "scale", i),
+            _ptr(routing.sorted_ids, torch.int32, "sorted_ids", i), _ptr(routing.offsets, torch.int32, "offsets", i),
             routing.num_pairs, routing.top_k, routing.num_experts, N, K, routing.block_size, mp,
-            _ptr(workspace, torch.uint8, "workspace", a), workspace.numel() if workspace is not None else 0)
+            _ptr(workspace, torch.uint8, "workspace", i), workspace.numel() if workspace is not None else 0)
     return out
 
 
@@ -166,6 +184,9 @@ class FewTokensPlan:
     renormalize: bool
     workspace: torch.Tensor
     structs: Tuple[MoeWeight, MoeWeight, MoeWeight]
+
+    def __post_init__(self):
+        self.refs = tuple(ctypes.byref(w) for w in self.structs)
 
     @property
     def device(self) -> torch.device:
@@ -221,23 +242,28 @@ def moe_few_tokens(plan: FewTokensPlan, logits: torch.Tensor, x: torch.Tensor,
     ``max_tokens``, in two launches.  Returns (out [T, H] bf16, topk_ids [T, k] int32, topk_w [T, k]
     fp32).  Activations stay bf16 whatever the weights' type."""
     who = "moe_few_tokens"
-    _need(x.dim() == 2 and x.shape[1] == plan.H, f"{who}: x is {tuple(x.shape)}; its width must be {plan.H}")
+    if x.dim() != 2 or x.shape[1] != plan.H:
+        raise ValueError(f"{who}: x is {tuple(x.shape)}; its width must be {plan.H}")
     T, k = x.shape[0], plan.top_k
-    _need(T <= plan.max_tokens, f"{who}: {T} tokens; the plan holds {plan.max_tokens}")
-    _need(tuple(logits.shape) == (T, plan.E), f"{who}: logits is {tuple(logits.shape)}; needs {(T, plan.E)}")
-    _need(x.device == plan.device, f"{who}: x is on {x.device}, the plan on {plan.device}")
+    if T > plan.max_tokens:
+        raise ValueError(f"{who}: {T} tokens; the plan holds {plan.max_tokens}")
+    if tuple(logits.shape) != (T, plan.E):
+        raise ValueError(f"{who}: logits is {tuple(logits.shape)}; needs {(T, plan.E)}")
+    i = _index(x, torch.bfloat16, "x")
+    if i != plan.workspace.get_device():
+        raise ValueError(f"{who}: x is on {x.device}, the plan on {plan.device}")
     if out is None:
         out = torch.empty_like(x)
     if topk_ids is None:
         topk_ids = torch.empty((T, k), dtype=torch.int32, device=x.device)
     if topk_w is None:
         topk_w = torch.empty((T, k), dtype=torch.float32, device=x.device)
-    _need(out.shape == x.shape, f"{who}: out is {tuple(out.shape)}; needs {tuple(x.shape)}")
-    _numel_at_least(topk_ids, T * k, f"{who}: topk_ids")
-    _numel_at_least(topk_w, T * k, f"{who}: topk_w")
-    g, u, d = plan.structs
-    _launch(who, x.device, _ptr(logits, torch.float32, "logits", x), _dev(x, torch.bfloat16, "x"), ctypes.byref(g),
-            ctypes.byref(u), ctypes.byref(d), T, plan.E, k, plan.H, plan.I, int(plan.renormalize),
-            _ptr(topk_ids, torch.int32, "topk_ids", x), _ptr(topk_w, torch.float32, "topk_w", x),
-            _ptr(out, torch.bfloat16, "out", x), plan.workspace.data_ptr(), plan.workspace.numel())
+    if out.shape != x.shape:
+        raise ValueError(f"{who}: out is {tuple(out.shape)}; needs {tuple(x.shape)}")
+    if topk_ids.numel() < T * k or topk_w.numel() < T * k:
+        raise ValueError(f"{who}: topk_ids and topk_w hold {topk_ids.numel()} and {topk_w.numel()}; need {T * k}")
+    g, u, d = plan.refs
+    _launch(who, i, _ptr(logits, torch.float32, "logits", i), x.data_ptr(), g, u, d, T, plan.E, k, plan.H, plan.I,
+            plan.renormalize, _ptr(topk_ids, torch.int32, "topk_ids", i), _ptr(topk_w, torch.float32, "topk_w", i),
+            _ptr(out, torch.bfloat16, "out", i), plan.workspace.data_ptr(), plan.workspace.numel())
     return out, topk_ids, topk_w
