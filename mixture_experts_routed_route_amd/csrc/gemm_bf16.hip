@@ -734,35 +734,56 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm_bf16_kernel(const Elem<FP8>* 
                         return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
                                      (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
                     };
-                    i32x8 af[NF][2];
+                    auto factor = [&](int i, int j) __attribute__((always_inline)) { return GATE_UP && j >= 2 ? f1[i] : f0[i]; };
+                    if constexpr (BLK == 1) {
+                        i32x8 af[NF][2];
 #pragma unroll
-                    for (int i = 0; i < NF; ++i)
+                        for (int i = 0; i < NF; ++i)
 #pragma unroll
-                        for (int kk = 0; kk < 2; ++kk) af[i][kk] = frag(a_off[i], kk);
+                            for (int kk = 0; kk < 2; ++kk) af[i][kk] = frag(a_off[i], kk);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const i32x8 b0 = frag(b_off[j], 0), b1 = frag(b_off[j], 1);
+                        for (int j = 0; j < 4; ++j) {
+                            const i32x8 b0 = frag(b_off[j], 0), b1 = frag(b_off[j], 1);
 #pragma unroll
-                        for (int i = 0; i < NF; ++i) {
-                            f32x16 d;
-#pragma unroll
-                            for (int v = 0; v < 16; ++v) d[v] = 0.f;
-                            if constexpr (BLK == 1) {
+                            for (int i = 0; i < NF; ++i) {
+                                f32x16 d = {};
                                 d = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b0, af[i][0], d, 0, 0, 0, 127, 0, 127);
                                 d = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b1, af[i][1], d, 0, 0, 0, 127, 0, 127);
-                            } else {
 #pragma unroll
-                                for (int g = 0; g < 4; ++g)
-                                    d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fp8_to_bf16(b0[2 * g], b0[2 * g + 1]),
-                                                                                fp8_to_bf16(af[i][0][2 * g], af[i][0][2 * g + 1]), d, 0, 0, 0);
-#pragma unroll
-                                for (int g = 0; g < 4; ++g)
-                                    d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fp8_to_bf16(b1[2 * g], b1[2 * g + 1]),
-                                                                                fp8_to_bf16(af[i][1][2 * g], af[i][1][2 * g + 1]), d, 0, 0, 0);
+                                for (int v = 0; v < 16; ++v) acc[i][j][v] = fmaf(factor(i, j), d[v], acc[i][j][v]);
                             }
-                            const float f = GATE_UP && j >= 2 ? f1[i] : f0[i];
+                        }
+                    } else {
+                        // bf16 MFMAs over the converted codes, half a stage (64 k) at a time: the token
+                        // operands, converted once for the four weight blocks, then take 32 registers (a
+                        // whole stage's spilled inside the loop, and a spill's reload waits for the loads of
+                        // the next stage: 475 against 400 us at 64 experts of 1408 x 4096 and 12288 rows)
 #pragma unroll
-                            for (int v = 0; v < 16; ++v) acc[i][j][v] = fmaf(f, d[v], acc[i][j][v]);
+                        for (int kk = 0; kk < 2; ++kk) {
+                            bf16x8 ac[NF][4];
+#pragma unroll
+                            for (int i = 0; i < NF; ++i) {
+                                const i32x8 r = frag(a_off[i], kk);
+#pragma unroll
+                                for (int g = 0; g < 4; ++g) ac[i][g] = fp8_to_bf16(r[2 * g], r[2 * g + 1]);
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const i32x8 r = frag(b_off[j], kk);
+                                f32x16 d[NF] = {};
+#pragma unroll
+                                for (int g = 0; g < 4; ++g) {
+                                    const bf16x8 w = fp8_to_bf16(r[2 * g], r[2 * g + 1]);
+#pragma unroll
+                                    for (int i = 0; i < NF; ++i)
+                                        d[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, ac[i][g], d[i], 0, 0, 0);
+                                }
+#pragma unroll
+                                for (int i = 0; i < NF; ++i)
+#pragma unroll
+                                    for (int v = 0; v < 16; ++v) acc[i][j][v] = fmaf(factor(i, j), d[i][v], acc[i][j][v]);
+                            }
+                            __builtin_amdgcn_sched_barrier(0);
                         }
                     }
                 }
