@@ -81,7 +81,7 @@ moe_status moe_grouped_gemm_fp8_block(int32_t op, const uint8_t* a, const float*
 /* The whole routed layer for a few tokens (moe_route, gate/up + SiLU, down and moe_combine), without
  * a sorted layout, in two launches:
  *   ids, w = moe_route(logits)                 bit for bit
- *   h[t,j] = bf16(silu(x[t] Wg[e]^T) * (x[t] Wu[e]^T)), e = ids[t,j], from fp32 sums
+ *   h[t,j] = silu(x[t] Wg[e]^T) * (x[t] Wu[e]^T), e = ids[t,j], to 16 bits, from fp32 sums
  *   out[t] = bf16(sum_j w[t,j] * (h[t,j] Wd[e]^T)), fp32, the expert outputs not rounded in between
  *   logits   fp32 [num_tokens, num_experts], finite
  *   x        bf16 [num_tokens, hidden]

@@ -851,7 +851,7 @@ moe_status moe_few_tokens(const float* logits, const uint16_t* x, const moe_weig
         return fail(MOE_EUNSUPPORTED, "%s: hidden=%d > %d", who, hidden, moe::kFewMaxHidden);
     // the kernels address each expert's matrix and h with 31-bit byte offsets
     const double cells = static_cast<double>(hidden) * inter;
-    if (cells * bytes >= 2147483648.0 || static_cast<double>(num_tokens) * top_k * inter * 2 >= 2147483648.0)
+    if (cells * bytes >= 2147483648.0 || static_cast<double>(num_tokens) * top_k * inter * 4 >= 2147483648.0)
         return fail(MOE_EUNSUPPORTED, "%s: an expert matrix (%d x %d) or the activations exceed 2 GiB", who, inter,
                     hidden);
     if (num_tokens == 0) return ok();

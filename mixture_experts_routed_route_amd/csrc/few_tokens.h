@@ -27,7 +27,7 @@ struct FewArgs {
     int32_t* ids;
     float* w;
     uint16_t* out;
-    uint16_t* hs;   // workspace: bf16 [T * top_k, I]
+    uint16_t* hs;   // workspace: bf16 [2, T * top_k, I], high and low parts
     float* part;    // workspace: partial output panels
     int32_t* cnt;   // workspace: one counter per output panel, zero between calls
     int T, E, top_k, H, I, renorm, splits, group;
@@ -54,7 +54,7 @@ inline FewLayout few_layout(int T, int E, int top_k, int H, int I, bool int4) {
     l.part_at = kFewCounterBytes;
     const int tf = T <= 16 ? 1 : 2;
     l.hs_at = l.part_at + up(l.splits > 1 ? static_cast<int64_t>(panels) * l.splits * tf * 16 * ncol * 4 : 0);
-    l.bytes = l.hs_at + up(static_cast<int64_t>(T) * top_k * I * 2);
+    l.bytes = l.hs_at + up(static_cast<int64_t>(T) * top_k * I * 4);
     return l;
 }
 

@@ -1,6 +1,6 @@
 // The whole routed layer for at most 32 tokens in two launches:
 //
-//   few_gate_up   top-k softmax routing, then h[p] = bf16(SiLU(x Wg^T) * (x Wu^T)) of every (token,
+//   few_gate_up   top-k softmax routing, then h[p] = SiLU(x Wg^T) * (x Wu^T) of every (token,
 //                 slot) pair p = t * top_k + j
 //   few_down      out[t] = bf16(sum_j w[t, j] * (h[p] Wd^T)), fp32 sums over k and over the experts
 //
@@ -24,8 +24,10 @@
 // panels meet in the workspace, the last workgroup to arrive adding them in the order of s, so the
 // result does not depend on who arrives last.
 //
-// Roundings: h to bf16 (the operand type of the second product, as between the grouped GEMMs); the
-// expert outputs are not rounded before the weighted sum; out once to bf16.  fp8 weights convert to
+// Roundings: h is kept as the sum of two bf16 values (16 bits of it: the operand type of the second
+// product, whose spare MFMA rate makes the second part free, where one bf16 value alone would put as much
+// error into out as out's own rounding); the expert outputs are not rounded before the weighted sum; out
+// once to bf16.  fp8 weights convert to
 // bf16 exactly, their scales multiply fp32 sums; int4 words enter as 128 + q (int4_dequant.h).
 //
 // Rows past N or T, k past K and tokens that are not the expert's are read through bounds-checked
@@ -158,11 +160,15 @@ struct Matrix {
     int N, K, group;
 };
 
-// Where a stream's token rows come from: memory, row by row (the rows of h, which differ from expert to
-// expert), or LDS (the rows of x, the same for every expert), laid out as MFMA operands by stage_x.
+// Where a stream's token rows come from: LDS (kTile: the rows of x, the same for every expert, laid out as
+// MFMA operands by stage_x), memory, row by row (kRow: x where LDS cannot hold it), or memory as pairs of
+// bf16 values whose sum is the operand (kPair: the rows of h, which differ from expert to expert).
+enum { kTile, kRow, kPair };
+
 template <int TF>
 struct TokenRows {
     __amdgpu_buffer_rsrc_t buf;
+    int lo;  // kPair: byte offset of the low parts
 };
 
 template <int TF>
@@ -173,7 +179,7 @@ struct TokenTile {
 
 // [E, N, K] weights, K contiguous: a load takes 16 bytes of 4 consecutive k chunks of 16 rows.  A granule
 // is US loads per column set.
-template <int KIND, int CPL_, int TF, int US, bool XL>
+template <int KIND, int CPL_, int TF, int US, int SRC>
 struct Rows {
     static constexpr int CPL = CPL_;
     static constexpr int ES = KIND == kBf16 ? 2 : 1;
@@ -182,9 +188,10 @@ struct Rows {
     static constexpr int UK = KS * US;
     static constexpr int NB = UK > 128 ? UK / 128 : 1;  // block scales of a granule
     static_assert(KIND != kFp8Blk || 128 % UK == 0 || UK % 128 == 0, "granules and blocks of k nest");
-    using X = std::conditional_t<XL, TokenTile<TF>, TokenRows<TF>>;
+    using X = std::conditional_t<SRC == kTile, TokenTile<TF>, TokenRows<TF>>;
+    static constexpr int NP = SRC == kPair ? 2 : 1;  // bf16 parts of a token operand
     struct Set {
-        u32x4 b[US][CPL], x[XL ? 1 : US][TF][FR];
+        u32x4 b[US][CPL], x[SRC == kTile ? 1 : US][TF][FR][NP];
         float sc[NB];
     };
     // the 8 k of chunk c of a row: which 32-k fragment, and which quarter wave of it
@@ -220,7 +227,7 @@ struct Rows {
 #pragma unroll
             for (int j = 0; j < CPL; ++j) r.b[u][j] = load16(g.w, in ? g.woff[j] + k * ES : kPast);
         }
-        if constexpr (!XL)
+        if constexpr (SRC != kTile)
 #pragma unroll
         for (int u = 0; u < US; ++u) {
             const int k = (i * US + u) * KS;
@@ -229,24 +236,28 @@ struct Rows {
             for (int f = 0; f < TF; ++f)
 #pragma unroll
                 for (int c = 0; c < FR; ++c)
-                    r.x[u][f][c] = load16(x.buf, in && arow[f] != kPast ? arow[f] + (k + kq * (8 * FR) + c * 8) * 2 : kPast);
+#pragma unroll
+                    for (int h = 0; h < NP; ++h)
+                        r.x[u][f][c][h] =
+                            load16(x.buf, in && arow[f] != kPast ? arow[f] + (k + kq * (8 * FR) + c * 8) * 2 + h * x.lo : kPast);
         }
         if constexpr (KIND == kFp8Blk)
 #pragma unroll
             for (int b = 0; b < NB; ++b) r.sc[b] = some ? g.bscale[min(i * UK / 128 + b, (m.K + 127) / 128 - 1)] : 0.f;
     }
     __device__ static __forceinline__ void multiply(const Set& r, const X& x, int i, f32x4 (&out)[CPL][TF]) {
-        bf16x8 xf[US][TF][FR];
+        bf16x8 xf[US][TF][FR][NP];
 #pragma unroll
         for (int u = 0; u < US; ++u)
 #pragma unroll
             for (int f = 0; f < TF; ++f)
 #pragma unroll
                 for (int c = 0; c < FR; ++c) {
-                    if constexpr (XL)
-                        xf[u][f][c] = *reinterpret_cast<const bf16x8*>(x.at[f] + ((i * US + u) * FR + c) * x.step[f]);
+                    if constexpr (SRC == kTile)
+                        xf[u][f][c][0] = *reinterpret_cast<const bf16x8*>(x.at[f] + ((i * US + u) * FR + c) * x.step[f]);
                     else
-                        xf[u][f][c] = as_bf16x8(r.x[u][f][c]);
+#pragma unroll
+                        for (int h = 0; h < NP; ++h) xf[u][f][c][h] = as_bf16x8(r.x[u][f][c][h]);
                 }
         constexpr int UB = KIND == kFp8Blk ? US / NB : US;  // loads under one scale
 #pragma unroll
@@ -263,7 +274,9 @@ struct Rows {
                         const bf16x8 w = KIND == kBf16 ? as_bf16x8(r.b[u][j]) : fp8_to_bf16(r.b[u][j][2 * c], r.b[u][j][2 * c + 1]);
 #pragma unroll
                         for (int f = 0; f < TF; ++f)
-                            d[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][f][c], w, d[f], 0, 0, 0);
+#pragma unroll
+                            for (int h = 0; h < NP; ++h)
+                                d[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][f][c][h], w, d[f], 0, 0, 0);
                     }
 #pragma unroll
                 for (int f = 0; f < TF; ++f)
@@ -288,13 +301,14 @@ struct Rows {
 
 // GPTQ words [E, K/8, N]: a lane reads 4 consecutive columns of a k-octet, one column per MFMA.  A granule
 // of 32 * STEPS k lies in one quantisation group and contributes s * (acc - (128 + z) * sum_k x), the sum from one more MFMA against ones.
-template <int STEPS, int TF, bool XL>
+template <int STEPS, int TF, int SRC>
 struct Words {
     static constexpr int CPL = 4;
     static constexpr int UK = STEPS * 32;
-    using X = std::conditional_t<XL, TokenTile<TF>, TokenRows<TF>>;
+    using X = std::conditional_t<SRC == kTile, TokenTile<TF>, TokenRows<TF>>;
+    static constexpr int NP = SRC == kPair ? 2 : 1;  // bf16 parts of a token operand
     struct Set {
-        u32x4 q[STEPS], x[XL ? 1 : STEPS][TF];
+        u32x4 q[STEPS], x[SRC == kTile ? 1 : STEPS][TF][NP];
         uint2 s;
         uint32_t z;
     };
@@ -322,12 +336,15 @@ struct Words {
             r.q[st] = load16(g.w, some ? ((i * (UK / 8) + st * 4 + kq) * m.N + ncol) * 4 : kPast);
         r.s = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(g.s, some ? (sg * m.N + ncol) * 2 : kPast, 0, 0));
         r.z = __builtin_amdgcn_raw_buffer_load_b32(g.z, some ? (sg * (m.N / 8) + ncol / 8) * 4 : kPast, 0, 0);
-        if constexpr (!XL)
+        if constexpr (SRC != kTile)
 #pragma unroll
         for (int st = 0; st < STEPS; ++st)
 #pragma unroll
             for (int f = 0; f < TF; ++f)
-                r.x[st][f] = load16(x.buf, some && arow[f] != kPast ? arow[f] + (i * UK + st * 32 + kq * 8) * 2 : kPast);
+#pragma unroll
+                for (int h = 0; h < NP; ++h)
+                    r.x[st][f][h] =
+                        load16(x.buf, some && arow[f] != kPast ? arow[f] + (i * UK + st * 32 + kq * 8) * 2 + h * x.lo : kPast);
     }
     __device__ static __forceinline__ void multiply(const Set& r, const X& x, int i, f32x4 (&out)[4][TF]) {
         const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
@@ -344,19 +361,23 @@ struct Words {
         }
 #pragma unroll
         for (int st = 0; st < STEPS; ++st) {
-            bf16x8 xf[TF];
+            bf16x8 xf[TF][NP];
 #pragma unroll
-            for (int f = 0; f < TF; ++f) {
-                if constexpr (XL) xf[f] = *reinterpret_cast<const bf16x8*>(x.at[f] + (i * STEPS + st) * x.step[f]);
-                else xf[f] = as_bf16x8(permute_k(r.x[st][f]));
-                accx[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[f], as_bf16x8(ones), accx[f], 0, 0, 0);
-            }
+            for (int f = 0; f < TF; ++f)
+#pragma unroll
+                for (int h = 0; h < NP; ++h) {
+                    if constexpr (SRC == kTile) xf[f][h] = *reinterpret_cast<const bf16x8*>(x.at[f] + (i * STEPS + st) * x.step[f]);
+                    else xf[f][h] = as_bf16x8(permute_k(r.x[st][f][h]));
+                    accx[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[f][h], as_bf16x8(ones), accx[f], 0, 0, 0);
+                }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const bf16x8 w = as_bf16x8(dequant_word(r.q[st][j], nib_mask, bf16_128));
 #pragma unroll
                 for (int f = 0; f < TF; ++f)
-                    acc[j][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[f], w, acc[j][f], 0, 0, 0);
+#pragma unroll
+                    for (int h = 0; h < NP; ++h)
+                        acc[j][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[f][h], w, acc[j][f], 0, 0, 0);
             }
         }
 #pragma unroll
@@ -374,14 +395,16 @@ struct Words {
 };
 
 // The weight types' streams.  The granule is what two register sets, the sums and the addresses leave room
-// for in 128 registers, which lets sixteen waves share a compute unit; with the token rows in LDS (XL) all of
-// a set is weights (4 to 8 KB a wave in flight).  int4 with two token fragments from memory takes up to 256
-// registers and eight waves instead.
-template <int KIND, int STEPS, int TF, bool XL>
+// for, given the waves that are to share a compute unit: sixteen (128 registers) with x in LDS or in memory,
+// twelve with pairs, eight for int4 with two token fragments from memory.  2 to 8 KB of weights a wave are
+// in flight.
+template <int KIND, int STEPS, int TF, int SRC>
 using Stream = std::conditional_t<
-    KIND == kInt4, Words<STEPS, TF, XL>,
-    Rows<KIND, 2, TF, XL ? (KIND == kBf16 ? (TF == 1 ? 4 : 3) : (TF == 1 ? 4 : 2)) : KIND == kBf16 ? (TF == 1 ? 3 : 2) : (TF == 1 ? 2 : 1), XL>>;
-constexpr int min_waves(int kind, int tf, bool xl) { return kind == kInt4 && tf == 2 && !xl ? 2 : 4; }
+    KIND == kInt4, Words<STEPS, TF, SRC>,
+    Rows<KIND, 2, TF, SRC == kTile ? (KIND == kBf16 ? (TF == 1 ? 4 : 3) : (TF == 1 ? 4 : 2)) : KIND == kBf16 ? (TF == 1 ? 3 : 2) : (TF == 1 ? 2 : 1), SRC>>;
+constexpr int min_waves(int kind, int tf, int src) {
+    return kind == kInt4 && tf == 2 && src != kTile ? 2 : src == kPair ? 3 : 4;
+}
 
 // The wave's granules: `n` of them from granule g of segment `seg`, the segments' granules being [gb, ge) and
 // their numbers `stride` apart.  open_at(seg, Seg&, arow) opens a segment; flush(seg, out) takes its sums
@@ -487,14 +510,14 @@ __device__ __forceinline__ void stage_x(const FewArgs& a, uint16_t* lds, int kpa
     }
 }
 
-template <int KIND, int STEPS, int TF, int NW, bool XL>
-__global__ __launch_bounds__(64 * NW, min_waves(KIND, TF, XL)) void few_gate_up_kernel(FewArgs a) {
-    using S = Stream<KIND, STEPS, TF, XL>;
+template <int KIND, int STEPS, int TF, int NW, int SRC>
+__global__ __launch_bounds__(64 * NW, min_waves(KIND, TF, SRC)) void few_gate_up_kernel(FewArgs a) {
+    using S = Stream<KIND, STEPS, TF, SRC>;
     constexpr int CPL = S::CPL, NCOL = 16 * CPL, NT = 64 * NW;
     constexpr int PARTS = NW / 2;  // waves of one projection
     __shared__ Routed r;
     __shared__ f32x4 red[NW][CPL][64];
-    __shared__ __attribute__((aligned(16))) uint16_t xl[XL ? x_bytes(CPL, NW) / 2 : 8];
+    __shared__ __attribute__((aligned(16))) uint16_t xl[SRC == kTile ? x_bytes(CPL, NW) / 2 : 8];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
@@ -514,7 +537,7 @@ __global__ __launch_bounds__(64 * NW, min_waves(KIND, TF, XL)) void few_gate_up_
     const int grans = S::granules(m);
     typename S::X x;
     if (tid < kMaxE) r.tok[tid] = 0;
-    if constexpr (XL) stage_x<S, TF, NT>(a, xl, grans * S::UK, x);
+    if constexpr (SRC == kTile) stage_x<S, TF, NT>(a, xl, grans * S::UK, x);
     else x.buf = buffer(a.x, static_cast<int64_t>(a.T) * a.H * 2);
     lds_barrier();
     select_all<NW>(a, r, wave, lane);
@@ -564,11 +587,24 @@ __global__ __launch_bounds__(64 * NW, min_waves(KIND, TF, XL)) void few_gate_up_
                 }
                 h[j] = silu_mul(g, u);
             }
+            // the value and what its rounding to bf16 left, in two planes
             uint16_t* dst = a.hs + static_cast<int64_t>(t * a.top_k + r.slot[t][e]) * a.I + col;
-            if constexpr (CPL == 4)
-                *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
-            else
-                *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(h[0], h[1]);
+            uint16_t* rest = dst + static_cast<int64_t>(a.T) * a.top_k * a.I;
+            uint32_t hi[CPL / 2], lo[CPL / 2];
+#pragma unroll
+            for (int j = 0; j < CPL / 2; ++j) {
+                hi[j] = pack_bf16x2(h[2 * j], h[2 * j + 1]);
+                // (an infinite value has no rest: inf - inf would be NaN)
+                const float h0 = bf_lo(hi[j]), h1 = bf_hi(hi[j]);
+                lo[j] = pack_bf16x2(fabsf(h0) < INFINITY ? h[2 * j] - h0 : 0.f, fabsf(h1) < INFINITY ? h[2 * j + 1] - h1 : 0.f);
+            }
+            if constexpr (CPL == 4) {
+                *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2*>(rest) = make_uint2(lo[0], lo[1]);
+            } else {
+                *reinterpret_cast<uint32_t*>(dst) = hi[0];
+                *reinterpret_cast<uint32_t*>(rest) = lo[0];
+            }
         }
     };
     if (ge > gb) {
@@ -587,8 +623,8 @@ __global__ __launch_bounds__(64 * NW, min_waves(KIND, TF, XL)) void few_gate_up_
 // The granules of a column panel, expert by expert of the work list, are one sequence; the waves of the
 // panel's workgroups take equal consecutive shares of it, whatever the number of active experts.
 template <int KIND, int STEPS, int TF, int NW>
-__global__ __launch_bounds__(64 * NW, min_waves(KIND, TF, false)) void few_down_kernel(FewArgs a) {
-    using S = Stream<KIND, STEPS, TF, false>;
+__global__ __launch_bounds__(64 * NW, min_waves(KIND, TF, kPair)) void few_down_kernel(FewArgs a) {
+    using S = Stream<KIND, STEPS, TF, kPair>;
     constexpr int CPL = S::CPL, NCOL = 16 * CPL, NT = 64 * NW;
     __shared__ Routed r;
     __shared__ float s_w[kFewTokens * kFewTopK];
@@ -620,7 +656,8 @@ __global__ __launch_bounds__(64 * NW, min_waves(KIND, TF, false)) void few_down_
     const int q1 = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<int64_t>(total) * (who + 1) / waves));
     const int n0 = panel * NCOL;
     typename S::X x;
-    x.buf = buffer(a.hs, static_cast<int64_t>(a.T) * a.top_k * a.I * 2);
+    x.lo = a.T * a.top_k * a.I * 2;
+    x.buf = buffer(a.hs, 2 * static_cast<int64_t>(x.lo));
     f32x4 sum[CPL][TF];
 #pragma unroll
     for (int j = 0; j < CPL; ++j)
@@ -735,27 +772,27 @@ __global__ __launch_bounds__(64 * NW, min_waves(KIND, TF, false)) void few_down_
     }
 }
 
-template <int KIND, int STEPS, int TF, bool XL>
+template <int KIND, int STEPS, int TF, int SRC>
 hipError_t launch_gate_up(const FewArgs& a, hipStream_t s) {
-    constexpr int NCOL = 16 * Stream<KIND, STEPS, TF, XL>::CPL, NW = 4 * min_waves(KIND, TF, XL);
+    constexpr int NCOL = 16 * Stream<KIND, STEPS, TF, SRC>::CPL, NW = 4 * min_waves(KIND, TF, SRC);
     const int most = a.T * a.top_k < a.E ? a.T * a.top_k : a.E;  // active experts at most
     const int64_t items = static_cast<int64_t>(most) * ((a.I + NCOL - 1) / NCOL);
     const int grid = static_cast<int>(items < kFewGrid ? items : kFewGrid);
-    few_gate_up_kernel<KIND, STEPS, TF, NW, XL><<<grid + 1, 64 * NW, 0, s>>>(a);
+    few_gate_up_kernel<KIND, STEPS, TF, NW, SRC><<<grid + 1, 64 * NW, 0, s>>>(a);
     return hipGetLastError();
 }
 
 // LSTEPS: the int4 granule with x in LDS
 template <int KIND, int LSTEPS, int STEPS, int TF>
 hipError_t launch_kind(const FewArgs& a, hipStream_t s) {
-    using L = Stream<KIND, LSTEPS, TF, true>;
+    using L = Stream<KIND, LSTEPS, TF, kTile>;
     const int64_t kpad = (a.H + L::UK - 1) / L::UK * L::UK;
     int64_t rows = 0;
     for (int f = 0; f < TF; ++f) rows += x_rows(a.T, f);
     const bool lds = rows * kpad * 2 <= x_bytes(L::CPL, 16);
-    const hipError_t err = lds ? launch_gate_up<KIND, LSTEPS, TF, true>(a, s) : launch_gate_up<KIND, STEPS, TF, false>(a, s);
+    const hipError_t err = lds ? launch_gate_up<KIND, LSTEPS, TF, kTile>(a, s) : launch_gate_up<KIND, STEPS, TF, kRow>(a, s);
     if (err != hipSuccess) return err;
-    constexpr int NCOL = 16 * L::CPL, NW = 4 * min_waves(KIND, TF, false);
+    constexpr int NCOL = 16 * L::CPL, NW = 4 * min_waves(KIND, TF, kPair);
     few_down_kernel<KIND, STEPS, TF, NW><<<(a.H + NCOL - 1) / NCOL * a.splits, 64 * NW, 0, s>>>(a);
     return hipGetLastError();
 }

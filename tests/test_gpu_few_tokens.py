@@ -209,3 +209,30 @@ def test_few_tokens_graph_and_stream(m, weights):
         torch.cuda.synchronize()
         assert torch.equal(out, want[i][0]) and torch.equal(ids, want[i][1]) and torch.equal(w, want[i][2])
         assert torch.equal(other[0], want[(i + 1) % 4][0])
+
+
+@pytest.mark.parametrize("weights", ["bf16", "int4_gptq", "fp8", "fp8_block"])
+@pytest.mark.parametrize("T", [3, 20])
+def test_few_tokens_non_finite_rows_stay_their_own(m, weights, T):
+    """A token of NaN or infinities spoils its own row only, and an expert nobody chose is not read."""
+    cfg = C("nan", T, 256, 128, 8, 2, weights, group_size=64, seed=21)
+    d, dev, _ = inputs(cfg)
+    d["logits"][:, 5] = -100.0       # expert 5 is chosen by nobody
+    for w in dev:
+        if weights == "int4_gptq":
+            w.scales[5] = float("nan")
+        elif weights == "bf16":
+            w.w[5] = float("nan")
+        else:
+            w.codes[5] = 0x7F
+    plan = m.few_tokens_plan(*dev, 2, T)
+    logits, x = to_dev(d["logits"]), bf16_dev(d["x"])
+    clean = m.moe_few_tokens(plan, logits, x)[0]
+    assert torch.isfinite(clean.float()).all()
+    bad = x.clone()
+    bad[1] = float("nan")
+    bad[2, 7] = float("inf")
+    got = m.moe_few_tokens(plan, logits, bad)[0]
+    keep = [t for t in range(T) if t not in (1, 2)]
+    assert torch.equal(got[keep], clean[keep])
+    assert torch.isnan(got[1].float()).all() and not torch.isfinite(got[2].float()).any()
