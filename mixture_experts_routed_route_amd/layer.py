@@ -17,6 +17,12 @@ which is what decode batches want: there the sorted layout is mostly padding.  O
 rows with bf16 weights, the down-projection fold runs by default in the down GEMM's epilogue
 (``moe_grouped_gemm_down_lora``), as the gate and up folds run in the gate/up GEMM's.
 
+With fp8 weights under block scales (``Fp8BlockWeight``) x is quantised per token and 128 columns and the
+GEMMs are the block-scaled ones; Hs is quantised in between, or leaves the gate/up GEMM as codes
+(``hs_codes``).  ``norm_stage`` runs the residual addition and norm in front of the layer and, for fp8
+weights, hands the layer x already quantised.  With ``few_tokens``, batches of at most 32 tokens run the
+two launches of ``moe_few_tokens`` instead of the stages above.
+
 Buffers are allocated once per token count (``plan``) so a forward pass allocates
 nothing and its launch grids depend on host scalars only.
 """
@@ -33,6 +39,8 @@ from .ops import (Bf16Weight, Fp8Weight, GptqWeight, LoraTables, Routing, gemm_w
                   moe_align, moe_combine, moe_grouped_gemm, moe_grouped_gemm_fp8, moe_lora_fold, moe_lora_gather_fold,
                   moe_quantize_fp8, moe_route, moe_route_align, moe_silu_mul, pack_lora_tables, stack_lora_tables,
                   moe_grouped_gemm_gate_up_lora, moe_grouped_gemm_down_lora)
+from .serving import (FEW_TOKENS, FP8_BLOCK, FewTokensPlan, Fp8BlockWeight, few_tokens_plan, moe_few_tokens,
+                      moe_grouped_gemm_fp8_block, moe_quantize_fp8_block, moe_rmsnorm)
 
 FOLD_MODES = ("auto", "grouped", "gather")
 
@@ -54,17 +62,24 @@ class Buffers:
     sx: Optional[torch.Tensor] = None
     hq: Optional[torch.Tensor] = None
     sh: Optional[torch.Tensor] = None
+    xn: Optional[torch.Tensor] = None  # norm_stage's output (allocated by its first call)
+    few: Optional[FewTokensPlan] = None  # few_tokens: the weights and workspace of the two-launch form
 
 
 class MoeLayer:
     def __init__(self, num_experts: int, hidden: int, inter: int, top_k: int, block_size: int, gate, up, down,
                  lora: Optional[LoraTables] = None, renormalize: bool = True, lora_cap: Optional[int] = None,
                  fold: str = "auto", lora_gate: Optional[LoraTables] = None, lora_up: Optional[LoraTables] = None,
-                 gate_up_fused: bool = True, down_fused: bool = True):
+                 gate_up_fused: bool = True, down_fused: bool = True, few_tokens: bool = False,
+                 hs_codes: bool = False):
         if fold not in FOLD_MODES:
             raise ValueError(f"fold must be one of {FOLD_MODES}")
-        if isinstance(gate, Fp8Weight) and (lora_gate is not None or lora_up is not None):
+        if isinstance(gate, (Fp8Weight, Fp8BlockWeight)) and (lora_gate is not None or lora_up is not None):
             raise ValueError("gate/up LoRA tables are not supported with fp8 weights")
+        if few_tokens and (lora is not None or lora_gate is not None or lora_up is not None):
+            raise ValueError("few_tokens does not take LoRA tables")
+        if hs_codes and (not isinstance(gate, Fp8BlockWeight) or lora is not None):
+            raise ValueError("hs_codes is for block-scaled fp8 weights without LoRA (whose fold reads the bf16 Hs)")
         self.E, self.H, self.I, self.top_k, self.bs = num_experts, hidden, inter, top_k, block_size
         self.gate, self.up, self.down, self.lora = gate, up, down, lora
         self.lora_gate, self.lora_up = lora_gate, lora_up
@@ -77,10 +92,20 @@ class MoeLayer:
         # down-projection LoRA folded in the down GEMM's epilogue where the fold runs over the sorted
         # rows (bf16 weights), else the shrink and expand kernels after the down GEMM
         self.down_fused = down_fused and isinstance(down, Bf16Weight)
+        # batches of at most FEW_TOKENS tokens in two launches (activations stay bf16 with fp8 weights too)
+        self.few_tokens = few_tokens
+        # Hs as E4M3 codes straight from the gate/up GEMM: exact block scales and no bf16 Hs, but slower
+        # than the bf16 form and the quantisation kernel (402 against 258 us at 12288 rows of 64 experts
+        # of 1408 x 4096), whose products run at the fp8 MFMA rate
+        self.hs_codes = hs_codes
 
     @property
     def fp8(self) -> bool:
         return isinstance(self.gate, Fp8Weight)
+
+    @property
+    def fp8_block(self) -> bool:
+        return isinstance(self.gate, Fp8BlockWeight)
 
     @property
     def gate_up_lora(self) -> bool:
@@ -92,7 +117,8 @@ class MoeLayer:
     # ------------------------------------------------------------------ construction from host arrays
     @staticmethod
     def from_arrays(d: Dict[str, object], device, lora_cap: Optional[int] = None, fold: str = "auto",
-                    gate_up_fused: bool = True, down_fused: bool = True) -> "MoeLayer":
+                    gate_up_fused: bool = True, down_fused: bool = True, few_tokens: bool = False,
+                    hs_codes: bool = False) -> "MoeLayer":
         """Build from host numpy arrays (bf16 / fp16 as uint16 bit patterns, GPTQ words as int32)."""
         cfg = d["cfg"]
         bf = lambda a: torch.from_numpy(np.ascontiguousarray(a)).view(torch.bfloat16).to(device)
@@ -100,7 +126,8 @@ class MoeLayer:
             gate, up, down = Bf16Weight(bf(d["wg"])), Bf16Weight(bf(d["wu"])), Bf16Weight(bf(d["wd"]))
         elif "fp8_gate" in d:
             def f8(w):
-                return Fp8Weight(torch.from_numpy(w["codes"]).to(device), torch.from_numpy(w["scales"]).to(device))
+                kind = Fp8BlockWeight if w["scales"].ndim == 3 else Fp8Weight  # scales per block, or per channel
+                return kind(torch.from_numpy(w["codes"]).to(device), torch.from_numpy(w["scales"]).to(device))
             gate, up, down = f8(d["fp8_gate"]), f8(d["fp8_up"]), f8(d["fp8_down"])
         else:
             def gq(w):
@@ -128,7 +155,7 @@ class MoeLayer:
         lora_gate = tables("lora_gate")
         lora_up = tables("lora_up")
         return MoeLayer(cfg.E, cfg.H, cfg.I, cfg.top_k, cfg.block_size, gate, up, down, lora, cfg.renormalize,
-                        lora_cap, fold, lora_gate, lora_up, gate_up_fused, down_fused)
+                        lora_cap, fold, lora_gate, lora_up, gate_up_fused, down_fused, few_tokens, hs_codes)
 
     # ------------------------------------------------------------------ buffers
     def plan(self, T: int, device) -> Buffers:
@@ -142,7 +169,7 @@ class MoeLayer:
             xa = torch.empty(cap * max(t.max_rank for t in self._tables()), **bf)
         b = Buffers(T, torch.empty((T, self.top_k), dtype=torch.int32, device=device),
                     torch.empty((T, self.top_k), dtype=torch.float32, device=device), r,
-                    torch.empty((r.max_pad, self.I), **bf), torch.empty((r.max_pad, self.H), **bf),
+                    torch.empty((0 if self.hs_codes else r.max_pad, self.I), **bf), torch.empty((r.max_pad, self.H), **bf),
                     torch.empty((T, self.H), **bf), xa, gemm_workspace(device))
         if self.gate_up_lora and self.gate_up_fused:
             rank = max(t.max_rank for t in (self.lora_gate, self.lora_up) if t is not None)
@@ -154,17 +181,46 @@ class MoeLayer:
             u8, f32 = dict(dtype=torch.uint8, device=device), dict(dtype=torch.float32, device=device)
             b.xq, b.sx = torch.empty((T, self.H), **u8), torch.empty(max(T, 1), **f32)
             b.hq, b.sh = torch.empty((r.max_pad, self.I), **u8), torch.empty(r.max_pad, **f32)
+        if self.fp8_block:
+            u8, f32 = dict(dtype=torch.uint8, device=device), dict(dtype=torch.float32, device=device)
+            b.xq, b.sx = torch.empty((T, self.H), **u8), torch.empty((T, -(-self.H // FP8_BLOCK)), **f32)
+            b.hq, b.sh = torch.empty((r.max_pad, self.I), **u8), torch.empty((r.max_pad, -(-self.I // FP8_BLOCK)), **f32)
+        if self.few_tokens and T <= FEW_TOKENS:
+            b.few = few_tokens_plan(self.gate, self.up, self.down, self.top_k, T, self.renormalize)
         return b
 
     # ------------------------------------------------------------------ forward
     def route_align(self, logits: torch.Tensor, b: Buffers) -> None:
         moe_route_align(logits, self.top_k, self.renormalize, self.bs, b.ids, b.w, b.routing)
 
-    def gate_up_stage(self, x: torch.Tensor, b: Buffers, row_adapter: Optional[torch.Tensor] = None) -> None:
+    def norm_stage(self, x: torch.Tensor, weight: torch.Tensor, b: Buffers, eps: float = 1e-6,
+                   residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """The residual addition (in place in ``residual``) and root-mean-square norm in front of the layer.
+        Returns the normed rows (``b.xn``), what the router and ``forward`` take; with fp8 weights the same
+        launch quantises them into the buffers, and ``forward`` is called with ``x_quantized=True``."""
+        if b.xn is None:
+            b.xn = torch.empty_like(b.out)
+        if b.xq is None or b.few is not None:  # the few-token form reads the bf16 rows
+            return moe_rmsnorm(x, weight, eps, residual=residual, y=b.xn)
+        return moe_rmsnorm(x, weight, eps, residual=residual, y=b.xn, q=b.xq, scale=b.sx[: b.T])
+
+    def gate_up_stage(self, x: torch.Tensor, b: Buffers, row_adapter: Optional[torch.Tensor] = None,
+                      x_quantized: bool = False) -> None:
         """Hs from x: the fused kernel, or gathered gate and up, their folds and SiLU * up; with fp8
-        weights, x quantised per token and the fp8 fused kernel."""
+        weights, x quantised per token (unless ``norm_stage`` has) and the fp8 fused kernel."""
+        if self.fp8_block:
+            if not x_quantized:
+                moe_quantize_fp8_block(x, b.xq, b.sx)
+            if self.hs_codes:
+                moe_grouped_gemm_fp8_block(MOE_OP_GATE_UP_SILU, b.xq, b.sx, self.gate, self.up, b.routing, q=b.hq,
+                                           scale=b.sh, workspace=b.ws)
+            else:
+                moe_grouped_gemm_fp8_block(MOE_OP_GATE_UP_SILU, b.xq, b.sx, self.gate, self.up, b.routing, out=b.hs,
+                                           workspace=b.ws)
+            return
         if self.fp8:
-            moe_quantize_fp8(x, b.xq, b.sx)
+            if not x_quantized:
+                moe_quantize_fp8(x, b.xq, b.sx)
             moe_grouped_gemm_fp8(MOE_OP_GATE_UP_SILU, b.xq, b.sx, self.gate, self.up, b.routing, out=b.hs,
                                  workspace=b.ws)
             return
@@ -185,6 +241,11 @@ class MoeLayer:
 
     def down_stage(self, b: Buffers, row_adapter: Optional[torch.Tensor] = None) -> None:
         """Ys from Hs; with the fused down fold, the LoRA shrink and the down GEMM whose epilogue folds."""
+        if self.fp8_block:  # the real rows of Hs quantised per 128 columns (unless they came as codes)
+            if not self.hs_codes:
+                moe_quantize_fp8_block(b.hs, b.hq, b.sh, b.routing)
+            moe_grouped_gemm_fp8_block(MOE_OP_DOWN, b.hq, b.sh, self.down, None, b.routing, out=b.ys, workspace=b.ws)
+            return
         if self.fp8:  # the real rows of Hs quantised per row, then the fp8 down GEMM
             moe_quantize_fp8(b.hs, b.hq, b.sh, b.routing)
             moe_grouped_gemm_fp8(MOE_OP_DOWN, b.hq, b.sh, self.down, None, b.routing, out=b.ys, workspace=b.ws)
@@ -202,8 +263,9 @@ class MoeLayer:
         return (self.lora is not None and self.down_fused and self.fold_mode(b) == "grouped"
                 and b.xa.numel() >= b.routing.max_pad * self.lora.max_rank)
 
-    def experts(self, x: torch.Tensor, b: Buffers, row_adapter: Optional[torch.Tensor] = None) -> None:
-        self.gate_up_stage(x, b, row_adapter)
+    def experts(self, x: torch.Tensor, b: Buffers, row_adapter: Optional[torch.Tensor] = None,
+                x_quantized: bool = False) -> None:
+        self.gate_up_stage(x, b, row_adapter, x_quantized)
         self.down_stage(b, row_adapter)
         self.lora_fold(b, row_adapter)
 
@@ -237,9 +299,14 @@ class MoeLayer:
         return moe_combine(b.ys, b.routing.inv_sorted, b.w, out=b.out)
 
     def forward(self, logits: torch.Tensor, x: torch.Tensor, b: Optional[Buffers] = None,
-                row_adapter: Optional[torch.Tensor] = None) -> torch.Tensor:
+                row_adapter: Optional[torch.Tensor] = None, x_quantized: bool = False) -> torch.Tensor:
+        """``x_quantized``: with fp8 weights, x is ``norm_stage``'s output and its codes are in the buffers."""
         if b is None:
+            if x_quantized:
+                raise ValueError("x_quantized needs the buffers that norm_stage filled")
             b = self.plan(x.shape[0], x.device)
+        if b.few is not None:
+            return moe_few_tokens(b.few, logits, x, b.ids, b.w, b.out)[0]
         self.route_align(logits, b)
-        self.experts(x, b, row_adapter)
+        self.experts(x, b, row_adapter, x_quantized)
         return self.combine(b)

@@ -290,3 +290,18 @@ def test_gemm_fp8_block_binding_refuses_mismatched_buffers():
             args["w1"] = args["w0"]
         with pytest.raises(ValueError, match=word):
             m.moe_grouped_gemm_fp8_block(**args)
+
+
+def test_layer_refuses_combinations_it_has_no_path_for():
+    w8 = m.Fp8BlockWeight(u8(4, 128, 128), torch.zeros(4, 1, 1))
+    wb = m.Bf16Weight(bf(4, 128, 128))
+    tabs = m.LoraTables(torch.zeros(4, dtype=torch.int64), torch.zeros(4, dtype=torch.int64), torch.zeros(4), 4, 128, 128, 32)
+
+    def layer(w, **kw):
+        return m.MoeLayer(4, 128, 128, 2, 16, w, w, w, **kw)
+    for w, kw, word in [(wb, dict(lora=tabs, few_tokens=True), "few_tokens"), (wb, dict(lora_up=tabs, few_tokens=True), "few_tokens"),
+                        (w8, dict(lora_gate=tabs), "fp8"), (wb, dict(hs_codes=True), "hs_codes"),
+                        (w8, dict(hs_codes=True, lora=tabs), "hs_codes")]:
+        with pytest.raises(ValueError, match=word):
+            layer(w, **kw)
+    assert layer(w8, lora=tabs).fp8_block and layer(w8, hs_codes=True).hs_codes
