@@ -52,8 +52,7 @@ inline FewLayout few_layout(int T, int E, int top_k, int H, int I, bool int4) {
     FewLayout l;
     l.splits = splits < 1 ? 1 : splits;
     l.part_at = kFewCounterBytes;
-    const int tf = T <= 16 ? 1 : 2;
-    l.hs_at = l.part_at + up(l.splits > 1 ? static_cast<int64_t>(panels) * l.splits * tf * 16 * ncol * 4 : 0);
+    l.hs_at = l.part_at + up(l.splits > 1 ? static_cast<int64_t>(panels) * l.splits * T * ncol * 4 : 0);
     l.bytes = l.hs_at + up(static_cast<int64_t>(T) * top_k * I * 4);
     return l;
 }

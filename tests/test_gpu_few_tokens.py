@@ -94,6 +94,10 @@ CASES = [
     C("e1", 6, 128, 64, 1, 1, seed=8), C("e63", 9, 128, 64, 63, 5, seed=9), C("e65", 9, 128, 64, 65, 5, seed=10),
     C("e200", 20, 64, 64, 200, 8, seed=11), C("e256", 32, 64, 32, 256, 32, seed=12), C("all", 4, 128, 64, 12, 12, seed=13),
     C("no_renorm", 5, 128, 64, 8, 2, renormalize=False, seed=14), C("skewed", 32, 128, 64, 128, 8, logits="zipf", seed=15),
+    # experts with more than 16 tokens (two groups): one more, all of them
+    *[C(f"{w}_two_groups_T{T}", T, 256, 128, E, E, w, group_size=64, seed=T + E)
+      for w in ("bf16", "int4_gptq", "fp8", "fp8_block") for T, E in ((17, 3), (32, 8))],
+    C("two_groups_e256", 32, 64, 32, 256, 32, logits="zipf", seed=33),
     # int4: every group size, one and two token fragments, few groups per wave
     *[C(f"int4_g{G}_T{T}", T, 512, 256, 8, 2, "int4_gptq", group_size=G, seed=G + T) for G in (32, 64, 128, 256) for T in (1, 19)],
     C("int4_one_unit", 3, 64, 64, 4, 2, "int4_gptq", group_size=64, seed=20), C("int4_mid", 16, 1024, 704, 16, 4, "int4_gptq", group_size=64, seed=21),
