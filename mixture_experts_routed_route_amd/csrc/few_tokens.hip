@@ -405,11 +405,13 @@ struct Words {
 
 // The weight types' streams.  The granule is what two register sets, the sums and the addresses leave room
 // for, given the waves that are to share a compute unit: sixteen (128 registers) with x in LDS or in memory,
-// twelve with pairs.  2 to 8 KB of weights a wave are in flight.
+// twelve with pairs, or eight with the larger granule that int4 groups of 128 allow (16 tokens of 8 of 64
+// experts of 1408 x 2048: 23.7 us for few_down against 25.1 with granules of 64 k and twelve waves).  2 to
+// 8 KB of weights a wave are in flight.
 template <int KIND, int STEPS, int SRC>
 using Stream = std::conditional_t<KIND == kInt4, Words<STEPS, SRC>,
                                   Rows<KIND, 2, KIND != kBf16 ? 2 : SRC == kTile ? 4 : 3, SRC>>;
-constexpr int min_waves(int src) { return src == kPair ? 3 : 4; }
+constexpr int min_waves(int steps, int src) { return src != kPair ? 4 : steps == 4 ? 2 : 3; }
 
 // The wave's granules: `n` of them from granule g of segment `seg`, the segments' granules being [gb, ge) and
 // their numbers `stride` apart.  open_at(seg, Seg&) opens a segment, rows_at(seg) is this lane's token row in
@@ -506,7 +508,7 @@ __device__ __forceinline__ void stage_x(const FewArgs& a, uint16_t* lds, int kpa
 }
 
 template <int KIND, int STEPS, int NW, int SRC>
-__global__ __launch_bounds__(64 * NW, min_waves(SRC)) void few_gate_up_kernel(FewArgs a) {
+__global__ __launch_bounds__(64 * NW, min_waves(STEPS, SRC)) void few_gate_up_kernel(FewArgs a) {
     using S = Stream<KIND, STEPS, SRC>;
     constexpr int CPL = S::CPL, NCOL = 16 * CPL, NT = 64 * NW;
     constexpr int PARTS = NW / 2;  // waves of one projection
@@ -615,7 +617,7 @@ __global__ __launch_bounds__(64 * NW, min_waves(SRC)) void few_gate_up_kernel(Fe
 // The granules of a column panel, expert by expert of the work list, are one sequence; the waves of the
 // panel's workgroups take equal consecutive shares of it, whatever the number of active experts.
 template <int KIND, int STEPS, int NW>
-__global__ __launch_bounds__(64 * NW, min_waves(kPair)) void few_down_kernel(FewArgs a) {
+__global__ __launch_bounds__(64 * NW, min_waves(STEPS, kPair)) void few_down_kernel(FewArgs a) {
     using S = Stream<KIND, STEPS, kPair>;
     constexpr int CPL = S::CPL, NCOL = 16 * CPL, NT = 64 * NW;
     using Cell = std::conditional_t<CPL == 4, f32x4, f32x2>;  // CPL columns of a token
@@ -720,7 +722,7 @@ __global__ __launch_bounds__(64 * NW, min_waves(kPair)) void few_down_kernel(Few
 
 template <int KIND, int STEPS, int SRC>
 hipError_t launch_gate_up(const FewArgs& a, hipStream_t s) {
-    constexpr int NCOL = 16 * Stream<KIND, STEPS, SRC>::CPL, NW = 4 * min_waves(SRC);
+    constexpr int NCOL = 16 * Stream<KIND, STEPS, SRC>::CPL, NW = 4 * min_waves(STEPS, SRC);
     const int most = a.T * a.top_k < a.E ? a.T * a.top_k : a.E;  // active experts at most
     const int64_t items = static_cast<int64_t>(most) * ((a.I + NCOL - 1) / NCOL);
     const int grid = static_cast<int>(items < kFewGrid ? items : kFewGrid);
@@ -728,15 +730,15 @@ hipError_t launch_gate_up(const FewArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// LSTEPS: the int4 granule with x in LDS
-template <int KIND, int LSTEPS, int STEPS>
+// ROW_STEPS: the int4 granule where the registers have to hold x of sixteen waves
+template <int KIND, int STEPS, int ROW_STEPS>
 hipError_t launch_kind(const FewArgs& a, hipStream_t s) {
-    using L = Stream<KIND, LSTEPS, kTile>;
+    using L = Stream<KIND, STEPS, kTile>;
     const int64_t kpad = (a.H + L::UK - 1) / L::UK * L::UK;
     const bool lds = a.T * kpad * 2 <= x_bytes(L::CPL, 16);
-    const hipError_t err = lds ? launch_gate_up<KIND, LSTEPS, kTile>(a, s) : launch_gate_up<KIND, STEPS, kRow>(a, s);
+    const hipError_t err = lds ? launch_gate_up<KIND, STEPS, kTile>(a, s) : launch_gate_up<KIND, ROW_STEPS, kRow>(a, s);
     if (err != hipSuccess) return err;
-    constexpr int NCOL = 16 * L::CPL, NW = 4 * min_waves(kPair);
+    constexpr int NCOL = 16 * L::CPL, NW = 4 * min_waves(STEPS, kPair);
     few_down_kernel<KIND, STEPS, NW><<<(a.H + NCOL - 1) / NCOL * a.splits, 64 * NW, 0, s>>>(a);
     return hipGetLastError();
 }
