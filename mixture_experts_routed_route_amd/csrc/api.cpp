@@ -709,14 +709,14 @@ moe_status moe_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16
     REQUIRE(rows >= 0, "%s: rows %lld is negative", who, static_cast<long long>(rows));
     REQUIRE(k >= 8 && k % 8 == 0 && k <= (1 << 20), "%s: k %d must be a positive multiple of 8, at most 2^20", who, k);
     REQUIRE(eps >= 0.0f, "%s: eps must not be negative or NaN", who);
+    REQUIRE(scale_block == 0 || scale_block == MOE_FP8_BLOCK, "%s: scale_block %d not 0 or %d", who, scale_block,
+            MOE_FP8_BLOCK);
+    if (rows == 0) return ok();  // empty buffers may have no address
     REQUIRE(y_out != nullptr || q != nullptr, "%s: one of y_out and q is needed", who);
     REQUIRE((residual == nullptr) == (residual_out == nullptr), "%s: residual and residual_out go together", who);
     REQUIRE(residual_out == nullptr || residual_out != y_out, "%s: residual_out and y_out are one buffer", who);
-    REQUIRE(scale_block == 0 || scale_block == MOE_FP8_BLOCK, "%s: scale_block %d not 0 or %d", who, scale_block,
-            MOE_FP8_BLOCK);
     REQUIRE((q == nullptr) == (scale == nullptr), "%s: q and scale go together", who);
     if (q) REQUIRE(k % 16 == 0, "%s: k %d must be a multiple of 16 with q", who, k);
-    if (rows == 0) return ok();
     REQUIRE_PTR(who, x);
     REQUIRE_PTR(who, weight);
     if (residual) REQUIRE_PTR(who, residual);

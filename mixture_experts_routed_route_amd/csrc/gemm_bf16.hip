@@ -61,6 +61,20 @@
 // there a wave reads each k-step's fragments just before its MFMAs.  The epilogue multiplies by
 // the row's activation scale and the column's weight scale before SiLU * up.
 //
+// Block-scaled fp8 form (BLK > 0).  A stage is one block of 128 k, over which a row's activation scale
+// and the 128 weight rows' scale are constant: acc += (sa * sw) * (product over the stage).  The MFMA
+// operands are swapped (weights as rows, tokens as columns), so that a lane's 16 values of a block belong
+// to one token and share one factor; with tokens as rows the factors had to be broadcast value by value,
+// which cost 1576 against 1211 us.  The stage's activation scales come into LDS with its rows (one more
+// 4-byte load per wave).  What bounds it is issue: one multiply-add per value and stage beside the MFMAs,
+// which are 44% busy (57% in the row-scaled form, whose scales wait for the epilogue).
+//   bf16 out (BLK 1) multiplies the codes with the fp8 MFMA, which rounds sums of neighbouring products at
+//   about 2^-14 of the largest (measured: 2.7e-5 of the result, unbiased); below bf16's 2^-8.  8 experts,
+//   8192 rows, gate/up of 14336 x 4096: 1211 us, 1.59 PFLOP/s (the row-scaled form: 1030).
+//   Codes out (BLK 2) multiplies the codes converted to bf16, exactly, with the bf16 MFMA: its fp32 scales
+//   are results, and with the fp8 MFMA they were 2.0e-5 off.  64 experts of 1408 x 4096, 12288 rows: 385 us
+//   (244 with bf16 out); MFMA 39% busy, the conversions take the issue slots between them.
+//
 // LoRA epilogue (LORA > 0; atlas moe_lora_grouped.rs): before the stores, rows of adapted experts
 // get bf16(bf16(acc) + scale * bf16(xa . B_e^T)), from the shrink's xa rows (by sorted row) and the
 // adapter's B_e.  Gate/up folds the gate and up blocks with their own tables before SiLU * up;
@@ -168,11 +182,6 @@ struct BlockScales {
     float* qs;    // [max_pad, ceil(N/128)]
 };
 
-// LORA: 0 no LoRA epilogue (gate/up, or with GATE_UP false the down projection); 1 one adapter (every
-// folded row is adapter 0; down: only at rank == BK, folded from LDS); 2 any adapters (the rows of one
-// fragment may belong to different adapters: one pass per adapter present; down: any rank).  The
-// one-adapter form is the common case and keeps the lean epilogue, which the loop of the general
-// form would cost registers in the main loop.
 // Epilogue of the block-scaled form, whose accumulators hold one token row per lane: value v of block
 // [i][j] is row wm * 64 + i * 32 + fr, column j * 32 + (v / 4) * 8 + fc * 4 + v % 4 of the wave's columns.
 // Four consecutive values are four adjacent columns; the two half waves swap quads, so that a lane ends
@@ -257,6 +266,11 @@ __device__ __forceinline__ void store_rows(f32x16 (&acc)[FI][4], uint16_t* C, ui
     }
 }
 
+// LORA: 0 no LoRA epilogue (gate/up, or with GATE_UP false the down projection); 1 one adapter (every
+// folded row is adapter 0; down: only at rank == BK, folded from LDS); 2 any adapters (the rows of one
+// fragment may belong to different adapters: one pass per adapter present; down: any rank).  The
+// one-adapter form is the common case and keeps the lean epilogue, which the loop of the general
+// form would cost registers in the main loop.
 // BLK (with FP8): the block-scaled form, 1 with bf16 out on the fp8 MFMA, 2 with codes out on the bf16 one.
 template <bool GATE_UP, int BM, int BK, int STAGES, int NW, int LORA = 0, bool FP8 = false, int BLK = 0>
 __global__ __launch_bounds__(64 * NW, 1) void gemm_bf16_kernel(const Elem<FP8>* __restrict__ A,

@@ -301,9 +301,9 @@ class MoeLayer:
     def forward(self, logits: torch.Tensor, x: torch.Tensor, b: Optional[Buffers] = None,
                 row_adapter: Optional[torch.Tensor] = None, x_quantized: bool = False) -> torch.Tensor:
         """``x_quantized``: with fp8 weights, x is ``norm_stage``'s output and its codes are in the buffers."""
+        if x_quantized and (b is None or b.xn is None):
+            raise ValueError("x_quantized needs the buffers that norm_stage filled")
         if b is None:
-            if x_quantized:
-                raise ValueError("x_quantized needs the buffers that norm_stage filled")
             b = self.plan(x.shape[0], x.device)
         if b.few is not None:
             return moe_few_tokens(b.few, logits, x, b.ids, b.w, b.out)[0]

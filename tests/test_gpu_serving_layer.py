@@ -135,8 +135,23 @@ def test_norm_stage_feeds_the_layer(m, weights):
         b2.sx.copy_(s)
         layer.experts(want, b2, x_quantized=True)
         assert torch.equal(out, layer.combine(b2))
-    with pytest.raises(ValueError, match="norm_stage"):
-        layer.forward(logits, y, x_quantized=True)
+    for bufs in (None, layer.plan(cfg.T, "cuda")):
+        with pytest.raises(ValueError, match="norm_stage"):
+            layer.forward(logits, y, bufs, x_quantized=True)
+    with pytest.raises(ValueError, match="needs"):
+        layer.norm_stage(x[:-1], nw, b)          # buffers of another token count
+
+
+@pytest.mark.parametrize("kw", [{}, {"hs_codes": True}, {"few_tokens": True}])
+def test_no_tokens(m, kw):
+    d = block_inputs(BLOCK)
+    layer = m.MoeLayer.from_arrays(d, "cuda", **kw)
+    b = layer.plan(0, "cuda")
+    y = layer.norm_stage(torch.empty((0, BLOCK.H), dtype=torch.bfloat16, device="cuda"),
+                         torch.ones(BLOCK.H, dtype=torch.bfloat16, device="cuda"), b)
+    out = layer.forward(torch.empty((0, BLOCK.E), device="cuda"), y, b, x_quantized=True)
+    torch.cuda.synchronize()
+    assert out.shape == (0, BLOCK.H)
 
 
 @pytest.mark.parametrize("weights", ["bf16", "int4_gptq"])
