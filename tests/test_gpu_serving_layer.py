@@ -201,3 +201,28 @@ def test_norm_and_few_tokens_replay_from_a_graph(m):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(b.out, want[i])
+
+
+def test_two_streams_at_once(m):
+    """Buffers (plans) of their own on two streams, calls interleaved without waiting: as one at a time."""
+    layers, ins, bufs, want = [], [], [], []
+    for seed, kw in ((31, {"few_tokens": True}), (32, {"few_tokens": True}), (33, {})):
+        cfg = BLOCK.with_(T=12, seed=seed)
+        d = block_inputs(cfg)
+        layer = m.MoeLayer.from_arrays(d, "cuda", **kw)
+        b = layer.plan(cfg.T, "cuda")
+        args = to_dev(d["logits"]), bf16_dev(d["x"])
+        layers.append(layer), ins.append(args), bufs.append(b)
+        want.append(layer.forward(*args, b).clone())
+    torch.cuda.synchronize()
+    for b in bufs:
+        b.out.zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in layers]
+    for _ in range(25):
+        for s, layer, args, b in zip(streams, layers, ins, bufs):
+            with torch.cuda.stream(s):
+                layer.forward(*args, b)
+    torch.cuda.synchronize()
+    for b, w in zip(bufs, want):
+        assert torch.equal(b.out, w)
