@@ -188,11 +188,12 @@ void launch_scale(const NormArgs& a, hipStream_t s) {
 
 // ------------------------------------------------------------------ block quantisation
 // Codes of bf16 rows with one scale per 128 columns: 16 lanes of 8 columns make a block, so a row needs
-// no exchange beyond DPP.  TPR lanes walk a row, 2048 columns of it at a time at most; the loads of two
-// steps are in flight together.
-// 8191 rows of 4096 (102 MB) take 18.5 us, 5.5 TB/s; 12288 real rows of 1408 among 16320 sorted ones (52 MB)
-// 13.1 us, 4.0 TB/s: short rows, whose id each waits for.
-template <int TPR>
+// no exchange beyond DPP.  TPR lanes walk a row, U chunks each in flight together.  Rows of up to 2048
+// columns take one wave and one round of loads: 12288 real rows of 1408 among 16320 sorted ones (52 MB) 11.4
+// us, 4.6 TB/s, against 14.9 with a workgroup per row, most of whose lanes had one chunk or none.  Longer rows
+// take a workgroup, so that one row alone is one round up to 4096 columns: 8191 rows of 4096 (102 MB) 17.3 us
+// either way, 5.9 TB/s of reads and writes.
+template <int TPR, int U>
 __global__ __launch_bounds__(kThreads) void quantize_block_kernel(const uint16_t* __restrict__ x,
                                                                   uint8_t* __restrict__ q,
                                                                   float* __restrict__ scale,
@@ -223,10 +224,13 @@ __global__ __launch_bounds__(kThreads) void quantize_block_kernel(const uint16_t
                 make_uint2(fp8_codes4(bf_lo(v[0]) * f, bf_hi(v[0]) * f, bf_lo(v[1]) * f, bf_hi(v[1]) * f),
                            fp8_codes4(bf_lo(v[2]) * f, bf_hi(v[2]) * f, bf_lo(v[3]) * f, bf_hi(v[3]) * f));
         };
-        for (int c = t; c < blocks * 16; c += 2 * TPR) {
-            const u32x4 v0 = load(c), v1 = load(c + TPR);
-            emit(c, v0);
-            if (c + TPR < blocks * 16) emit(c + TPR, v1);
+        for (int c = t; c < blocks * 16; c += U * TPR) {
+            u32x4 v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = load(c + u * TPR);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (c + u * TPR < blocks * 16) emit(c + u * TPR, v[u]);
         }
     }
 }
@@ -251,9 +255,9 @@ hipError_t launch_quantize_fp8_block(const uint16_t* x, int64_t rows, int K, con
         const int64_t need = (rows + rpw - 1) / rpw;
         return static_cast<unsigned>(need < (1 << 20) ? need : (1 << 20));
     };
-    if (slots <= 16) quantize_block_kernel<16><<<grid(16), kThreads, 0, s>>>(x, q, scale, sorted_ids, P, rows, K);
-    else if (slots <= 64) quantize_block_kernel<64><<<grid(4), kThreads, 0, s>>>(x, q, scale, sorted_ids, P, rows, K);
-    else quantize_block_kernel<256><<<grid(1), kThreads, 0, s>>>(x, q, scale, sorted_ids, P, rows, K);
+    if (slots <= 16) quantize_block_kernel<16, 1><<<grid(16), kThreads, 0, s>>>(x, q, scale, sorted_ids, P, rows, K);
+    else if (slots <= 256) quantize_block_kernel<64, 4><<<grid(4), kThreads, 0, s>>>(x, q, scale, sorted_ids, P, rows, K);
+    else quantize_block_kernel<256, 2><<<grid(1), kThreads, 0, s>>>(x, q, scale, sorted_ids, P, rows, K);
     return hipGetLastError();
 }
 
