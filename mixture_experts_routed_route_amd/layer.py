@@ -63,6 +63,8 @@ class Buffers:
     hq: Optional[torch.Tensor] = None
     sh: Optional[torch.Tensor] = None
     xn: Optional[torch.Tensor] = None  # norm_stage's output (allocated by its first call)
+    pq: Optional[torch.Tensor] = None  # once norm_stage has run: where forward quantises an x of its own, so
+    ps: Optional[torch.Tensor] = None  # that xq and sx are always the codes of xn
     few: Optional[FewTokensPlan] = None  # few_tokens: the weights and workspace of the two-launch form
 
 
@@ -198,30 +200,45 @@ class MoeLayer:
         """The residual addition (in place in ``residual``) and root-mean-square norm in front of the layer.
         Returns the normed rows (``b.xn``), what the router and ``forward`` take; with fp8 weights the same
         launch quantises them into the buffers, and ``forward`` is called with ``x_quantized=True``."""
-        if b.xn is None:
-            b.xn = torch.empty_like(b.out)
+        y = torch.empty_like(b.out) if b.xn is None else b.xn
         if b.xq is None or b.few is not None:  # the few-token form reads the bf16 rows
-            return moe_rmsnorm(x, weight, eps, residual=residual, y=b.xn)
-        return moe_rmsnorm(x, weight, eps, residual=residual, y=b.xn, q=b.xq, scale=b.sx[: b.T])
+            moe_rmsnorm(x, weight, eps, residual=residual, y=y)
+        else:
+            first = b.pq is None
+            q, scale = (torch.empty_like(b.xq), torch.empty_like(b.sx)) if first else (b.xq, b.sx)
+            moe_rmsnorm(x, weight, eps, residual=residual, y=y, q=q, scale=scale[: b.T])
+            if first:  # (graphs captured before this go on quantising into the buffers they know)
+                b.pq, b.ps, b.xq, b.sx = b.xq, b.sx, q, scale
+        b.xn = y
+        return y
+
+    def _x_codes(self, x: torch.Tensor, b: Buffers, x_quantized: bool):
+        """Codes and scales of x: quantised here, or norm_stage's (without a norm_stage, what the caller has
+        put into the buffers)."""
+        if x_quantized:
+            if b.xn is not None and (x.data_ptr() != b.xn.data_ptr() or x.shape != b.xn.shape):
+                raise ValueError("x_quantized: x is not norm_stage's output, whose codes the buffers hold")
+            return b.xq, b.sx
+        q, scale = (b.xq, b.sx) if b.pq is None else (b.pq, b.ps)
+        (moe_quantize_fp8_block if self.fp8_block else moe_quantize_fp8)(x, q, scale)
+        return q, scale
 
     def gate_up_stage(self, x: torch.Tensor, b: Buffers, row_adapter: Optional[torch.Tensor] = None,
                       x_quantized: bool = False) -> None:
         """Hs from x: the fused kernel, or gathered gate and up, their folds and SiLU * up; with fp8
         weights, x quantised per token (unless ``norm_stage`` has) and the fp8 fused kernel."""
         if self.fp8_block:
-            if not x_quantized:
-                moe_quantize_fp8_block(x, b.xq, b.sx)
+            xq, sx = self._x_codes(x, b, x_quantized)
             if self.hs_codes:
-                moe_grouped_gemm_fp8_block(MOE_OP_GATE_UP_SILU, b.xq, b.sx, self.gate, self.up, b.routing, q=b.hq,
+                moe_grouped_gemm_fp8_block(MOE_OP_GATE_UP_SILU, xq, sx, self.gate, self.up, b.routing, q=b.hq,
                                            scale=b.sh, workspace=b.ws)
             else:
-                moe_grouped_gemm_fp8_block(MOE_OP_GATE_UP_SILU, b.xq, b.sx, self.gate, self.up, b.routing, out=b.hs,
+                moe_grouped_gemm_fp8_block(MOE_OP_GATE_UP_SILU, xq, sx, self.gate, self.up, b.routing, out=b.hs,
                                            workspace=b.ws)
             return
         if self.fp8:
-            if not x_quantized:
-                moe_quantize_fp8(x, b.xq, b.sx)
-            moe_grouped_gemm_fp8(MOE_OP_GATE_UP_SILU, b.xq, b.sx, self.gate, self.up, b.routing, out=b.hs,
+            xq, sx = self._x_codes(x, b, x_quantized)
+            moe_grouped_gemm_fp8(MOE_OP_GATE_UP_SILU, xq, sx, self.gate, self.up, b.routing, out=b.hs,
                                  workspace=b.ws)
             return
         if not self.gate_up_lora:
@@ -300,7 +317,8 @@ class MoeLayer:
 
     def forward(self, logits: torch.Tensor, x: torch.Tensor, b: Optional[Buffers] = None,
                 row_adapter: Optional[torch.Tensor] = None, x_quantized: bool = False) -> torch.Tensor:
-        """``x_quantized``: with fp8 weights, x is ``norm_stage``'s output and its codes are in the buffers."""
+        """``x_quantized``: x is what ``norm_stage`` returned on these buffers, unchanged; with fp8 weights its
+        codes are read there (another x is refused), with the other types x itself."""
         if x_quantized and (b is None or b.xn is None):
             raise ValueError("x_quantized needs the buffers that norm_stage filled")
         if b is None:
