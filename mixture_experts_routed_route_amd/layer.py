@@ -324,7 +324,11 @@ class MoeLayer:
         if b is None:
             b = self.plan(x.shape[0], x.device)
         if b.few is not None:
-            return moe_few_tokens(b.few, logits, x, b.ids, b.w, b.out)[0]
+            p = b.few
+            if p.gate is not self.gate or p.up is not self.up or p.down is not self.down:
+                p.use(self.gate, self.up, self.down)
+            p.renormalize = bool(self.renormalize)
+            return moe_few_tokens(p, logits, x, b.ids, b.w, b.out)[0]
         self.route_align(logits, b)
         self.experts(x, b, row_adapter, x_quantized)
         return self.combine(b)

@@ -172,7 +172,10 @@ def moe_grouped_gemm_fp8_block(op: int, a: torch.Tensor, a_scale: torch.Tensor, 
 @dataclass
 class FewTokensPlan:
     """What ``moe_few_tokens`` keeps between calls: the checked weights and the workspace (calls on one
-    plan must not overlap: one plan per stream that runs the layer)."""
+    plan must not overlap: one plan per stream that runs the layer).
+
+    The weights may be replaced, by ``use`` or by giving a weight object other tensors: a call that finds
+    another tensor or address than the checked one checks the weights again."""
     gate: object
     up: object
     down: object
@@ -183,14 +186,29 @@ class FewTokensPlan:
     max_tokens: int
     renormalize: bool
     workspace: torch.Tensor
-    structs: Tuple[MoeWeight, MoeWeight, MoeWeight]
 
     def __post_init__(self):
-        self.refs = tuple(ctypes.byref(w) for w in self.structs)
+        self.use(self.gate, self.up, self.down)
 
     @property
     def device(self) -> torch.device:
         return self.workspace.device
+
+    def use(self, gate, up, down) -> None:
+        """Check the weights, of the plan's sizes, and note their addresses; refused ones change nothing."""
+        who = "moe_few_tokens"
+        ws = (gate, up, down)
+        _check_weights(*ws, who)
+        _need(tuple(gate.shape) == (self.E, self.I, self.H),
+              f"{who}: gate is {tuple(gate.shape)}; the plan was made for {(self.E, self.I, self.H)}")
+        _need(all(t.device == self.device for w in ws for t in _weight_tensors(w)),
+              f"{who}: the weights are not on {self.device}")
+        structs = tuple(w.struct() for w in ws)
+        self.gate, self.up, self.down = ws
+        self.tensors = tuple((w, name, t, t.data_ptr()) for w in ws for name, t in vars(w).items()
+                             if isinstance(t, torch.Tensor))
+        self.structs = structs
+        self.refs = tuple(ctypes.byref(w) for w in structs)
 
 
 def _weight_tensors(w):
@@ -212,6 +230,15 @@ def _check_weight(w, who: str) -> None:
         _need(tuple(getattr(w, name).shape) == shape, f"{who}: {name} is {tuple(getattr(w, name).shape)}; needs {shape}")
 
 
+def _check_weights(gate, up, down, who: str) -> None:
+    E, I, H = gate.shape
+    _need(type(gate) is type(up) is type(down), f"{who}: gate, up and down must have one type")
+    _need(tuple(up.shape) == (E, I, H) and tuple(down.shape) == (E, H, I),
+          f"{who}: gate is {(E, I, H)}, up {tuple(up.shape)}, down {tuple(down.shape)}")
+    for w in (gate, up, down):
+        _check_weight(w, who)
+
+
 def few_tokens_plan(gate, up, down, top_k: int, max_tokens: int = FEW_TOKENS,
                     renormalize: bool = True) -> FewTokensPlan:
     """Check the expert weights of a layer (gate and up ``[E, I, H]``, down ``[E, H, I]``; all bf16, GPTQ
@@ -219,12 +246,8 @@ def few_tokens_plan(gate, up, down, top_k: int, max_tokens: int = FEW_TOKENS,
     to ``max_tokens`` tokens."""
     who = "few_tokens_plan"
     E, I, H = gate.shape
-    _need(type(gate) is type(up) is type(down), f"{who}: gate, up and down must have one type")
-    _need(tuple(up.shape) == (E, I, H) and tuple(down.shape) == (E, H, I),
-          f"{who}: gate is {(E, I, H)}, up {tuple(up.shape)}, down {tuple(down.shape)}")
     _need(0 <= max_tokens <= FEW_TOKENS, f"{who}: max_tokens {max_tokens} not in [0, {FEW_TOKENS}]")
-    for w in (gate, up, down):
-        _check_weight(w, who)
+    _check_weights(gate, up, down, who)
     structs = tuple(w.struct() for w in (gate, up, down))
     device = _weight_tensors(gate)[0].device
     _need(all(t.device == device for w in (gate, up, down) for t in _weight_tensors(w)),
@@ -232,7 +255,7 @@ def few_tokens_plan(gate, up, down, top_k: int, max_tokens: int = FEW_TOKENS,
     n = int(lib().moe_few_tokens_workspace_bytes(max_tokens, E, top_k, H, I, structs[0].type))
     _need(n >= 0, f"{who}: unsupported sizes (E={E}, top_k={top_k}, hidden={H}, inter={I})")
     return FewTokensPlan(gate, up, down, E, H, I, top_k, max_tokens, bool(renormalize),
-                         torch.zeros(n, dtype=torch.uint8, device=device), structs)
+                         torch.zeros(n, dtype=torch.uint8, device=device))
 
 
 def moe_few_tokens(plan: FewTokensPlan, logits: torch.Tensor, x: torch.Tensor,
@@ -244,6 +267,10 @@ def moe_few_tokens(plan: FewTokensPlan, logits: torch.Tensor, x: torch.Tensor,
     who = "moe_few_tokens"
     if x.dim() != 2 or x.shape[1] != plan.H:
         raise ValueError(f"{who}: x is {tuple(x.shape)}; its width must be {plan.H}")
+    for w, name, t, address in plan.tensors:
+        if getattr(w, name) is not t or t.data_ptr() != address:
+            plan.use(plan.gate, plan.up, plan.down)
+            break
     T, k = x.shape[0], plan.top_k
     if T > plan.max_tokens:
         raise ValueError(f"{who}: {T} tokens; the plan holds {plan.max_tokens}")

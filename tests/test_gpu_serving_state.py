@@ -4,10 +4,11 @@ import pytest
 import torch
 
 from _util import bf16_dev, to_dev
-from moe_synth import make_inputs
+from moe_synth import MoeConfig, make_inputs
 from test_gpu_serving_layer import BLOCK, block_inputs
 
 pytestmark = pytest.mark.gpu
+FEW = MoeConfig("few_state", T=6, H=512, I=256, E=16, top_k=4, block_size=16, group_size=64)
 
 
 @pytest.fixture(scope="module")
@@ -46,3 +47,26 @@ def test_codes_of_a_norm_outlast_other_batches(m, weights):
         assert torch.equal(layer.forward(logits, y, b, x_quantized=True), want)
     with pytest.raises(ValueError, match="norm_stage"):
         layer.forward(logits, x2, b, x_quantized=True)
+
+
+@pytest.mark.parametrize("weights", ["bf16", "int4_gptq"])
+def test_few_tokens_layer_follows_replaced_weights(m, weights):
+    """A weight object with other tensors, and another weight object: the answer of a layer made of them."""
+    first, second = (make_inputs(FEW.with_(weights=weights, seed=s)) for s in (1, 2))
+    layer, other = (m.MoeLayer.from_arrays(d, "cuda", few_tokens=True) for d in (first, second))
+    b = layer.plan(FEW.T, "cuda")
+    args = to_dev(first["logits"]), bf16_dev(first["x"])
+    before = layer.forward(*args, b).clone()
+    want = other.forward(*args, other.plan(FEW.T, "cuda")).clone()
+    assert not torch.equal(before, want)
+    kept = [dict(vars(w)) for w in (layer.gate, layer.up, layer.down)]
+    for mine, its in ((layer.gate, other.gate), (layer.up, other.up), (layer.down, other.down)):
+        for name, t in vars(its).items():
+            setattr(mine, name, t)
+    assert torch.equal(layer.forward(*args, b), want)
+    for w, tensors in zip((layer.gate, layer.up, layer.down), kept):
+        for name, t in tensors.items():
+            setattr(w, name, t)
+    assert torch.equal(layer.forward(*args, b), before)
+    layer.gate, layer.up, layer.down = other.gate, other.up, other.down
+    assert torch.equal(layer.forward(*args, b), want)

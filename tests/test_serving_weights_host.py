@@ -1,0 +1,104 @@
+"""Expert weights of the serving operators, CPU side: the addresses and devices that reach the library.
+Tensors that claim to be on a GPU stand for device memory; the launches are noted, not made."""
+import ctypes
+
+import pytest
+import torch
+
+import mixture_experts_routed_route_amd as m
+from mixture_experts_routed_route_amd import serving
+from mixture_experts_routed_route_amd._lib import MoeWeight
+
+
+class OnGpu(torch.Tensor):
+    """A CPU tensor that says it is on GPU ``index``."""
+    index = 0
+    is_cuda = True
+
+    @property
+    def device(self):
+        return torch.device("cuda", self.index)
+
+    def get_device(self):
+        return self.index
+
+
+class OnOther(OnGpu):
+    index = 1
+
+
+def gpu(t, cls=OnGpu):
+    return t.as_subclass(cls)
+
+
+def bf(*shape):
+    return gpu(torch.zeros(shape, dtype=torch.bfloat16))
+
+
+E, H, I, K = 4, 64, 32, 2
+
+
+@pytest.fixture
+def launches(monkeypatch):
+    seen = []
+    monkeypatch.setattr(serving, "_launch", lambda name, index, *args: seen.append((name, index, args)))
+    return seen
+
+
+@pytest.fixture
+def few(launches, monkeypatch):
+    """A plan of bf16 weights and a call of it that gives the three data addresses."""
+    monkeypatch.setattr(serving.torch, "zeros", lambda *s, device=None, **kw: gpu(torch.empty(*s, **kw).zero_()))
+    plan = m.few_tokens_plan(m.Bf16Weight(bf(E, I, H)), m.Bf16Weight(bf(E, I, H)), m.Bf16Weight(bf(E, H, I)), K, 4)
+    args = (gpu(torch.empty((3, E))), bf(3, H), gpu(torch.empty((3, K), dtype=torch.int32)),
+            gpu(torch.empty((3, K))), bf(3, H))
+
+    def call():
+        m.moe_few_tokens(plan, *args)
+        return [ctypes.cast(ref, ctypes.POINTER(MoeWeight)).contents.data for ref in launches.pop()[2][2:5]]
+    return plan, call
+
+
+def test_few_tokens_follows_replaced_weights(few):
+    """A weight object that gets another tensor, or a tensor that gets other memory: the next call reads that."""
+    plan, call = few
+    old = plan.gate.w
+    assert call() == [plan.gate.w.data_ptr(), plan.up.w.data_ptr(), plan.down.w.data_ptr()]
+    plan.gate.w = bf(E, I, H)
+    assert plan.gate.w.data_ptr() != old.data_ptr() and call()[0] == plan.gate.w.data_ptr()
+    kept = plan.up.w.data
+    plan.up.w.data = bf(E, I, H)
+    assert kept.data_ptr() != plan.up.w.data_ptr() and call()[1] == plan.up.w.data_ptr()
+    down = m.Bf16Weight(bf(E, H, I))
+    plan.use(plan.gate, plan.up, down)
+    assert call() == [plan.gate.w.data_ptr(), plan.up.w.data_ptr(), down.w.data_ptr()]
+
+
+def test_few_tokens_refuses_replacements_it_cannot_read(few):
+    plan, call = few
+    want = call()
+    before = (plan.gate, plan.up, plan.down)
+    for bad, word in [(m.Bf16Weight(bf(E, I, H + 8)), "up"), (m.Bf16Weight(bf(E, I, H).transpose(1, 2)), "up"),
+                      (m.Bf16Weight(gpu(torch.empty((E, I, H), dtype=torch.bfloat16), OnOther)), "not on")]:
+        with pytest.raises(ValueError, match=word):
+            plan.use(bad, plan.up, plan.down)
+        assert (plan.gate, plan.up, plan.down) == before and call() == want
+    wide = [m.Bf16Weight(bf(*s)) for s in ((E, I, H + 8), (E, I, H + 8), (E, H + 8, I))]
+    with pytest.raises(ValueError, match="made for"):
+        plan.use(*wide)
+    plan.gate.w = bf(E, I + 8, H)
+    for _ in range(2):                 # refused as long as it is there
+        with pytest.raises(ValueError, match="up"):
+            call()
+
+
+def test_layer_hands_replaced_weights_to_its_few_token_plan(few, monkeypatch):
+    plan, _ = few
+    layer = m.MoeLayer(E, H, I, K, 16, plan.gate, plan.up, plan.down, few_tokens=True)
+    b = m.layer.Buffers(3, None, None, None, None, None, None, None, None, few=plan)
+    monkeypatch.setattr(m.layer, "moe_few_tokens", lambda p, *a: (p,))
+    assert layer.forward(None, None, b) is plan and plan.renormalize
+    layer.down = m.Bf16Weight(bf(E, H, I))
+    layer.renormalize = False
+    layer.forward(None, None, b)
+    assert plan.down is layer.down and plan.tensors[2][2] is layer.down.w and not plan.renormalize
