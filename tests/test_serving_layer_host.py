@@ -38,8 +38,9 @@ def calls(monkeypatch):
         return y
 
     def quantize(x, q, scale, routing=None):
-        q.fill_(int(x[0, 0]) if x.numel() else 0)
-        scale.fill_(float(x[0, 0]) if x.numel() else 0.0)
+        if routing is None:            # (Hs in the sorted layout is not computed here)
+            q.fill_(int(x[0, 0]))
+            scale.fill_(float(x[0, 0]))
 
     def gemm(op, a, a_scale, *args, **kw):
         if op == m.MOE_OP_GATE_UP_SILU:
