@@ -80,6 +80,10 @@ def _index(t: torch.Tensor, dtype: torch.dtype, name: str) -> int:
     return t.get_device()
 
 
+def _weight_tensors(w):
+    return [t for t in vars(w).values() if isinstance(t, torch.Tensor)]
+
+
 def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
                 residual_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
                 q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
@@ -159,6 +163,10 @@ def moe_grouped_gemm_fp8_block(op: int, a: torch.Tensor, a_scale: torch.Tensor, 
     s0 = w0.struct()
     s1 = w1.struct() if w1 is not None else None
     i = _index(a, torch.uint8, "a")
+    for w in (w0,) if w1 is None else (w0, w1):
+        for t in _weight_tensors(w):
+            if t.get_device() != i:
+                raise ValueError(f"{who}: a weight is on {t.device}, a on device {i}")
     _launch(who, i, op, a.data_ptr(), _ptr(a_scale, torch.float32, "a_scale", i),
             ctypes.byref(s0), ctypes.byref(s1) if s1 is not None else None, _ptr(out, torch.bfloat16, "out", i),
             _ptr(q, torch.uint8, "q", i), _ptr(scale, torch.float32, "scale", i),
@@ -209,10 +217,6 @@ class FewTokensPlan:
                              if isinstance(t, torch.Tensor))
         self.structs = structs
         self.refs = tuple(ctypes.byref(w) for w in structs)
-
-
-def _weight_tensors(w):
-    return [t for t in vars(w).values() if isinstance(t, torch.Tensor)]
 
 
 def _check_weight(w, who: str) -> None:

@@ -38,6 +38,11 @@ def bf(*shape):
 E, H, I, K = 4, 64, 32, 2
 
 
+def block(cls=OnGpu, n=I, k=H, scales_cls=None):
+    return m.Fp8BlockWeight(gpu(torch.zeros((E, n, k), dtype=torch.uint8), cls),
+                            gpu(torch.zeros((E, -(-n // 128), -(-k // 128))), scales_cls or cls))
+
+
 @pytest.fixture
 def launches(monkeypatch):
     seen = []
@@ -102,3 +107,21 @@ def test_layer_hands_replaced_weights_to_its_few_token_plan(few, monkeypatch):
     layer.renormalize = False
     layer.forward(None, None, b)
     assert plan.down is layer.down and plan.tensors[2][2] is layer.down.w and not plan.renormalize
+
+
+def test_gemm_fp8_block_refuses_weights_of_another_device(launches):
+    """Codes or scales, gate or up: a kernel on the activations' device would read the other device's memory."""
+    r = m.Routing.allocate(8, K, E, 16, "cpu")
+    r = m.Routing(*[gpu(v) if isinstance(v, torch.Tensor) else v for v in vars(r).values()])
+    n = 128
+
+    def call(w0, w1):
+        m.moe_grouped_gemm_fp8_block(m.MOE_OP_GATE_UP_SILU, gpu(torch.zeros((4, n), dtype=torch.uint8)),
+                                     gpu(torch.zeros((4, 1))), w0, w1, r, out=bf(r.max_pad, n))
+    call(block(n=n, k=n), block(n=n, k=n))
+    assert len(launches) == 1 and launches[0][:2] == ("moe_grouped_gemm_fp8_block", 0)
+    for kw in (dict(cls=OnOther), dict(scales_cls=OnOther)):
+        for w0, w1 in ((block(n=n, k=n, **kw), block(n=n, k=n)), (block(n=n, k=n), block(n=n, k=n, **kw))):
+            with pytest.raises(ValueError, match="a weight is on cuda:1"):
+                call(w0, w1)
+    assert len(launches) == 1
