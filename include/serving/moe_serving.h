@@ -104,8 +104,14 @@ moe_status moe_few_tokens(const float* logits, const uint16_t* x, const moe_weig
                           int32_t hidden, int32_t inter, int32_t renormalize, int32_t* topk_ids, float* topk_w,
                           uint16_t* out, void* workspace, int64_t workspace_bytes, moe_stream stream);
 
-/* Bytes of workspace for up to num_tokens tokens (wtype: the moe_wtype of the weights); -1 on invalid
- * arguments. */
+/* MOE_OK where moe_few_tokens takes these sizes, weight types and group sizes, else the status (and
+ * moe_last_error) that it would return.  The weights' addresses are not looked at.  A layer that is not
+ * supported runs through moe_route, moe_align and the grouped GEMMs, whose limits are wider. */
+moe_status moe_few_tokens_check(const moe_weight* w_gate, const moe_weight* w_up, const moe_weight* w_down,
+                                int32_t num_tokens, int32_t num_experts, int32_t top_k, int32_t hidden, int32_t inter);
+
+/* Bytes of workspace for up to num_tokens tokens (wtype: the moe_wtype of the weights); -1 for sizes that
+ * moe_few_tokens does not take with any group size. */
 int64_t moe_few_tokens_workspace_bytes(int32_t num_tokens, int32_t num_experts, int32_t top_k, int32_t hidden,
                                        int32_t inter, int32_t wtype);
 

@@ -76,6 +76,7 @@ SERVING_SIGNATURES = {
     "moe_grouped_gemm_fp8_block": (c_int32, [c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                              c_void_p, c_void_p, c_void_p, c_int64, c_int32, c_int32, c_int32,
                                              c_int32, c_int32, c_int64, c_void_p, c_int64, c_void_p]),
+    "moe_few_tokens_check": (c_int32, [c_void_p, c_void_p, c_void_p] + [c_int32] * 5),
     "moe_few_tokens_workspace_bytes": (c_int64, [c_int32] * 6),
     "moe_few_tokens": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32,
                                  c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p]),

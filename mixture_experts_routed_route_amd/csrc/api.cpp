@@ -810,20 +810,12 @@ moe_status moe_grouped_gemm_fp8_block(int32_t op, const uint8_t* a, const float*
                              static_cast<int>(max_pad), workspace, workspace_bytes, static_cast<hipStream_t>(stream)));
 }
 
-int64_t moe_few_tokens_workspace_bytes(int32_t num_tokens, int32_t num_experts, int32_t top_k, int32_t hidden,
-                                       int32_t inter, int32_t wtype) {
-    if (num_tokens < 0 || num_tokens > moe::kFewTokens || num_experts < 1 || num_experts > 256 || top_k < 1 ||
-        top_k > moe::kFewTopK || top_k > num_experts || hidden < 8 || hidden > moe::kFewMaxHidden || inter < 8 ||
-        wtype < MOE_W_BF16 || wtype > MOE_W_FP8_BLOCK)
-        return -1;
-    return moe::few_layout(num_tokens, num_experts, top_k, hidden, inter, wtype == MOE_W_INT4_GPTQ).bytes;
-}
-
-moe_status moe_few_tokens(const float* logits, const uint16_t* x, const moe_weight* w_gate, const moe_weight* w_up,
-                          const moe_weight* w_down, int32_t num_tokens, int32_t num_experts, int32_t top_k,
-                          int32_t hidden, int32_t inter, int32_t renormalize, int32_t* topk_ids, float* topk_w,
-                          uint16_t* out, void* workspace, int64_t workspace_bytes, moe_stream stream) {
-    const char* who = "moe_few_tokens";
+// Sizes and weight type of a few-token layer: the one test behind the call, moe_few_tokens_check and the size
+// query.
+// groups: the three weights' group sizes (int4; NULL while they are not known: the widths are then checked
+// against the smallest step of the type).
+static moe_status few_sizes(const char* who, int32_t num_tokens, int32_t num_experts, int32_t top_k, int32_t hidden,
+                            int32_t inter, int32_t type, const int32_t* groups) {
     REQUIRE(num_tokens >= 0, "%s: num_tokens %d is negative", who, num_tokens);
     REQUIRE(num_experts >= 1, "%s: num_experts %d < 1", who, num_experts);
     REQUIRE(top_k >= 1 && top_k <= num_experts, "%s: top_k %d not in [1, num_experts=%d]", who, top_k, num_experts);
@@ -831,19 +823,19 @@ moe_status moe_few_tokens(const float* logits, const uint16_t* x, const moe_weig
         return fail(MOE_EUNSUPPORTED, "%s: num_tokens=%d > %d", who, num_tokens, moe::kFewTokens);
     if (num_experts > 256) return fail(MOE_EUNSUPPORTED, "%s: num_experts=%d > 256", who, num_experts);
     if (top_k > moe::kFewTopK) return fail(MOE_EUNSUPPORTED, "%s: top_k=%d > %d", who, top_k, moe::kFewTopK);
-    REQUIRE(w_gate && w_up && w_down, "%s: w_gate, w_up and w_down are required", who);
-    const int type = w_gate->type;
     REQUIRE(type >= MOE_W_BF16 && type <= MOE_W_FP8_BLOCK, "%s: unknown weight type %d", who, type);
-    REQUIRE(w_up->type == type && w_down->type == type, "%s: the weights have different types", who);
-    int step = type == MOE_W_BF16 ? 8 : 16, group = 0;
+    int step = type == MOE_W_BF16 ? 8 : 16;
     double bytes = type == MOE_W_BF16 ? 2 : 1;  // per value
     if (type == MOE_W_INT4_GPTQ) {
-        group = w_gate->group_size;
-        REQUIRE(group == 32 || group == 64 || group == 128 || group == 256,
-                "%s: group_size %d not in {32,64,128,256}", who, group);
-        REQUIRE(w_up->group_size == group && w_down->group_size == group, "%s: the group sizes differ", who);
-        step = group > 64 ? group : 64;
+        step = 64;
         bytes = 0.5;
+        if (groups) {
+            const int32_t group = groups[0];
+            REQUIRE(group == 32 || group == 64 || group == 128 || group == 256,
+                    "%s: group_size %d not in {32,64,128,256}", who, group);
+            REQUIRE(groups[1] == group && groups[2] == group, "%s: the group sizes differ", who);
+            step = group > 64 ? group : 64;
+        }
     }
     REQUIRE(hidden >= step && hidden % step == 0, "%s: hidden %d must be a positive multiple of %d", who, hidden, step);
     REQUIRE(inter >= step && inter % step == 0, "%s: inter %d must be a positive multiple of %d", who, inter, step);
@@ -854,6 +846,40 @@ moe_status moe_few_tokens(const float* logits, const uint16_t* x, const moe_weig
     if (cells * bytes >= 2147483648.0 || static_cast<double>(num_tokens) * top_k * inter * 4 >= 2147483648.0)
         return fail(MOE_EUNSUPPORTED, "%s: an expert matrix (%d x %d) or the activations exceed 2 GiB", who, inter,
                     hidden);
+    return ok();
+}
+
+// The same from the three weights' descriptions, whose addresses are not looked at.
+static moe_status few_supported(const char* who, int32_t num_tokens, int32_t num_experts, int32_t top_k,
+                                int32_t hidden, int32_t inter, const moe_weight* w_gate, const moe_weight* w_up,
+                                const moe_weight* w_down) {
+    REQUIRE(w_gate && w_up && w_down, "%s: w_gate, w_up and w_down are required", who);
+    const int32_t groups[3] = {w_gate->group_size, w_up->group_size, w_down->group_size};
+    REQUIRE(w_up->type == w_gate->type && w_down->type == w_gate->type, "%s: the weights have different types", who);
+    return few_sizes(who, num_tokens, num_experts, top_k, hidden, inter, w_gate->type, groups);
+}
+
+int64_t moe_few_tokens_workspace_bytes(int32_t num_tokens, int32_t num_experts, int32_t top_k, int32_t hidden,
+                                       int32_t inter, int32_t wtype) {
+    if (few_sizes("moe_few_tokens_workspace_bytes", num_tokens, num_experts, top_k, hidden, inter, wtype, nullptr) != MOE_OK)
+        return -1;
+    return moe::few_layout(num_tokens, num_experts, top_k, hidden, inter, wtype == MOE_W_INT4_GPTQ).bytes;
+}
+
+moe_status moe_few_tokens_check(const moe_weight* w_gate, const moe_weight* w_up, const moe_weight* w_down,
+                                int32_t num_tokens, int32_t num_experts, int32_t top_k, int32_t hidden, int32_t inter) {
+    return few_supported("moe_few_tokens", num_tokens, num_experts, top_k, hidden, inter, w_gate, w_up, w_down);
+}
+
+moe_status moe_few_tokens(const float* logits, const uint16_t* x, const moe_weight* w_gate, const moe_weight* w_up,
+                          const moe_weight* w_down, int32_t num_tokens, int32_t num_experts, int32_t top_k,
+                          int32_t hidden, int32_t inter, int32_t renormalize, int32_t* topk_ids, float* topk_w,
+                          uint16_t* out, void* workspace, int64_t workspace_bytes, moe_stream stream) {
+    const char* who = "moe_few_tokens";
+    const moe_status rc = few_supported(who, num_tokens, num_experts, top_k, hidden, inter, w_gate, w_up, w_down);
+    if (rc != MOE_OK) return rc;
+    const int type = w_gate->type;
+    const int group = type == MOE_W_INT4_GPTQ ? w_gate->group_size : 0;
     if (num_tokens == 0) return ok();
     const moe::FewLayout l = moe::few_layout(num_tokens, num_experts, top_k, hidden, inter, type == MOE_W_INT4_GPTQ);
     REQUIRE_PTR(who, workspace);

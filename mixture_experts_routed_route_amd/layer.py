@@ -21,7 +21,8 @@ With fp8 weights under block scales (``Fp8BlockWeight``) x is quantised per toke
 GEMMs are the block-scaled ones; Hs is quantised in between, or leaves the gate/up GEMM as codes
 (``hs_codes``).  ``norm_stage`` runs the residual addition and norm in front of the layer and, for fp8
 weights, hands the layer x already quantised.  With ``few_tokens``, batches of at most 32 tokens run the
-two launches of ``moe_few_tokens`` instead of the stages above.
+two launches of ``moe_few_tokens`` instead of the stages above, where it takes the layer's sizes
+(``few_tokens_supported``).
 
 Buffers are allocated once per token count (``plan``) so a forward pass allocates
 nothing and its launch grids depend on host scalars only.
@@ -39,8 +40,8 @@ from .ops import (Bf16Weight, Fp8Weight, GptqWeight, LoraTables, Routing, gemm_w
                   moe_align, moe_combine, moe_grouped_gemm, moe_grouped_gemm_fp8, moe_lora_fold, moe_lora_gather_fold,
                   moe_quantize_fp8, moe_route, moe_route_align, moe_silu_mul, pack_lora_tables, stack_lora_tables,
                   moe_grouped_gemm_gate_up_lora, moe_grouped_gemm_down_lora)
-from .serving import (FEW_TOKENS, FP8_BLOCK, FewTokensPlan, Fp8BlockWeight, few_tokens_plan, moe_few_tokens,
-                      moe_grouped_gemm_fp8_block, moe_quantize_fp8_block, moe_rmsnorm)
+from .serving import (FEW_TOKENS, FP8_BLOCK, FewTokensPlan, Fp8BlockWeight, few_tokens_plan, few_tokens_supported,
+                      moe_few_tokens, moe_grouped_gemm_fp8_block, moe_quantize_fp8_block, moe_rmsnorm)
 
 FOLD_MODES = ("auto", "grouped", "gather")
 
@@ -94,7 +95,8 @@ class MoeLayer:
         # down-projection LoRA folded in the down GEMM's epilogue where the fold runs over the sorted
         # rows (bf16 weights), else the shrink and expand kernels after the down GEMM
         self.down_fused = down_fused and isinstance(down, Bf16Weight)
-        # batches of at most FEW_TOKENS tokens in two launches (activations stay bf16 with fp8 weights too)
+        # batches of at most FEW_TOKENS tokens in two launches where moe_few_tokens takes the layer
+        # (activations stay bf16 with fp8 weights too); else the stages
         self.few_tokens = few_tokens
         # Hs as E4M3 codes straight from the gate/up GEMM: exact block scales and no bf16 Hs, but slower
         # than the bf16 form and the quantisation kernel (402 against 258 us at 12288 rows of 64 experts
@@ -187,7 +189,7 @@ class MoeLayer:
             u8, f32 = dict(dtype=torch.uint8, device=device), dict(dtype=torch.float32, device=device)
             b.xq, b.sx = torch.empty((T, self.H), **u8), torch.empty((T, -(-self.H // FP8_BLOCK)), **f32)
             b.hq, b.sh = torch.empty((r.max_pad, self.I), **u8), torch.empty((r.max_pad, -(-self.I // FP8_BLOCK)), **f32)
-        if self.few_tokens and T <= FEW_TOKENS:
+        if self.few_tokens and T <= FEW_TOKENS and few_tokens_supported(self.gate, self.up, self.down, self.top_k, T):
             b.few = few_tokens_plan(self.gate, self.up, self.down, self.top_k, T, self.renormalize)
         return b
 

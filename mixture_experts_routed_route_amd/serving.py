@@ -13,11 +13,11 @@ from typing import Optional, Tuple
 
 import torch
 
-from ._lib import MOE_W_FP8_BLOCK, MoeWeight, check, lib
-from .ops import Fp8Weight, GptqWeight, Routing, _check_gemm_shapes, _dev, _need, _numel_at_least
+from ._lib import (MOE_OK, MOE_W_BF16, MOE_W_FP8, MOE_W_FP8_BLOCK, MOE_W_INT4_GPTQ, MoeWeight, check, lib)
+from .ops import Bf16Weight, Fp8Weight, GptqWeight, Routing, _check_gemm_shapes, _dev, _need, _numel_at_least
 
 __all__ = ["FP8_BLOCK", "FEW_TOKENS", "Fp8BlockWeight", "FewTokensPlan", "moe_rmsnorm", "moe_quantize_fp8_block",
-           "moe_grouped_gemm_fp8_block", "few_tokens_plan", "moe_few_tokens"]
+           "moe_grouped_gemm_fp8_block", "few_tokens_supported", "few_tokens_plan", "moe_few_tokens"]
 
 FP8_BLOCK = 128   # columns under one scale (weights: 128 x 128 blocks)
 FEW_TOKENS = 32   # most tokens of moe_few_tokens
@@ -209,6 +209,8 @@ class FewTokensPlan:
         _check_weights(*ws, who)
         _need(tuple(gate.shape) == (self.E, self.I, self.H),
               f"{who}: gate is {tuple(gate.shape)}; the plan was made for {(self.E, self.I, self.H)}")
+        why = _unsupported(*ws, self.top_k, self.max_tokens)
+        _need(why is None, f"{who}: unsupported: {why}")
         _need(all(t.device == self.device for w in ws for t in _weight_tensors(w)),
               f"{who}: the weights are not on {self.device}")
         structs = tuple(w.struct() for w in ws)
@@ -243,6 +245,26 @@ def _check_weights(gate, up, down, who: str) -> None:
         _check_weight(w, who)
 
 
+_KINDS = ((Bf16Weight, MOE_W_BF16), (GptqWeight, MOE_W_INT4_GPTQ), (Fp8Weight, MOE_W_FP8),
+          (Fp8BlockWeight, MOE_W_FP8_BLOCK))
+
+
+def _unsupported(gate, up, down, top_k: int, num_tokens: int) -> Optional[str]:
+    """Why ``moe_few_tokens`` does not take a layer, from its sizes and types alone (None: it does)."""
+    E, I, H = gate.shape
+    ws = [MoeWeight(next(kind for c, kind in _KINDS if isinstance(w, c)), int(getattr(w, "group_size", 0)),
+                    None, None, None) for w in (gate, up, down)]
+    status = lib().moe_few_tokens_check(*[ctypes.byref(w) for w in ws], num_tokens, E, top_k, H, I)
+    return None if status == MOE_OK else lib().moe_last_error().decode()
+
+
+def few_tokens_supported(gate, up, down, top_k: int, num_tokens: int = FEW_TOKENS) -> bool:
+    """Whether ``moe_few_tokens`` takes a layer of these weights' sizes, types and group sizes with up to
+    ``num_tokens`` tokens.  The grouped GEMMs take layers that it does not (int4 widths that are no multiple
+    of 64, group sizes that differ, expert matrices of 2 GiB and more, more than 32 experts per token)."""
+    return _unsupported(gate, up, down, top_k, num_tokens) is None
+
+
 def few_tokens_plan(gate, up, down, top_k: int, max_tokens: int = FEW_TOKENS,
                     renormalize: bool = True) -> FewTokensPlan:
     """Check the expert weights of a layer (gate and up ``[E, I, H]``, down ``[E, H, I]``; all bf16, GPTQ
@@ -252,12 +274,13 @@ def few_tokens_plan(gate, up, down, top_k: int, max_tokens: int = FEW_TOKENS,
     E, I, H = gate.shape
     _need(0 <= max_tokens <= FEW_TOKENS, f"{who}: max_tokens {max_tokens} not in [0, {FEW_TOKENS}]")
     _check_weights(gate, up, down, who)
+    why = _unsupported(gate, up, down, top_k, max_tokens)
+    _need(why is None, f"{who}: unsupported: {why}")
     structs = tuple(w.struct() for w in (gate, up, down))
     device = _weight_tensors(gate)[0].device
     _need(all(t.device == device for w in (gate, up, down) for t in _weight_tensors(w)),
           f"{who}: the weights are on more than one device")
     n = int(lib().moe_few_tokens_workspace_bytes(max_tokens, E, top_k, H, I, structs[0].type))
-    _need(n >= 0, f"{who}: unsupported sizes (E={E}, top_k={top_k}, hidden={H}, inter={I})")
     return FewTokensPlan(gate, up, down, E, H, I, top_k, max_tokens, bool(renormalize),
                          torch.zeros(n, dtype=torch.uint8, device=device))
 

@@ -3,7 +3,8 @@ that they are used in."""
 import pytest
 import torch
 
-from _util import bf16_dev, to_dev
+import oracle
+from _util import assert_close_rows, bf16_dev, bf16_host, to_dev
 from moe_synth import MoeConfig, make_inputs
 from test_gpu_serving_layer import BLOCK, block_inputs
 
@@ -70,3 +71,21 @@ def test_few_tokens_layer_follows_replaced_weights(m, weights):
     assert torch.equal(layer.forward(*args, b), before)
     layer.gate, layer.up, layer.down = other.gate, other.up, other.down
     assert torch.equal(layer.forward(*args, b), want)
+
+
+@pytest.mark.parametrize("kw", [dict(H=2080, I=96, weights="int4_gptq", group_size=32),
+                                dict(H=256, I=128, E=40, top_k=33)], ids=["int4_widths", "top_k_33"])
+def test_few_tokens_layer_outside_the_form_runs_its_stages(m, kw):
+    """few_tokens=True on a layer that moe_few_tokens refuses: the stages, within the layer's bar."""
+    cfg = FEW.with_(**kw)
+    d = make_inputs(cfg)
+    layer = m.MoeLayer.from_arrays(d, "cuda", few_tokens=True)
+    assert not m.few_tokens_supported(layer.gate, layer.up, layer.down, cfg.top_k)
+    b = layer.plan(cfg.T, "cuda")
+    assert b.few is None
+    nw = torch.ones(cfg.H, dtype=torch.bfloat16, device="cuda")
+    out = layer.forward(to_dev(d["logits"]), bf16_dev(d["x"]), b)
+    assert_close_rows(bf16_host(out), oracle.moe_layer(d)["out"], 2e-2, "stages")
+    y = layer.norm_stage(bf16_dev(d["x"]), nw, b)
+    out = layer.forward(to_dev(d["logits"]), y, b, x_quantized=True).clone()
+    assert torch.equal(out, layer.forward(to_dev(d["logits"]), y, b))
