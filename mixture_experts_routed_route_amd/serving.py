@@ -260,8 +260,9 @@ def _unsupported(gate, up, down, top_k: int, num_tokens: int) -> Optional[str]:
 
 def few_tokens_supported(gate, up, down, top_k: int, num_tokens: int = FEW_TOKENS) -> bool:
     """Whether ``moe_few_tokens`` takes a layer of these weights' sizes, types and group sizes with up to
-    ``num_tokens`` tokens.  The grouped GEMMs take layers that it does not (int4 widths that are no multiple
-    of 64, group sizes that differ, expert matrices of 2 GiB and more, more than 32 experts per token)."""
+    ``num_tokens`` tokens.  The grouped GEMMs take layers that it does not: a down projection of
+    another type or group size than gate and up, expert matrices of 2 GiB and more, more than 65536 hidden
+    columns or 32 experts per token."""
     return _unsupported(gate, up, down, top_k, num_tokens) is None
 
 

@@ -73,12 +73,14 @@ def test_few_tokens_layer_follows_replaced_weights(m, weights):
     assert torch.equal(layer.forward(*args, b), want)
 
 
-@pytest.mark.parametrize("kw", [dict(H=2080, I=96, weights="int4_gptq", group_size=32),
-                                dict(H=256, I=128, E=40, top_k=33)], ids=["int4_widths", "top_k_33"])
+@pytest.mark.parametrize("kw", [dict(weights="int4_gptq"), dict(H=256, I=128, E=40, top_k=33)],
+                         ids=["int4_down_group", "top_k_33"])
 def test_few_tokens_layer_outside_the_form_runs_its_stages(m, kw):
     """few_tokens=True on a layer that moe_few_tokens refuses: the stages, within the layer's bar."""
     cfg = FEW.with_(**kw)
     d = make_inputs(cfg)
+    if "weights" in kw:                # gate and up in groups of 64, down in groups of 128
+        d["down"] = make_inputs(cfg.with_(group_size=128))["down"]
     layer = m.MoeLayer.from_arrays(d, "cuda", few_tokens=True)
     assert not m.few_tokens_supported(layer.gate, layer.up, layer.down, cfg.top_k)
     b = layer.plan(cfg.T, "cuda")
