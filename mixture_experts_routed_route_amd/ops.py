@@ -63,6 +63,17 @@ def _dev(t: torch.Tensor, dtype: torch.dtype, name: str) -> int:
     return t.data_ptr()
 
 
+def _zeroed(nbytes: int, device) -> torch.Tensor:
+    """Zeroed bytes for a workspace whose counters have to be zero at its first use, on whatever stream that
+    is: the fill has ended when this returns (in a graph capture it is recorded instead)."""
+    t = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    if t.is_cuda:
+        with torch.cuda.device(t.device):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
+    return t
+
+
 # ----------------------------------------------------------------------------- weights
 @dataclass
 class Bf16Weight:
@@ -127,8 +138,7 @@ def align_workspace_bytes(num_pairs: int, num_experts: int) -> int:
 
 def gemm_workspace(device) -> torch.Tensor:
     """A zero-filled workspace for moe_grouped_gemm's split-K tile balancing (calls leave it zeroed)."""
-    n = int(lib().moe_grouped_gemm_workspace_bytes())
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    return _zeroed(int(lib().moe_grouped_gemm_workspace_bytes()), device)
 
 
 def check_group_arrays(num_experts: int, per_expert: Sequence[Tuple[str, int]], offsets: Sequence[int]) -> None:

@@ -14,7 +14,7 @@ from typing import Optional, Tuple
 import torch
 
 from ._lib import (MOE_OK, MOE_W_BF16, MOE_W_FP8, MOE_W_FP8_BLOCK, MOE_W_INT4_GPTQ, MoeWeight, check, lib)
-from .ops import Bf16Weight, Fp8Weight, GptqWeight, Routing, _check_gemm_shapes, _dev, _need, _numel_at_least
+from .ops import Bf16Weight, Fp8Weight, GptqWeight, Routing, _check_gemm_shapes, _dev, _need, _numel_at_least, _zeroed
 
 __all__ = ["FP8_BLOCK", "FEW_TOKENS", "Fp8BlockWeight", "FewTokensPlan", "moe_rmsnorm", "moe_quantize_fp8_block",
            "moe_grouped_gemm_fp8_block", "few_tokens_supported", "few_tokens_plan", "moe_few_tokens"]
@@ -283,7 +283,7 @@ def few_tokens_plan(gate, up, down, top_k: int, max_tokens: int = FEW_TOKENS,
           f"{who}: the weights are on more than one device")
     n = int(lib().moe_few_tokens_workspace_bytes(max_tokens, E, top_k, H, I, structs[0].type))
     return FewTokensPlan(gate, up, down, E, H, I, top_k, max_tokens, bool(renormalize),
-                         torch.zeros(n, dtype=torch.uint8, device=device))
+                         _zeroed(n, device))
 
 
 def moe_few_tokens(plan: FewTokensPlan, logits: torch.Tensor, x: torch.Tensor,

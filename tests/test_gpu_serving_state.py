@@ -91,3 +91,29 @@ def test_few_tokens_layer_outside_the_form_runs_its_stages(m, kw):
     y = layer.norm_stage(bf16_dev(d["x"]), nw, b)
     out = layer.forward(to_dev(d["logits"]), y, b, x_quantized=True).clone()
     assert torch.equal(out, layer.forward(to_dev(d["logits"]), y, b))
+
+
+def test_new_workspaces_serve_another_stream_at_once(m):
+    """Buffers made while the current stream is busy and used on another one, which waits for nothing: their
+    memory held other bytes before, so their zero counters must have been written by then."""
+    layers = [(cfg, make_inputs(cfg)) for cfg in (FEW, MoeConfig("split", T=96, H=1024, I=512, E=4, top_k=2, block_size=32))]
+    for cfg, d in layers:
+        layer = m.MoeLayer.from_arrays(d, "cuda", few_tokens=True)
+        args = to_dev(d["logits"]), bf16_dev(d["x"])
+        b = layer.plan(cfg.T, "cuda")
+        want = layer.forward(*args, b).clone()
+        for t in (b.ws, b.few.workspace if b.few is not None else b.ws):
+            t.fill_(255)               # what the allocator hands out next
+        del b
+        a = torch.randn((4096, 4096), device="cuda")
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        for _ in range(30):
+            a = a @ a
+            a /= a.abs().max()
+        b = layer.plan(cfg.T, "cuda")
+        with torch.cuda.stream(side):
+            got = layer.forward(*args, b)
+        side.synchronize()
+        assert torch.equal(got, want)
+        torch.cuda.synchronize()

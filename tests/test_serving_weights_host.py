@@ -53,7 +53,7 @@ def launches(monkeypatch):
 @pytest.fixture
 def few(launches, monkeypatch):
     """A plan of bf16 weights and a call of it that gives the three data addresses."""
-    monkeypatch.setattr(serving.torch, "zeros", lambda *s, device=None, **kw: gpu(torch.empty(*s, **kw).zero_()))
+    monkeypatch.setattr(serving, "_zeroed", lambda n, device: gpu(torch.zeros(n, dtype=torch.uint8)))
     plan = m.few_tokens_plan(m.Bf16Weight(bf(E, I, H)), m.Bf16Weight(bf(E, I, H)), m.Bf16Weight(bf(E, H, I)), K, 4)
     args = (gpu(torch.empty((3, E))), bf(3, H), gpu(torch.empty((3, K), dtype=torch.int32)),
             gpu(torch.empty((3, K))), bf(3, H))
@@ -125,3 +125,26 @@ def test_gemm_fp8_block_refuses_weights_of_another_device(launches):
             with pytest.raises(ValueError, match="a weight is on cuda:1"):
                 call(w0, w1)
     assert len(launches) == 1
+
+
+@pytest.mark.parametrize("capturing", [False, True])
+@pytest.mark.parametrize("make", [lambda: m.gemm_workspace("cuda"), lambda: m.few_tokens_plan(
+    m.Bf16Weight(bf(E, I, H)), m.Bf16Weight(bf(E, I, H)), m.Bf16Weight(bf(E, H, I)), K, 4).workspace], ids=["gemm", "few"])
+def test_workspaces_are_filled_before_any_stream_uses_them(monkeypatch, capturing, make):
+    """Their zero counters are waited for (a call on another stream would not wait); a capture records the fill."""
+    import contextlib
+    log, zeros = [], torch.zeros
+
+    class Stream:
+        def synchronize(self):
+            log.append("wait")
+
+    def filled(n, dtype=None, device=None):
+        log.append("fill")
+        return gpu(zeros(n, dtype=dtype))
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+    monkeypatch.setattr(torch, "zeros", lambda n, **kw: filled(n, **kw) if kw.get("device") is not None else zeros(n, **kw))
+    assert make().is_cuda
+    assert log == (["fill"] if capturing else ["fill", "wait"])
