@@ -184,8 +184,12 @@ __device__ __forceinline__ void select_all(const FewArgs& a, Routed& r, int wave
 // A wave walks a list of granules: UK consecutive k of one column panel (16 * CPL columns n0 + CPL * m + j,
 // m = lane % 16) of one expert.  Granules of one segment (an expert's panel) add up in `out`:
 //   out[j][v] += sum_k A(row, k) * W(column, k), rows 4 (lane / 16) + v of the segment's group of tokens
-// The next granule's loads (weights and token rows, of the next segment too) are always in flight while
-// one is multiplied: two register sets take turns.
+// The next granule's loads (weights and token rows, of the next segment too) are issued before one is
+// multiplied: two register sets take turns.  In eight of the seventeen kernels (few_gate_up: fp8 of both
+// kinds with x in LDS, int4 in groups of 64 and more with x in memory; few_down: bf16, int4 and block fp8) the
+// compiler waits with vmcnt(0) at the loop's head, where an edge of the control flow leaves the idle set
+// loading: there every second granule is multiplied with its successor's loads issued only after its own
+// have landed.
 struct Seg {
     int e, n0;                     // expert, first column
     __amdgpu_buffer_rsrc_t w;      // its matrix

@@ -66,14 +66,26 @@
 // operands are swapped (weights as rows, tokens as columns), so that a lane's 16 values of a block belong
 // to one token and share one factor; with tokens as rows the factors had to be broadcast value by value,
 // which cost 1576 against 1211 us.  The stage's activation scales come into LDS with its rows (one more
-// 4-byte load per wave).  What bounds it is issue: one multiply-add per value and stage beside the MFMAs,
-// which are 44% busy (57% in the row-scaled form, whose scales wait for the epilogue).
+// 4-byte load per wave); the weights' scales are loaded from memory stage by stage.
+// What bounds it is the order within a wave: neither the MFMAs (44% busy; 57% in the row-scaled form, whose
+// scales wait for the epilogue) nor the vector issue is full.
+//   - A block's 16 products go through one set of registers, so its multiply-adds wait for its MFMAs, and
+//     the next block's MFMAs for them; only the SIMD's other wave covers that, and 128-row tiles have none.
+//   - The weights' scales are vector loads that the compiler waits for with vmcnt(0), not knowing of the
+//     direct-to-LDS loads.  With 256-row tiles that is their latency at each stage's start; with 128-row
+//     tiles, every stage waits for the loads just issued, and the ring of three stages hides nothing.
+//   - The 256-row forms spill (17 registers, codes out 33, down 13).  Codes out reloads the activation
+//     scales' pointer in every stage behind the next stage's panel loads and waits for those with it; down
+//     reloads two registers once per tile that way.
+// Measured against the row-scaled form (us): 256-row tiles, 8192 rows, 8 experts of 14336 x 4096, gate/up
+// 1220 to 1280 (1.50 to 1.58 PFLOP/s) against 940 to 955, down 627 against 488; 128-row tiles, 3840 rows, 64 experts
+// of 1408 x 4096, gate/up 259 against 190, down 136 against 109.
 //   bf16 out (BLK 1) multiplies the codes with the fp8 MFMA, which rounds sums of neighbouring products at
-//   about 2^-14 of the largest (measured: 2.7e-5 of the result, unbiased); below bf16's 2^-8.  8 experts,
-//   8192 rows, gate/up of 14336 x 4096: 1211 us, 1.59 PFLOP/s (the row-scaled form: 1030).
+//   about 2^-14 of the largest (measured: 2.7e-5 of the result's rms, unbiased); below bf16's 2^-8.
 //   Codes out (BLK 2) multiplies the codes converted to bf16, exactly, with the bf16 MFMA: its fp32 scales
-//   are results, and with the fp8 MFMA they were 2.0e-5 off.  64 experts of 1408 x 4096, 12288 rows: 385 us
-//   (244 with bf16 out); MFMA 39% busy, the conversions take the issue slots between them.
+//   are results, and with the fp8 MFMA they were 2.0e-5 off.  64 experts of 1408 x 4096, 12288 rows: 382 us
+//   (bf16 out and the quantisation kernel: 258); 192 conversions and, the product entering the sum per half
+//   stage, 256 multiply-adds a stage instead of 128.
 //
 // LoRA epilogue (LORA > 0; atlas moe_lora_grouped.rs): before the stores, rows of adapted experts
 // get bf16(bf16(acc) + scale * bf16(xa . B_e^T)), from the shrink's xa rows (by sorted row) and the
@@ -769,9 +781,10 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm_bf16_kernel(const Elem<FP8>* 
                         }
                     } else {
                         // bf16 MFMAs over the converted codes, half a stage (64 k) at a time: the token
-                        // operands, converted once for the four weight blocks, then take 32 registers (a
-                        // whole stage's spilled inside the loop, and a spill's reload waits for the loads of
-                        // the next stage: 475 against 400 us at 64 experts of 1408 x 4096 and 12288 rows)
+                        // operands, converted once for the four weight blocks, then take 32 registers.  A
+                        // whole stage's spilled between the MFMAs: 475 against 400 us at 64 experts of 1408 x
+                        // 4096 and 12288 rows.  (The one reload left in the stage is the activation scales'
+                        // pointer, in issue_at.)
 #pragma unroll
                         for (int kk = 0; kk < 2; ++kk) {
                             bf16x8 ac[NF][4];
