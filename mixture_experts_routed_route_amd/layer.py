@@ -67,6 +67,7 @@ class Buffers:
     pq: Optional[torch.Tensor] = None  # once norm_stage has run: where forward quantises an x of its own, so
     ps: Optional[torch.Tensor] = None  # that xq and sx are always the codes of xn
     few: Optional[FewTokensPlan] = None  # few_tokens: the weights and workspace of the two-launch form
+    few_of: Optional["MoeLayer"] = None  # the layer whose weights those are
 
 
 class MoeLayer:
@@ -99,6 +100,7 @@ class MoeLayer:
         # (activations stay bf16 with fp8 weights too); else the stages.  It gains most at few tokens; from
         # 8 int4 tokens of 64 experts on the stages are level (16 of 1408 x 4096: 111 against 116 us)
         self.few_tokens = few_tokens
+        self._few: Optional[FewTokensPlan] = None  # this layer's weights on another layer's buffers
         # Hs as E4M3 codes straight from the gate/up GEMM: exact block scales and no bf16 Hs, but slower
         # than the bf16 form and the quantisation kernel (382 against 258 us at 12288 rows of 64 experts
         # of 1408 x 4096), whose products run at the fp8 MFMA rate
@@ -192,9 +194,27 @@ class MoeLayer:
             b.hq, b.sh = torch.empty((r.max_pad, self.I), **u8), torch.empty((r.max_pad, -(-self.I // FP8_BLOCK)), **f32)
         if self.few_tokens and T <= FEW_TOKENS and few_tokens_supported(self.gate, self.up, self.down, self.top_k, T):
             b.few = few_tokens_plan(self.gate, self.up, self.down, self.top_k, T, self.renormalize)
+            b.few_of = self
         return b
 
     # ------------------------------------------------------------------ forward
+    def few_plan(self, b: Buffers) -> Optional[FewTokensPlan]:
+        """The two-launch form with this layer's present weights and the buffers' workspace; None where this
+        layer runs its stages on them.  Layers of one size may share buffers, whichever of them planned them."""
+        if b.few is None or not self.few_tokens:
+            return None
+        p = b.few if b.few_of is self else self._few
+        if p is None or p.gate is not self.gate or p.up is not self.up or p.down is not self.down:
+            if not few_tokens_supported(self.gate, self.up, self.down, self.top_k, b.few.max_tokens):
+                return None
+            if p is not None:
+                p.use(self.gate, self.up, self.down)
+            else:
+                p = self._few = FewTokensPlan(self.gate, self.up, self.down, self.E, self.H, self.I, self.top_k,
+                                              b.few.max_tokens, bool(self.renormalize), b.few.workspace)
+        p.workspace, p.max_tokens, p.renormalize = b.few.workspace, b.few.max_tokens, bool(self.renormalize)
+        return p
+
     def route_align(self, logits: torch.Tensor, b: Buffers) -> None:
         moe_route_align(logits, self.top_k, self.renormalize, self.bs, b.ids, b.w, b.routing)
 
@@ -204,7 +224,7 @@ class MoeLayer:
         Returns the normed rows (``b.xn``), what the router and ``forward`` take; with fp8 weights the same
         launch quantises them into the buffers, and ``forward`` is called with ``x_quantized=True``."""
         y = torch.empty_like(b.out) if b.xn is None else b.xn
-        if b.xq is None or b.few is not None:  # the few-token form reads the bf16 rows
+        if b.xq is None or self.few_plan(b) is not None:  # the few-token form reads the bf16 rows
             moe_rmsnorm(x, weight, eps, residual=residual, y=y)
         else:
             first = b.pq is None
@@ -326,12 +346,9 @@ class MoeLayer:
             raise ValueError("x_quantized needs the buffers that norm_stage filled")
         if b is None:
             b = self.plan(x.shape[0], x.device)
-        if b.few is not None:
-            p = b.few
-            if p.gate is not self.gate or p.up is not self.up or p.down is not self.down:
-                p.use(self.gate, self.up, self.down)
-            p.renormalize = bool(self.renormalize)
-            return moe_few_tokens(p, logits, x, b.ids, b.w, b.out)[0]
+        few = self.few_plan(b)
+        if few is not None:
+            return moe_few_tokens(few, logits, x, b.ids, b.w, b.out)[0]
         self.route_align(logits, b)
         self.experts(x, b, row_adapter, x_quantized)
         return self.combine(b)

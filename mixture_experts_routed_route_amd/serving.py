@@ -252,7 +252,7 @@ _KINDS = ((Bf16Weight, MOE_W_BF16), (GptqWeight, MOE_W_INT4_GPTQ), (Fp8Weight, M
 def _unsupported(gate, up, down, top_k: int, num_tokens: int) -> Optional[str]:
     """Why ``moe_few_tokens`` does not take a layer, from its sizes and types alone (None: it does)."""
     E, I, H = gate.shape
-    ws = [MoeWeight(next(kind for c, kind in _KINDS if isinstance(w, c)), int(getattr(w, "group_size", 0)),
+    ws = [MoeWeight(next((kind for c, kind in _KINDS if isinstance(w, c)), -1), int(getattr(w, "group_size", 0)),
                     None, None, None) for w in (gate, up, down)]
     status = lib().moe_few_tokens_check(*[ctypes.byref(w) for w in ws], num_tokens, E, top_k, H, I)
     return None if status == MOE_OK else lib().moe_last_error().decode()

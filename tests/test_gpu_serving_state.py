@@ -117,3 +117,27 @@ def test_new_workspaces_serve_another_stream_at_once(m):
         side.synchronize()
         assert torch.equal(got, want)
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("weights", ["bf16", "int4_gptq"])
+def test_layers_share_buffers(m, weights):
+    """Layers of one size in turn on the buffers of the first, as a model's layers run: each the answer of its
+    own weights, renormalisation and path (the third has LoRA tables and runs its stages)."""
+    lora = dict(lora_rank=16, lora_max_rank=32)
+    made = []
+    for seed, few, kw in ((1, True, {}), (2, True, dict(renormalize=False)), (3, False, lora), (4, False, {})):
+        d = make_inputs(FEW.with_(weights=weights, seed=seed, **kw))
+        layer = m.MoeLayer.from_arrays(d, "cuda", few_tokens=few)
+        args = to_dev(d["logits"]), bf16_dev(d["x"])
+        made.append((layer, args, layer.forward(*args, layer.plan(FEW.T, "cuda")).clone()))
+    b = made[0][0].plan(FEW.T, "cuda")
+    rank = made[2][0].plan(FEW.T, "cuda")
+    b.xa = rank.xa                     # the LoRA scratch, which the first layer does not plan
+    small = made[0][0].plan(2, "cuda")
+    for _ in range(3):
+        for layer, args, want in made:
+            assert torch.equal(layer.forward(*args, b), want)
+        layer, args, _ = made[1]
+        got = layer.forward(args[0][:2].contiguous(), args[1][:2], small)
+        assert torch.equal(got, m.moe_few_tokens(m.few_tokens_plan(layer.gate, layer.up, layer.down, FEW.top_k, 2, False),
+                                                 args[0][:2].contiguous(), args[1][:2])[0])

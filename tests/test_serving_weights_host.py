@@ -100,13 +100,39 @@ def test_few_tokens_refuses_replacements_it_cannot_read(few):
 def test_layer_hands_replaced_weights_to_its_few_token_plan(few, monkeypatch):
     plan, _ = few
     layer = m.MoeLayer(E, H, I, K, 16, plan.gate, plan.up, plan.down, few_tokens=True)
-    b = m.layer.Buffers(3, None, None, None, None, None, None, None, None, few=plan)
+    b = m.layer.Buffers(3, None, None, None, None, None, None, None, None, few=plan, few_of=layer)
     monkeypatch.setattr(m.layer, "moe_few_tokens", lambda p, *a: (p,))
     assert layer.forward(None, None, b) is plan and plan.renormalize
     layer.down = m.Bf16Weight(bf(E, H, I))
     layer.renormalize = False
     layer.forward(None, None, b)
     assert plan.down is layer.down and plan.tensors[2][2] is layer.down.w and not plan.renormalize
+
+
+def test_layers_share_buffers(few, monkeypatch):
+    """Buffers that one layer planned, used by others of its size: each with its own weights and its own path."""
+    plan, _ = few
+
+    def layer(**kw):
+        return m.MoeLayer(E, H, I, K, 16, m.Bf16Weight(bf(E, I, H)), m.Bf16Weight(bf(E, I, H)), m.Bf16Weight(bf(E, H, I)), **kw)
+    first = m.MoeLayer(E, H, I, K, 16, plan.gate, plan.up, plan.down, few_tokens=True)
+    second, third, stages = layer(few_tokens=True), layer(few_tokens=True, renormalize=False), layer()
+    b = m.layer.Buffers(3, None, None, None, None, None, None, None, None, few=plan, few_of=first)
+    monkeypatch.setattr(m.layer, "moe_few_tokens", lambda p, *a: ((p.gate, p.up, p.down, p.renormalize, p.workspace),))
+    for _ in range(2):
+        for l in (first, second, third):
+            assert l.forward(None, None, b) == (l.gate, l.up, l.down, l.renormalize, plan.workspace)
+    assert b.few is plan is first.few_plan(b) and plan.gate is first.gate
+    kept = second.few_plan(b)
+    structs = kept.structs
+    other = m.layer.Buffers(2, None, None, None, None, None, None, None, None, few_of=first, few=m.serving.FewTokensPlan(
+        first.gate, first.up, first.down, E, H, I, K, 2, True, gpu(torch.zeros(8, dtype=torch.uint8))))
+    assert second.few_plan(other) is kept and kept.workspace is other.few.workspace and kept.max_tokens == 2
+    assert second.few_plan(b) is kept and kept.workspace is plan.workspace and kept.max_tokens == plan.max_tokens
+    assert kept.structs is structs                # checked once, not call by call
+    assert stages.few_plan(b) is None             # a layer that did not ask for the form (it may have LoRA tables)
+    second.down = m.Fp8Weight(torch.empty(1), torch.empty(1))
+    assert second.few_plan(b) is None             # nor one that the form does not take any more
 
 
 def test_gemm_fp8_block_refuses_weights_of_another_device(launches):
