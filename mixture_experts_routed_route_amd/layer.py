@@ -165,7 +165,9 @@ class MoeLayer:
                         lora_cap, fold, lora_gate, lora_up, gate_up_fused, down_fused, few_tokens, hs_codes)
 
     # ------------------------------------------------------------------ buffers
-    def plan(self, T: int, device) -> Buffers:
+    def plan(self, T: int, device, wait: bool = True) -> Buffers:
+        """Buffers for T tokens.  The workspaces' counters are filled when this returns, so that any stream may
+        make the first call; without ``wait``, the current one."""
         P = T * self.top_k
         r = Routing.allocate(P, self.top_k, self.E, self.bs, device)
         bf = dict(dtype=torch.bfloat16, device=device)
@@ -177,7 +179,7 @@ class MoeLayer:
         b = Buffers(T, torch.empty((T, self.top_k), dtype=torch.int32, device=device),
                     torch.empty((T, self.top_k), dtype=torch.float32, device=device), r,
                     torch.empty((0 if self.hs_codes else r.max_pad, self.I), **bf), torch.empty((r.max_pad, self.H), **bf),
-                    torch.empty((T, self.H), **bf), xa, gemm_workspace(device))
+                    torch.empty((T, self.H), **bf), xa, gemm_workspace(device, wait))
         if self.gate_up_lora and self.gate_up_fused:
             rank = max(t.max_rank for t in (self.lora_gate, self.lora_up) if t is not None)
             b.g = torch.empty((2, r.max_pad, rank), **bf)  # the two shrinks of the fused path
@@ -193,7 +195,7 @@ class MoeLayer:
             b.xq, b.sx = torch.empty((T, self.H), **u8), torch.empty((T, -(-self.H // FP8_BLOCK)), **f32)
             b.hq, b.sh = torch.empty((r.max_pad, self.I), **u8), torch.empty((r.max_pad, -(-self.I // FP8_BLOCK)), **f32)
         if self.few_tokens and T <= FEW_TOKENS and few_tokens_supported(self.gate, self.up, self.down, self.top_k, T):
-            b.few = few_tokens_plan(self.gate, self.up, self.down, self.top_k, T, self.renormalize)
+            b.few = few_tokens_plan(self.gate, self.up, self.down, self.top_k, T, self.renormalize, wait)
             b.few_of = self
         return b
 
@@ -345,7 +347,7 @@ class MoeLayer:
         if x_quantized and (b is None or b.xn is None):
             raise ValueError("x_quantized needs the buffers that norm_stage filled")
         if b is None:
-            b = self.plan(x.shape[0], x.device)
+            b = self.plan(x.shape[0], x.device, wait=False)  # used at once, on the current stream
         few = self.few_plan(b)
         if few is not None:
             return moe_few_tokens(few, logits, x, b.ids, b.w, b.out)[0]

@@ -63,11 +63,12 @@ def _dev(t: torch.Tensor, dtype: torch.dtype, name: str) -> int:
     return t.data_ptr()
 
 
-def _zeroed(nbytes: int, device) -> torch.Tensor:
+def _zeroed(nbytes: int, device, wait: bool = True) -> torch.Tensor:
     """Zeroed bytes for a workspace whose counters have to be zero at its first use, on whatever stream that
-    is: the fill has ended when this returns (in a graph capture it is recorded instead)."""
+    is: the fill has ended when this returns (in a graph capture it is recorded instead).  Without ``wait``
+    the first use has to be on the current stream."""
     t = torch.zeros(nbytes, dtype=torch.uint8, device=device)
-    if t.is_cuda:
+    if wait and t.is_cuda:
         with torch.cuda.device(t.device):
             if not torch.cuda.is_current_stream_capturing():
                 torch.cuda.current_stream().synchronize()
@@ -136,9 +137,10 @@ def align_workspace_bytes(num_pairs: int, num_experts: int) -> int:
     return int(lib().moe_align_workspace_bytes(num_pairs, num_experts))
 
 
-def gemm_workspace(device) -> torch.Tensor:
-    """A zero-filled workspace for moe_grouped_gemm's split-K tile balancing (calls leave it zeroed)."""
-    return _zeroed(int(lib().moe_grouped_gemm_workspace_bytes()), device)
+def gemm_workspace(device, wait: bool = True) -> torch.Tensor:
+    """A zero-filled workspace for moe_grouped_gemm's split-K tile balancing (calls leave it zeroed).  It is
+    filled when this returns, so that any stream may make the first call; without ``wait``, the current one."""
+    return _zeroed(int(lib().moe_grouped_gemm_workspace_bytes()), device, wait)
 
 
 def check_group_arrays(num_experts: int, per_expert: Sequence[Tuple[str, int]], offsets: Sequence[int]) -> None:

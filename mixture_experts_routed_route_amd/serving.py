@@ -267,10 +267,11 @@ def few_tokens_supported(gate, up, down, top_k: int, num_tokens: int = FEW_TOKEN
 
 
 def few_tokens_plan(gate, up, down, top_k: int, max_tokens: int = FEW_TOKENS,
-                    renormalize: bool = True) -> FewTokensPlan:
+                    renormalize: bool = True, wait: bool = True) -> FewTokensPlan:
     """Check the expert weights of a layer (gate and up ``[E, I, H]``, down ``[E, H, I]``; all bf16, GPTQ
     int4, fp8 with channel scales or fp8 with block scales) once and make the workspace for calls of up
-    to ``max_tokens`` tokens."""
+    to ``max_tokens`` tokens.  The workspace is filled when this returns, so that any stream may make the first
+    call; without ``wait``, the current one."""
     who = "few_tokens_plan"
     E, I, H = gate.shape
     _need(0 <= max_tokens <= FEW_TOKENS, f"{who}: max_tokens {max_tokens} not in [0, {FEW_TOKENS}]")
@@ -283,7 +284,7 @@ def few_tokens_plan(gate, up, down, top_k: int, max_tokens: int = FEW_TOKENS,
           f"{who}: the weights are on more than one device")
     n = int(lib().moe_few_tokens_workspace_bytes(max_tokens, E, top_k, H, I, structs[0].type))
     return FewTokensPlan(gate, up, down, E, H, I, top_k, max_tokens, bool(renormalize),
-                         _zeroed(n, device))
+                         _zeroed(n, device, wait))
 
 
 def moe_few_tokens(plan: FewTokensPlan, logits: torch.Tensor, x: torch.Tensor,

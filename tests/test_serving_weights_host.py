@@ -53,7 +53,7 @@ def launches(monkeypatch):
 @pytest.fixture
 def few(launches, monkeypatch):
     """A plan of bf16 weights and a call of it that gives the three data addresses."""
-    monkeypatch.setattr(serving, "_zeroed", lambda n, device: gpu(torch.zeros(n, dtype=torch.uint8)))
+    monkeypatch.setattr(serving, "_zeroed", lambda n, device, wait: gpu(torch.zeros(n, dtype=torch.uint8)))
     plan = m.few_tokens_plan(m.Bf16Weight(bf(E, I, H)), m.Bf16Weight(bf(E, I, H)), m.Bf16Weight(bf(E, H, I)), K, 4)
     args = (gpu(torch.empty((3, E))), bf(3, H), gpu(torch.empty((3, K), dtype=torch.int32)),
             gpu(torch.empty((3, K))), bf(3, H))
@@ -174,3 +174,17 @@ def test_workspaces_are_filled_before_any_stream_uses_them(monkeypatch, capturin
     monkeypatch.setattr(torch, "zeros", lambda n, **kw: filled(n, **kw) if kw.get("device") is not None else zeros(n, **kw))
     assert make().is_cuda
     assert log == (["fill"] if capturing else ["fill", "wait"])
+
+
+def test_forward_without_buffers_waits_for_nothing(monkeypatch):
+    """Its own buffers are used at once on the current stream, so it must not hold up the host."""
+    made = []
+    monkeypatch.setattr(m.layer, "gemm_workspace", lambda device, wait=True: made.append(wait))
+    monkeypatch.setattr(m.layer, "few_tokens_plan", lambda *a: made.append(a[-1]))
+    for name in ("route_align", "experts", "combine"):
+        monkeypatch.setattr(m.MoeLayer, name, lambda *a, **kw: None)
+    layer = m.MoeLayer(E, H, I, K, 16, m.Bf16Weight(bf(E, I, H)), m.Bf16Weight(bf(E, I, H)), m.Bf16Weight(bf(E, H, I)), few_tokens=True)
+    layer.forward(torch.zeros(3, E), torch.zeros(3, H, dtype=torch.bfloat16))
+    assert made == [False, False]
+    layer.plan(3, "cpu")
+    assert made == [False, False, True, True]
