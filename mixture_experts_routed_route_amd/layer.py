@@ -40,8 +40,9 @@ from .ops import (Bf16Weight, Fp8Weight, GptqWeight, LoraTables, Routing, gemm_w
                   moe_align, moe_combine, moe_grouped_gemm, moe_grouped_gemm_fp8, moe_lora_fold, moe_lora_gather_fold,
                   moe_quantize_fp8, moe_route, moe_route_align, moe_silu_mul, pack_lora_tables, stack_lora_tables,
                   moe_grouped_gemm_gate_up_lora, moe_grouped_gemm_down_lora)
-from .serving import (FEW_TOKENS, FP8_BLOCK, FewTokensPlan, Fp8BlockWeight, few_tokens_plan, few_tokens_supported,
-                      moe_few_tokens, moe_grouped_gemm_fp8_block, moe_quantize_fp8_block, moe_rmsnorm)
+from .serving import (FEW_TOKENS, FP8_BLOCK, FewTokensPlan, Fp8BlockWeight, few_tokens_fit, few_tokens_plan,
+                      few_tokens_supported, moe_few_tokens, moe_grouped_gemm_fp8_block, moe_quantize_fp8_block,
+                      moe_rmsnorm)
 
 FOLD_MODES = ("auto", "grouped", "gather")
 
@@ -206,15 +207,18 @@ class MoeLayer:
         if b.few is None or not self.few_tokens:
             return None
         p = b.few if b.few_of is self else self._few
-        if p is None or p.gate is not self.gate or p.up is not self.up or p.down is not self.down:
-            if not few_tokens_supported(self.gate, self.up, self.down, self.top_k, b.few.max_tokens):
+        ws, tokens = b.few.workspace, b.few.max_tokens
+        other = p is None or p.gate is not self.gate or p.up is not self.up or p.down is not self.down
+        if other or p.workspace is not ws:
+            if not few_tokens_fit(self.gate, self.up, self.down, self.top_k, tokens, ws):
                 return None
-            if p is not None:
-                p.use(self.gate, self.up, self.down)
-            else:
+            if p is None:
                 p = self._few = FewTokensPlan(self.gate, self.up, self.down, self.E, self.H, self.I, self.top_k,
-                                              b.few.max_tokens, bool(self.renormalize), b.few.workspace)
-        p.workspace, p.max_tokens, p.renormalize = b.few.workspace, b.few.max_tokens, bool(self.renormalize)
+                                              tokens, bool(self.renormalize), ws)
+            elif other:
+                p.use(self.gate, self.up, self.down)
+            p.workspace, p.max_tokens = ws, tokens
+        p.renormalize = bool(self.renormalize)
         return p
 
     def route_align(self, logits: torch.Tensor, b: Buffers) -> None:

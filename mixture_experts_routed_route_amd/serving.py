@@ -17,7 +17,7 @@ from ._lib import (MOE_OK, MOE_W_BF16, MOE_W_FP8, MOE_W_FP8_BLOCK, MOE_W_INT4_GP
 from .ops import Bf16Weight, Fp8Weight, GptqWeight, Routing, _check_gemm_shapes, _dev, _need, _numel_at_least, _zeroed
 
 __all__ = ["FP8_BLOCK", "FEW_TOKENS", "Fp8BlockWeight", "FewTokensPlan", "moe_rmsnorm", "moe_quantize_fp8_block",
-           "moe_grouped_gemm_fp8_block", "few_tokens_supported", "few_tokens_plan", "moe_few_tokens"]
+           "moe_grouped_gemm_fp8_block", "few_tokens_supported", "few_tokens_fit", "few_tokens_plan", "moe_few_tokens"]
 
 FP8_BLOCK = 128   # columns under one scale (weights: 128 x 128 blocks)
 FEW_TOKENS = 32   # most tokens of moe_few_tokens
@@ -249,11 +249,14 @@ _KINDS = ((Bf16Weight, MOE_W_BF16), (GptqWeight, MOE_W_INT4_GPTQ), (Fp8Weight, M
           (Fp8BlockWeight, MOE_W_FP8_BLOCK))
 
 
+def _kind(w) -> int:
+    return next((kind for c, kind in _KINDS if isinstance(w, c)), -1)
+
+
 def _unsupported(gate, up, down, top_k: int, num_tokens: int) -> Optional[str]:
     """Why ``moe_few_tokens`` does not take a layer, from its sizes and types alone (None: it does)."""
     E, I, H = gate.shape
-    ws = [MoeWeight(next((kind for c, kind in _KINDS if isinstance(w, c)), -1), int(getattr(w, "group_size", 0)),
-                    None, None, None) for w in (gate, up, down)]
+    ws = [MoeWeight(_kind(w), int(getattr(w, "group_size", 0)), None, None, None) for w in (gate, up, down)]
     status = lib().moe_few_tokens_check(*[ctypes.byref(w) for w in ws], num_tokens, E, top_k, H, I)
     return None if status == MOE_OK else lib().moe_last_error().decode()
 
@@ -264,6 +267,18 @@ def few_tokens_supported(gate, up, down, top_k: int, num_tokens: int = FEW_TOKEN
     another type or group size than gate and up, expert matrices of 2 GiB and more, more than 65536 hidden
     columns or 32 experts per token."""
     return _unsupported(gate, up, down, top_k, num_tokens) is None
+
+
+def _workspace_bytes(gate, top_k: int, num_tokens: int) -> int:
+    E, I, H = gate.shape
+    return int(lib().moe_few_tokens_workspace_bytes(num_tokens, E, top_k, H, I, _kind(gate)))
+
+
+def few_tokens_fit(gate, up, down, top_k: int, num_tokens: int, workspace: torch.Tensor) -> bool:
+    """Whether ``moe_few_tokens`` takes a layer of these weights with up to ``num_tokens`` tokens on another
+    layer's workspace (the weight types divide it differently)."""
+    return (few_tokens_supported(gate, up, down, top_k, num_tokens)
+            and _workspace_bytes(gate, top_k, num_tokens) <= workspace.numel())
 
 
 def few_tokens_plan(gate, up, down, top_k: int, max_tokens: int = FEW_TOKENS,
@@ -278,11 +293,12 @@ def few_tokens_plan(gate, up, down, top_k: int, max_tokens: int = FEW_TOKENS,
     _check_weights(gate, up, down, who)
     why = _unsupported(gate, up, down, top_k, max_tokens)
     _need(why is None, f"{who}: unsupported: {why}")
-    structs = tuple(w.struct() for w in (gate, up, down))
+    for w in (gate, up, down):
+        w.struct()                     # types and devices, before the workspace is made
     device = _weight_tensors(gate)[0].device
     _need(all(t.device == device for w in (gate, up, down) for t in _weight_tensors(w)),
           f"{who}: the weights are on more than one device")
-    n = int(lib().moe_few_tokens_workspace_bytes(max_tokens, E, top_k, H, I, structs[0].type))
+    n = _workspace_bytes(gate, top_k, max_tokens)
     return FewTokensPlan(gate, up, down, E, H, I, top_k, max_tokens, bool(renormalize),
                          _zeroed(n, device, wait))
 

@@ -126,11 +126,14 @@ def test_layers_share_buffers(few, monkeypatch):
     kept = second.few_plan(b)
     structs = kept.structs
     other = m.layer.Buffers(2, None, None, None, None, None, None, None, None, few_of=first, few=m.serving.FewTokensPlan(
-        first.gate, first.up, first.down, E, H, I, K, 2, True, gpu(torch.zeros(8, dtype=torch.uint8))))
+        first.gate, first.up, first.down, E, H, I, K, 2, True, gpu(torch.zeros(1 << 16, dtype=torch.uint8))))
     assert second.few_plan(other) is kept and kept.workspace is other.few.workspace and kept.max_tokens == 2
     assert second.few_plan(b) is kept and kept.workspace is plan.workspace and kept.max_tokens == plan.max_tokens
     assert kept.structs is structs                # checked once, not call by call
     assert stages.few_plan(b) is None             # a layer that did not ask for the form (it may have LoRA tables)
+    short = m.layer.Buffers(3, None, None, None, None, None, None, None, None, few_of=first, few=m.serving.FewTokensPlan(
+        first.gate, first.up, first.down, E, H, I, K, 3, True, gpu(torch.zeros(8200, dtype=torch.uint8))))
+    assert second.few_plan(short) is None and not m.few_tokens_fit(second.gate, second.up, second.down, K, 3, short.few.workspace)
     second.down = m.Fp8Weight(torch.empty(1), torch.empty(1))
     assert second.few_plan(b) is None             # nor one that the form does not take any more
 
