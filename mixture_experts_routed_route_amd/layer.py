@@ -65,8 +65,9 @@ class Buffers:
     hq: Optional[torch.Tensor] = None
     sh: Optional[torch.Tensor] = None
     xn: Optional[torch.Tensor] = None  # norm_stage's output (allocated by its first call)
+    coded: bool = False                # whether xq and sx hold the codes of the present xn
     pq: Optional[torch.Tensor] = None  # once norm_stage has run: where forward quantises an x of its own, so
-    ps: Optional[torch.Tensor] = None  # that xq and sx are always the codes of xn
+    ps: Optional[torch.Tensor] = None  # that xq and sx stay the codes of xn
     few: Optional[FewTokensPlan] = None  # few_tokens: the weights and workspace of the two-launch form
     few_of: Optional["MoeLayer"] = None  # the layer whose weights those are
 
@@ -230,7 +231,8 @@ class MoeLayer:
         Returns the normed rows (``b.xn``), what the router and ``forward`` take; with fp8 weights the same
         launch quantises them into the buffers, and ``forward`` is called with ``x_quantized=True``."""
         y = torch.empty_like(b.out) if b.xn is None else b.xn
-        if b.xq is None or self.few_plan(b) is not None:  # the few-token form reads the bf16 rows
+        codes = b.xq is not None and self.few_plan(b) is None  # (the few-token form reads the bf16 rows)
+        if not codes:
             moe_rmsnorm(x, weight, eps, residual=residual, y=y)
         else:
             first = b.pq is None
@@ -238,15 +240,15 @@ class MoeLayer:
             moe_rmsnorm(x, weight, eps, residual=residual, y=y, q=q, scale=scale[: b.T])
             if first:  # (graphs captured before this go on quantising into the buffers they know)
                 b.pq, b.ps, b.xq, b.sx = b.xq, b.sx, q, scale
-        b.xn = y
+        b.xn, b.coded = y, codes
         return y
 
     def _x_codes(self, x: torch.Tensor, b: Buffers, x_quantized: bool):
         """Codes and scales of x: quantised here, or norm_stage's (without a norm_stage, what the caller has
         put into the buffers)."""
         if x_quantized:
-            if b.xn is not None and (x.data_ptr() != b.xn.data_ptr() or x.shape != b.xn.shape):
-                raise ValueError("x_quantized: x is not norm_stage's output, whose codes the buffers hold")
+            if b.xn is not None and not (b.coded and x.data_ptr() == b.xn.data_ptr() and x.shape == b.xn.shape):
+                raise ValueError("x_quantized: x is not norm_stage's output, or was normed for a layer that reads no codes")
             return b.xq, b.sx
         q, scale = (b.xq, b.sx) if b.pq is None else (b.pq, b.ps)
         (moe_quantize_fp8_block if self.fp8_block else moe_quantize_fp8)(x, q, scale)

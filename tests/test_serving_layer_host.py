@@ -99,3 +99,22 @@ def test_a_refused_norm_leaves_the_buffers_without_codes(calls, monkeypatch):
     with pytest.raises(ValueError, match="norm_stage"):
         layer.forward(torch.zeros(T, E), bf(T, H), b, x_quantized=True)
     assert b.xn is None and b.pq is None
+
+
+def test_x_quantized_refuses_a_norm_without_codes(calls, monkeypatch):
+    """norm_stage of a layer that runs the two-launch form writes no codes: neither garbage nor an earlier
+    norm's codes may be read for its rows."""
+    form, stages = fp8_layer("fp8_block", few_tokens=True), fp8_layer("fp8_block")
+    monkeypatch.setattr(m.MoeLayer, "few_plan", lambda self, b: object() if self is form else None)
+    b = stages.plan(T, "cpu")
+    logits, nw = torch.zeros(T, E), bf(H)
+    y = form.norm_stage(bf(T, H) + 1, nw, b)
+    with pytest.raises(ValueError, match="no codes"):
+        stages.forward(logits, y, b, x_quantized=True)
+    y = stages.norm_stage(bf(T, H) + 2, nw, b)
+    stages.forward(logits, y, b, x_quantized=True)
+    y = form.norm_stage(bf(T, H) + 3, nw, b)
+    with pytest.raises(ValueError, match="no codes"):
+        stages.forward(logits, y, b, x_quantized=True)
+    stages.forward(logits, y, b)
+    assert calls == [2, 3]
