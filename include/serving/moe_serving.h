@@ -45,7 +45,8 @@ extern "C" {
  *                [rows, ceil(k/128)] (scale_block 128, what moe_grouped_gemm_fp8_block reads)
  * The norm is taken of the rounded h, the value that later layers read back, so that it can be
  * recomputed from residual_out bit for bit.  Sums of squares are fp32: a row whose sum of squares
- * passes the fp32 range comes out as zeros.  eps >= 0; with eps 0 a row of zeros gives NaN.
+ * passes the fp32 range comes out as zeros.  eps >= 0; with eps 0 a row of zeros gives NaN, and a row whose
+ * squares all underflow (|h| < 2^-75) infinities.
  * At least one of y_out and q.  k % 8 == 0, with q k % 16 == 0; k <= 2^20.  rows == 0 enqueues nothing. */
 moe_status moe_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps,
                        int64_t rows, int32_t k, uint16_t* residual_out, uint16_t* y_out, uint8_t* q, float* scale,

@@ -102,3 +102,20 @@ def test_row_scales_to_fp32(m, k):
     off = np.abs(s.cpu().numpy().astype(np.float64) - want) / want
     print(f"  k={k} worst {off.max() * 2 ** 24:.2f} of {depth / 2 + 8} steps of 2^-24", flush=True)
     assert (off <= (depth / 2 + 8) * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("k", [256, 4096, 16400])
+def test_norm_of_rows_at_the_ends_of_the_fp32_range(m, k):
+    """As the header states them: squares that pass fp32 give zeros, squares that underflow without eps give
+    infinities of h's sign (NaN where h is zero), and with eps the exact value."""
+    h = torch.full((3, k), 2.0 ** 70, device="cuda")
+    h[1] = 2.0 ** -80
+    h[1, ::2] *= -1
+    h[2] = 2.0 ** -80
+    h[2, 5] = 0.0
+    h, w = h.bfloat16(), torch.ones(k, dtype=torch.bfloat16, device="cuda")
+    y = m.moe_rmsnorm(h, w, 0.0)
+    assert (y[0] == 0).all() and torch.equal(y[1], torch.sign(h[1]) * float("inf"))
+    assert y[2, 5].isnan() and y[2].isinf().sum() == k - 1
+    y = m.moe_rmsnorm(h, w, 2.0 ** -20)
+    assert (y[0] == 0).all() and torch.equal(y[1:], h[1:] * 2.0 ** 10)
