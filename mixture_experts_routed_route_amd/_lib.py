@@ -1,5 +1,5 @@
-"""ctypes view of the C ABI in ``include/moe_mi355x.h``, ``include/moe_probes.h`` and
-``include/serving/moe_serving.h``
+"""ctypes view of the C ABI in ``include/moe_mi355x.h``, ``include/moe_probes.h``,
+``include/serving/moe_serving.h`` and ``include/training/moe_training.h``
 (``_lib/libmoe_mi355x.so``).
 
 No fallback: if the library is missing, loading raises and nothing runs.
@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_float, c_int32, c_int64, c_uint64, c_void_p
+from ctypes import POINTER, c_char_p, c_double, c_float, c_int32, c_int64, c_uint64, c_void_p
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libmoe_mi355x.so")
 
@@ -83,6 +83,23 @@ SERVING_SIGNATURES = {
 }
 
 
+# every symbol training/moe_training.h declares
+TRAINING_SIGNATURES = {
+    "moe_silu_mul_dropout": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int32, c_double,
+                                       c_void_p, c_void_p]),
+    "moe_silu_mul_backward": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int32,
+                                        c_double, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "moe_grouped_gemm_dgrad": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64,
+                                         c_int32, c_int32, c_int32, c_int32, c_int32, c_int64, c_int32, c_void_p,
+                                         c_int64, c_void_p]),
+    "moe_grouped_gemm_wgrad": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int64,
+                                         c_int32, c_int32, c_int32, c_int32, c_int32, c_int64, c_int32, c_int32,
+                                         c_void_p, c_int64, c_void_p]),
+    "moe_route_backward": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32, c_void_p,
+                                     c_void_p]),
+}
+
+
 class MoeWeight(ctypes.Structure):
     """struct moe_weight of the header."""
     _fields_ = [("type", c_int32), ("group_size", c_int32), ("data", c_void_p), ("scales", c_void_p),
@@ -99,7 +116,7 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"HIP library not built ({LIB_PATH}); run "
                                "`python -m mixture_experts_routed_route_amd.build`")
         L = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in {**SIGNATURES, **SERVING_SIGNATURES}.items():
+        for name, (res, args) in {**SIGNATURES, **SERVING_SIGNATURES, **TRAINING_SIGNATURES}.items():
             f = getattr(L, name)
             f.restype = res
             f.argtypes = args

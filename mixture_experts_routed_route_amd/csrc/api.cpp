@@ -3,6 +3,7 @@
 #include "../../include/moe_mi355x.h"
 #include "../../include/moe_probes.h"
 #include "../../include/serving/moe_serving.h"
+#include "../../include/training/moe_training.h"
 
 #include <hip/hip_runtime.h>
 
@@ -917,6 +918,168 @@ moe_status moe_few_tokens(const float* logits, const uint16_t* x, const moe_weig
     a.splits = l.splits;
     a.group = group;
     return launched(who, moe::launch_few_tokens(type, a, static_cast<hipStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ training operators (moe_training.h)
+namespace {
+
+// 16-bit random numbers below this drop their value
+uint32_t dropped_below(double p) {
+    const double v = p * 65536.0 + 0.5;
+    return v >= 65535.0 ? 65535u : static_cast<uint32_t>(v);
+}
+
+// sizes that every grouped gradient call shares
+moe_status check_grad(const char* who, int64_t num_pairs, int32_t top_k, int32_t num_experts, int32_t n, int32_t k,
+                      int32_t block_size, int64_t max_pad, const void* workspace, int64_t workspace_bytes) {
+    REQUIRE(num_pairs >= 0 && num_pairs < INT32_MAX, "%s: num_pairs out of range", who);
+    REQUIRE(top_k >= 1 && num_pairs % top_k == 0, "%s: num_pairs %lld is not a multiple of top_k %d", who,
+            static_cast<long long>(num_pairs), top_k);
+    REQUIRE(num_experts >= 1, "%s: num_experts %d < 1", who, num_experts);
+    if (num_experts > 256) return fail(MOE_EUNSUPPORTED, "%s: num_experts=%d > 256", who, num_experts);
+    REQUIRE(valid_block_size(block_size), "%s: block_size %d not in {16,32,64,128}", who, block_size);
+    REQUIRE(n >= 8 && n % 8 == 0, "%s: n %d must be a positive multiple of 8", who, n);
+    REQUIRE(k >= 8 && k % 8 == 0, "%s: k %d must be a positive multiple of 8", who, k);
+    if (n > (1 << 20) || k > (1 << 20)) return fail(MOE_EUNSUPPORTED, "%s: n %d or k %d above 2^20", who, n, k);
+    REQUIRE(max_pad >= max_padded(num_pairs, num_experts, block_size) && max_pad % block_size == 0 &&
+                max_pad < INT32_MAX,
+            "%s: max_pad %lld must be >= %lld and a multiple of block_size", who, static_cast<long long>(max_pad),
+            static_cast<long long>(max_padded(num_pairs, num_experts, block_size)));
+    if (workspace != nullptr) {
+        const int64_t need = moe_grouped_gemm_workspace_bytes();
+        REQUIRE_PTR(who, workspace);
+        REQUIRE(workspace_bytes >= need, "%s: workspace_bytes %lld < required %lld", who,
+                static_cast<long long>(workspace_bytes), static_cast<long long>(need));
+    }
+    return ok();
+}
+
+}  // namespace
+
+moe_status moe_silu_mul_dropout(const uint16_t* gate, const uint16_t* up, uint16_t* out, const int32_t* sorted_ids,
+                                int64_t num_pairs, int64_t rows, int32_t n, double p_drop, const int64_t* rng,
+                                moe_stream stream) {
+    const char* who = "moe_silu_mul_dropout";
+    REQUIRE(n >= 8 && n % 8 == 0, "%s: n %d must be a positive multiple of 8", who, n);
+    REQUIRE(rows >= 0 && rows < INT32_MAX, "%s: rows %lld out of range", who, static_cast<long long>(rows));
+    REQUIRE(num_pairs >= 0 && num_pairs < INT32_MAX, "%s: num_pairs out of range", who);
+    REQUIRE(p_drop >= 0.0 && p_drop < 1.0, "%s: p_drop %g not in [0, 1)", who, p_drop);
+    if (rows == 0 || (sorted_ids && num_pairs == 0)) return ok();
+    if (rows * (n / 8) > INT64_C(0xffffff00))
+        return fail(MOE_EUNSUPPORTED, "%s: rows %lld of %d columns exceed 2^35 values", who, static_cast<long long>(rows), n);
+    REQUIRE_PTR(who, gate);
+    REQUIRE_PTR(who, up);
+    REQUIRE_PTR(who, out);
+    if (sorted_ids) REQUIRE_PTR(who, sorted_ids);
+    const uint32_t below = dropped_below(p_drop);
+    if (below) REQUIRE_PTR(who, rng);
+    return launched(who, moe::launch_silu_mul_dropout(gate, up, out, sorted_ids, static_cast<int>(num_pairs), rows, n,
+                                                      below, rng, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_silu_mul_backward(const uint16_t* gate, const uint16_t* up, const uint16_t* d, const float* topk_w,
+                                 const int32_t* sorted_ids, int64_t num_pairs, int64_t rows, int32_t n,
+                                 double p_drop, const int64_t* rng, uint16_t* d_gate, uint16_t* d_up,
+                                 uint16_t* h_weighted, float* d_topk_w, moe_stream stream) {
+    const char* who = "moe_silu_mul_backward";
+    REQUIRE(n >= 8 && n % 8 == 0, "%s: n %d must be a positive multiple of 8", who, n);
+    REQUIRE(rows >= 0 && rows < INT32_MAX, "%s: rows %lld out of range", who, static_cast<long long>(rows));
+    REQUIRE(num_pairs >= 0 && num_pairs < INT32_MAX, "%s: num_pairs out of range", who);
+    REQUIRE(sorted_ids != nullptr || num_pairs >= rows, "%s: num_pairs %lld < rows %lld without sorted_ids", who,
+            static_cast<long long>(num_pairs), static_cast<long long>(rows));
+    REQUIRE(p_drop >= 0.0 && p_drop < 1.0, "%s: p_drop %g not in [0, 1)", who, p_drop);
+    if (rows == 0 || (sorted_ids && num_pairs == 0)) return ok();
+    if (rows >= (1 << 24)) return fail(MOE_EUNSUPPORTED, "%s: rows %lld >= 2^24", who, static_cast<long long>(rows));
+    REQUIRE(d_gate != d_up && d_gate != h_weighted && d_up != h_weighted, "%s: two outputs are one buffer", who);
+    REQUIRE_PTR(who, gate);
+    REQUIRE_PTR(who, up);
+    REQUIRE_PTR(who, d);
+    REQUIRE_PTR(who, topk_w);
+    REQUIRE_PTR(who, d_gate);
+    REQUIRE_PTR(who, d_up);
+    REQUIRE_PTR(who, h_weighted);
+    REQUIRE_PTR(who, d_topk_w);
+    if (sorted_ids) REQUIRE_PTR(who, sorted_ids);
+    const uint32_t below = dropped_below(p_drop);
+    if (below) REQUIRE_PTR(who, rng);
+    return launched(who, moe::launch_silu_mul_backward(gate, up, d, topk_w, sorted_ids, static_cast<int>(num_pairs), rows,
+                                                       n, below, rng, d_gate, d_up, h_weighted, d_topk_w,
+                                                       static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_grouped_gemm_dgrad(const uint16_t* dy0, const moe_weight* w0, const uint16_t* dy1, const moe_weight* w1,
+                                  uint16_t* dx, const int32_t* sorted_ids, const int32_t* expert_offsets,
+                                  int64_t num_pairs, int32_t top_k, int32_t num_experts, int32_t n, int32_t k,
+                                  int32_t block_size, int64_t max_pad, int32_t by_token, void* workspace,
+                                  int64_t workspace_bytes, moe_stream stream) {
+    const char* who = "moe_grouped_gemm_dgrad";
+    const moe_status st = check_grad(who, num_pairs, top_k, num_experts, n, k, block_size, max_pad, workspace, workspace_bytes);
+    if (st != MOE_OK) return st;
+    REQUIRE(w0 != nullptr, "%s: w0 is required", who);
+    REQUIRE((dy1 == nullptr) == (w1 == nullptr), "%s: dy1 and w1 go together", who);
+    if (w0->type != MOE_W_BF16 || (w1 && w1->type != MOE_W_BF16))
+        return fail(MOE_EUNSUPPORTED, "%s: gradients go through bf16 weights only", who);
+    if ((max_pad / 256 + num_experts) * ((k + 255) / 256) > (1 << 28))
+        return fail(MOE_EUNSUPPORTED, "%s: more than 2^28 tiles", who);
+    if (num_pairs == 0) return ok();
+    REQUIRE_PTR(who, dy0);
+    REQUIRE_PTR(who, dx);
+    REQUIRE_PTR(who, sorted_ids);
+    REQUIRE_PTR(who, expert_offsets);
+    REQUIRE_PTR(who, w0->data);
+    if (w1) {
+        REQUIRE_PTR(who, dy1);
+        REQUIRE_PTR(who, w1->data);
+    }
+    return launched(who, moe::launch_dgrad(dy0, static_cast<const uint16_t*>(w0->data), dy1,
+                                           w1 ? static_cast<const uint16_t*>(w1->data) : nullptr, dx, sorted_ids,
+                                           expert_offsets, static_cast<int>(num_pairs), top_k, num_experts, n, k,
+                                           static_cast<int>(max_pad), by_token ? 1 : 0, workspace, workspace_bytes,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_grouped_gemm_wgrad(const uint16_t* dy, const uint16_t* x, void* dw, const void* base, int32_t dw_fp32,
+                                  const int32_t* sorted_ids, const int32_t* expert_offsets, int64_t num_pairs,
+                                  int32_t top_k, int32_t num_experts, int32_t n, int32_t k, int32_t block_size,
+                                  int64_t max_pad, int32_t dy_by_token, int32_t x_by_token, void* workspace,
+                                  int64_t workspace_bytes, moe_stream stream) {
+    const char* who = "moe_grouped_gemm_wgrad";
+    const moe_status st = check_grad(who, num_pairs, top_k, num_experts, n, k, block_size, max_pad, workspace, workspace_bytes);
+    if (st != MOE_OK) return st;
+    if (static_cast<int64_t>(num_experts) * ((n + 255) / 256) * ((k + 255) / 256) > (1 << 28))
+        return fail(MOE_EUNSUPPORTED, "%s: more than 2^28 tiles", who);
+    REQUIRE_PTR(who, dw);
+    if (base) REQUIRE_PTR(who, base);
+    if (num_pairs > 0) {
+        REQUIRE_PTR(who, dy);
+        REQUIRE_PTR(who, x);
+        REQUIRE_PTR(who, sorted_ids);
+        REQUIRE_PTR(who, expert_offsets);
+    }
+    return launched(who, moe::launch_wgrad(dy, x, dw, base, dw_fp32 != 0, sorted_ids, expert_offsets,
+                                           static_cast<int>(num_pairs), top_k, num_experts, n, k,
+                                           static_cast<int>(max_pad), dy_by_token ? 1 : 0, x_by_token ? 1 : 0, workspace,
+                                           workspace_bytes, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_route_backward(const int32_t* topk_ids, const float* topk_w, const float* d_topk_w,
+                              const float* logits, int32_t num_tokens, int32_t num_experts, int32_t top_k,
+                              float* d_logits, moe_stream stream) {
+    const char* who = "moe_route_backward";
+    REQUIRE(num_tokens >= 0, "%s: num_tokens %d is negative", who, num_tokens);
+    REQUIRE(num_experts >= 1, "%s: num_experts %d < 1", who, num_experts);
+    REQUIRE(top_k >= 1, "%s: top_k %d < 1", who, top_k);
+    if (num_experts > 256 || top_k > 256)
+        return fail(MOE_EUNSUPPORTED, "%s: num_experts=%d or top_k=%d > 256", who, num_experts, top_k);
+    if (num_tokens > (1 << 25)) return fail(MOE_EUNSUPPORTED, "%s: num_tokens %d > 2^25", who, num_tokens);
+    if (num_tokens == 0) return ok();
+    REQUIRE_PTR(who, topk_ids);
+    REQUIRE_PTR(who, topk_w);
+    REQUIRE_PTR(who, d_topk_w);
+    REQUIRE_PTR(who, d_logits);
+    if (logits) REQUIRE_PTR(who, logits);
+    return launched(who, moe::launch_route_backward(topk_ids, topk_w, d_topk_w, logits, num_tokens, num_experts, top_k,
+                                                    d_logits, static_cast<hipStream_t>(stream)));
 }
 
 // ------------------------------------------------------------------ ceiling probes (moe_probes.h)

@@ -107,6 +107,24 @@ hipError_t launch_rmsnorm(const uint16_t* x, const uint16_t* r, const uint16_t* 
 hipError_t launch_quantize_fp8_block(const uint16_t* x, int64_t rows, int K, const int32_t* sorted_ids, int P,
                                      uint8_t* q, float* scale, hipStream_t s);
 
+// grad_rows.hip: SiLU(g) * u with dropout (values whose 16 random bits lie below `below` are dropped), its
+// backward with the router weight, and the gradient of the router's logits (logits NULL: renormalised weights)
+hipError_t launch_silu_mul_dropout(const uint16_t* g, const uint16_t* u, uint16_t* h, const int32_t* sorted_ids, int P,
+                                   int64_t rows, int N, uint32_t below, const int64_t* rng, hipStream_t s);
+hipError_t launch_silu_mul_backward(const uint16_t* g, const uint16_t* u, const uint16_t* d, const float* w,
+                                    const int32_t* sorted_ids, int P, int64_t rows, int N, uint32_t below,
+                                    const int64_t* rng, uint16_t* dg, uint16_t* du, uint16_t* hw, float* dw,
+                                    hipStream_t s);
+hipError_t launch_route_backward(const int32_t* ids, const float* w, const float* dw, const float* logits, int T, int E,
+                                 int k, float* out, hipStream_t s);
+// grad_gemm.hip: grouped products for the gradients of inputs (dy1 NULL: one pair) and of weights
+hipError_t launch_dgrad(const uint16_t* dy0, const uint16_t* w0, const uint16_t* dy1, const uint16_t* w1, uint16_t* dx,
+                        const int32_t* sorted_ids, const int32_t* offsets, int P, int top_k, int E, int N, int K,
+                        int max_pad, int by_token, void* ws, int64_t ws_bytes, hipStream_t s);
+hipError_t launch_wgrad(const uint16_t* dy, const uint16_t* x, void* dw, const void* base, bool f32,
+                        const int32_t* sorted_ids, const int32_t* offsets, int P, int top_k, int E, int N, int K,
+                        int max_pad, int dy_by_token, int x_by_token, void* ws, int64_t ws_bytes, hipStream_t s);
+
 // probes.hip (ceiling probes, not steps of the path)
 hipError_t launch_probe_stream_read(const void* src, int64_t bytes, uint32_t* sink, int blocks, hipStream_t s);
 hipError_t launch_probe_mfma_bf16(int64_t iters, float* sink, int blocks, hipStream_t s);

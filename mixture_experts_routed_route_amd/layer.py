@@ -26,11 +26,18 @@ two launches of ``moe_few_tokens`` instead of the stages above, where it takes t
 
 Buffers are allocated once per token count (``plan``) so a forward pass allocates
 nothing and its launch grids depend on host scalars only.
+
+For training (bf16 weights) ``train_plan``, ``train_forward`` and ``train_backward`` chain
+
+    moe_route -> moe_align -> moe_grouped_gemm(gather, gate) and (gather, up) -> moe_silu_mul_dropout
+              -> moe_grouped_gemm(down) -> moe_combine
+    moe_grouped_gemm_dgrad(down) -> moe_silu_mul_backward -> moe_grouped_gemm_wgrad (down, gate, up)
+              -> moe_grouped_gemm_dgrad(gate and up) -> moe_combine; moe_route_backward
 """
 from __future__ import annotations
 
 from dataclasses import dataclass
-from typing import Dict, Optional
+from typing import Dict, Optional, Tuple
 
 import numpy as np
 import torch
@@ -43,6 +50,8 @@ from .ops import (Bf16Weight, Fp8Weight, GptqWeight, LoraTables, Routing, gemm_w
 from .serving import (FEW_TOKENS, FP8_BLOCK, FewTokensPlan, Fp8BlockWeight, few_tokens_fit, few_tokens_plan,
                       few_tokens_supported, moe_few_tokens, moe_grouped_gemm_fp8_block, moe_quantize_fp8_block,
                       moe_rmsnorm)
+from .training import (moe_grouped_gemm_dgrad, moe_grouped_gemm_wgrad, moe_route_backward, moe_silu_mul_backward,
+                       moe_silu_mul_dropout)
 
 FOLD_MODES = ("auto", "grouped", "gather")
 
@@ -70,6 +79,29 @@ class Buffers:
     ps: Optional[torch.Tensor] = None  # that xq and sx stay the codes of xn
     few: Optional[FewTokensPlan] = None  # few_tokens: the weights and workspace of the two-launch form
     few_of: Optional["MoeLayer"] = None  # the layer whose weights those are
+
+
+@dataclass
+class TrainBuffers:
+    """What a training step keeps between ``train_forward`` and ``train_backward``, and its scratch."""
+    T: int
+    dropout: float
+    rng: torch.Tensor      # int64 [2]: seed and offset of the dropout masks; a step's backward has to find what its
+                           # forward found, and the next forward another offset (``rng[1] += 1``)
+    ids: torch.Tensor
+    w: torch.Tensor
+    routing: Routing
+    g: torch.Tensor        # gate and up outputs; the backward replaces them by their gradients
+    u: torch.Tensor
+    h: torch.Tensor        # hidden activations; in the backward their gradient, then the weighted ones
+    ys: torch.Tensor       # expert outputs; in the backward the pairs' gradients of x
+    out: torch.Tensor
+    d_x: torch.Tensor
+    d_w: torch.Tensor
+    d_logits: torch.Tensor
+    ones: torch.Tensor     # weights of the sum of the pairs' gradients of x
+    ws: torch.Tensor
+    forward_done: bool = False
 
 
 class MoeLayer:
@@ -360,3 +392,77 @@ class MoeLayer:
         self.route_align(logits, b)
         self.experts(x, b, row_adapter, x_quantized)
         return self.combine(b)
+
+    # ------------------------------------------------------------------ training
+    def train_plan(self, T: int, device, dropout: float = 0.0, seed: int = 0, wait: bool = True) -> TrainBuffers:
+        """Buffers of a training step of T tokens: one forward and its backward at a time.  ``dropout``: the
+        probability that a hidden activation (SiLU(gate) * up) is dropped.  ``wait``: as for ``plan``."""
+        if not all(isinstance(w, Bf16Weight) for w in (self.gate, self.up, self.down)):
+            raise ValueError("training needs bf16 expert weights")
+        if self._tables():
+            raise ValueError("training does not take LoRA tables")
+        if not 0.0 <= dropout < 1.0:
+            raise ValueError(f"dropout is {dropout}; needs [0, 1)")
+        r = Routing.allocate(T * self.top_k, self.top_k, self.E, self.bs, device)
+        bf, f32 = dict(dtype=torch.bfloat16, device=device), dict(dtype=torch.float32, device=device)
+        rows = lambda n: torch.empty((r.max_pad, n), **bf)
+        b = TrainBuffers(T, float(dropout), torch.tensor([seed, 0], dtype=torch.int64, device=device),
+                         torch.empty((T, self.top_k), dtype=torch.int32, device=device), torch.empty((T, self.top_k), **f32),
+                         r, rows(self.I), rows(self.I), rows(self.I), rows(self.H), torch.empty((T, self.H), **bf),
+                         torch.empty((T, self.H), **bf), torch.empty((T, self.top_k), **f32),
+                         torch.empty((T, self.E), **f32), torch.ones((T, self.top_k), **f32), gemm_workspace(device, False))
+        if wait and b.ws.is_cuda:  # rng, ones and the workspace are filled
+            with torch.cuda.device(b.ws.device):
+                if not torch.cuda.is_current_stream_capturing():
+                    torch.cuda.current_stream().synchronize()
+        return b
+
+    def train_forward(self, logits: torch.Tensor, x: torch.Tensor, b: TrainBuffers) -> torch.Tensor:
+        """The layer's output (``b.out``) for x [T, H], keeping in the buffers what ``train_backward`` needs.
+        Gate and up are rounded to bf16 before SiLU * up, as on the gate/up LoRA path."""
+        b.forward_done = False
+        moe_route_align(logits, self.top_k, self.renormalize, self.bs, b.ids, b.w, b.routing)
+        moe_grouped_gemm(MOE_OP_GATHER, x, self.gate, None, b.routing, out=b.g, workspace=b.ws)
+        moe_grouped_gemm(MOE_OP_GATHER, x, self.up, None, b.routing, out=b.u, workspace=b.ws)
+        moe_silu_mul_dropout(b.g, b.u, b.routing, b.dropout, b.rng, out=b.h)
+        moe_grouped_gemm(MOE_OP_DOWN, b.h, self.down, None, b.routing, out=b.ys, workspace=b.ws)
+        moe_combine(b.ys, b.routing.inv_sorted, b.w, out=b.out)
+        b.forward_done = True
+        return b.out
+
+    def train_backward(self, d_out: torch.Tensor, x: torch.Tensor, b: TrainBuffers,
+                       logits: Optional[torch.Tensor] = None, grads: Optional[Tuple[torch.Tensor, ...]] = None,
+                       accumulate: bool = False):
+        """Gradients from that of the layer's output, ``d_out`` [T, H] bf16, after ``train_forward`` of the same x
+        on the same buffers (once: it replaces what the forward kept).  A layer that does not renormalise its
+        routing weights needs the ``logits`` again.
+
+        Returns (d_x [T, H] bf16 and d_logits [T, E] fp32, of the buffers, and (d_gate, d_up, d_down)).
+        ``grads``: where the weight gradients go, bf16 or fp32 [E, I, H], [E, I, H] and [E, H, I] (allocated
+        in bf16 without); with ``accumulate`` they are added to what is there."""
+        if not b.forward_done:
+            raise ValueError("train_backward needs a train_forward on these buffers, once for each backward")
+        if not self.renormalize and logits is None:
+            raise ValueError("train_backward: without renormalised routing weights the logits are needed")
+        if accumulate and grads is None:
+            raise ValueError("train_backward: accumulate needs grads")
+        if d_out.shape != b.out.shape or x.shape != b.out.shape:
+            raise ValueError(f"train_backward: d_out is {tuple(d_out.shape)} and x {tuple(x.shape)}; need {tuple(b.out.shape)}")
+        if grads is None:
+            grads = tuple(torch.empty_like(w.w) for w in (self.gate, self.up, self.down))
+        dg, du, dd = grads
+        base = lambda t: t if accumulate else None
+        r = b.routing
+        b.forward_done = False
+        # d_out Wd by sorted row, before the routing weights
+        moe_grouped_gemm_dgrad(d_out, self.down, r, by_token=True, out=b.h, workspace=b.ws)
+        b.d_w.zero_()  # pairs without an expert have no row that would write theirs
+        moe_silu_mul_backward(b.g, b.u, b.h, b.w, r, b.dropout, b.rng, d_gate=b.g, d_up=b.u, h_weighted=b.h,
+                              d_topk_w=b.d_w)
+        moe_grouped_gemm_wgrad(d_out, b.h, r, dy_by_token=True, base=base(dd), out=dd, workspace=b.ws)
+        moe_grouped_gemm_wgrad(b.g, x, r, x_by_token=True, base=base(dg), out=dg, workspace=b.ws)
+        moe_grouped_gemm_wgrad(b.u, x, r, x_by_token=True, base=base(du), out=du, workspace=b.ws)
+        moe_grouped_gemm_dgrad(b.g, self.gate, r, dy1=b.u, w1=self.up, out=b.ys, workspace=b.ws)
+        moe_combine(b.ys, r.inv_sorted, b.ones, out=b.d_x)
+        moe_route_backward(b.ids, b.w, b.d_w, self.E, None if self.renormalize else logits, out=b.d_logits)
+        return b.d_x, b.d_logits, (dg, du, dd)
