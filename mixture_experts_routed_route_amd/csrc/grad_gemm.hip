@@ -31,12 +31,15 @@ namespace moe {
 namespace {
 
 constexpr int kTile = 256;     // output rows and columns of a tile
-constexpr int kBK = 64;        // contraction per stage
+constexpr int kBK = 32;        // contraction per LDS slot (a "half")
+constexpr int kSlots = 4;
 constexpr int kNT = 512;
-constexpr int kPart = kTile * kBK;      // elements of one operand's stage
-constexpr int kStage = 2 * kPart;
+constexpr int kPartB = kTile * kBK * 2;  // bytes of one operand in a slot
+constexpr int kSlotB = 2 * kPartB;
 constexpr int kMaxE = 256;
 constexpr int kBand = 8;       // row tiles per band of the tile order
+constexpr int kTab = 128;      // entries of a workgroup's list that are located in advance
+constexpr int kSegs = 8;       // dgrad: tiles whose row ids are held
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -64,14 +67,24 @@ struct GradArgs {
     int r_tok, c_tok;     // operand rows by token
 };
 
+struct Seg {
+    int e, r0, r_end;   // dgrad: expert, first sorted row, end of rows; wgrad: expert, its span
+    int row0, col0;     // first output row (wgrad: of N) and column
+    int nh;             // halves
+};
+enum { kEnd, kSkip, kIsTile };
+
 // DGRAD: bf16 out; else wgrad with bf16 (F32 false) or fp32 results
 template <bool DGRAD, bool F32>
 __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
-    __shared__ __attribute__((aligned(1024))) uint16_t smem[2 * kStage];
+    __shared__ __attribute__((aligned(1024))) char smem[kSlots * kSlotB];
     __shared__ int s_lo[kMaxE], s_hi[kMaxE], s_tb[kMaxE + 1], s_order[kMaxE];
     __shared__ int s_scan[kNT / 64];
-    __shared__ __attribute__((aligned(16))) int s_id[2][kTile];    // dgrad: sorted ids of the tile's rows; wgrad: of its first two stages
-    __shared__ __attribute__((aligned(16))) int s_ring[2][kBK];    // wgrad: sorted ids of stages 2, 3, ...
+    __shared__ int4 s_tab[kTab], s_tab2[kTab];
+    // sorted ids.  dgrad: of the rows of the last kSegs tiles.  wgrad: per wave, of its rows (4 per half) of 16 halves, twice
+    __shared__ __attribute__((aligned(16))) int s_id[DGRAD ? kSegs * kTile : kNT / 64 * 2 * 64];
+    // wgrad: per wave, the rows' addresses in the two operands (the zeros' where a row holds no pair)
+    __shared__ ulonglong2 s_ptr[DGRAD ? 1 : kNT];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -124,120 +137,255 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     const int units = E * units_e;
     const int l_n = DGRAD ? static_cast<int>(T * (xcd + 1) / 8) - l_lo : (units + 7) / 8 * unit;
 
-    struct Seg {
-        int e, r0, r_end;   // dgrad: expert, first sorted row, end of rows; wgrad: expert, its span
-        int row0, col0;     // first output row (wgrad: of N) and column
-        int nst;            // stages
+    const int nkh = (N + kBK - 1) / kBK;             // dgrad: halves of one pair
+    // entry number n of this workgroup: kTile, kSkip (no tile) or kEnd
+    auto locate = [&](int n, Seg& s) __attribute__((always_inline)) -> int {
+        const int i = slot + n * per_xcd;
+        if (i >= l_n) return kEnd;
+        int idx, m_lim, e = 0;
+        if constexpr (DGRAD) {
+            idx = l_lo + i;
+            m_lim = m_real;
+        } else {
+            const int v = i / unit;
+            const int u = v * 8 + ((v & 1) ? 7 - xcd : xcd);
+            idx = (u % units_e) * unit + i % unit;
+            if (u >= units || idx >= tiles_e) return kSkip;
+            m_lim = r_tiles;
+            e = s_order[u / units_e];
+        }
+        // bands of kBand row tiles, row tiles fastest: tiles that run together share operands in L2
+        const int band = idx / (kBand * n_tiles);
+        const int at = idx - band * kBand * n_tiles;
+        const int rows = min(kBand, m_lim - band * kBand);
+        const int n_t = at / rows;
+        const int m_t = band * kBand + at - n_t * rows;
+        s.col0 = n_t * kTile;
+        if constexpr (DGRAD) {
+            int hi = E - 1;  // e: the largest expert whose first row tile is <= m_t
+            while (e < hi) {
+                const int mid = (e + hi + 1) >> 1;
+                if (s_tb[mid] <= m_t) e = mid; else hi = mid - 1;
+            }
+            s.r0 = s_lo[e] + (m_t - s_tb[e]) * kTile;
+            s.r_end = min(s.r0 + kTile, s_hi[e]);
+            s.row0 = 0;
+            s.nh = g.r1 ? 2 * nkh : nkh;
+        } else {
+            s.row0 = m_t * kTile;
+            s.r0 = s_lo[e];
+            s.r_end = s_hi[e];
+            s.nh = (s.r_end - s.r0 + kBK - 1) / kBK;
+        }
+        s.e = e;
+        return kIsTile;
     };
-    const int nk = (N + kBK - 1) / kBK;              // dgrad: stages of one pair
-    // the next entry at or after i that is a tile; false: none
-    auto locate = [&](int& i, Seg& s) __attribute__((always_inline)) -> bool {
-        for (;; i += per_xcd) {
-            if (i >= l_n) return false;
-            int idx, m_lim, m_t, n_t;
-            if constexpr (DGRAD) {
-                idx = l_lo + i;
-                m_lim = m_real;
+    // the first entries, located once by a thread each (a dependent chain of divisions and searches)
+    if (tid < kTab) {
+        Seg s = {};
+        const int is_tile = locate(tid, s);
+        s_tab[tid] = int4{is_tile, s.e, s.r0, s.r_end};
+        s_tab2[tid] = int4{s.row0, s.col0, s.nh, 0};
+    }
+    __syncthreads();
+    // the next tile at or after entry n; false: none.  n moves past it.
+    auto find = [&](int& n, Seg& s) __attribute__((always_inline)) -> bool {
+        for (;;) {
+            int is_tile;
+            if (n < kTab) {
+                const int4 a = s_tab[n], b = s_tab2[n];
+                is_tile = a.x;
+                s = Seg{a.y, a.z, a.w, b.x, b.y, b.z};
             } else {
-                const int v = i / unit;
-                const int u = v * 8 + ((v & 1) ? 7 - xcd : xcd);
-                if (u >= units) continue;
-                idx = (u % units_e) * unit + i % unit;
-                if (idx >= tiles_e) continue;
-                m_lim = r_tiles;
-                s.e = __builtin_amdgcn_readfirstlane(s_order[u / units_e]);
+                is_tile = locate(n, s);
             }
-            // bands of kBand row tiles, row tiles fastest: tiles that run together share operands in L2
-            const int band = idx / (kBand * n_tiles);
-            const int in = idx - band * kBand * n_tiles;
-            const int rows = min(kBand, m_lim - band * kBand);
-            n_t = in / rows;
-            m_t = band * kBand + in - n_t * rows;
-            s.col0 = n_t * kTile;
-            if constexpr (DGRAD) {
-                int a = 0, b = E - 1;  // largest expert whose first row tile is <= m_t
-                while (a < b) {
-                    const int mid = (a + b + 1) >> 1;
-                    if (s_tb[mid] <= m_t) a = mid; else b = mid - 1;
-                }
-                s.e = __builtin_amdgcn_readfirstlane(a);
-                s.r0 = __builtin_amdgcn_readfirstlane(s_lo[s.e] + (m_t - s_tb[s.e]) * kTile);
-                s.r_end = __builtin_amdgcn_readfirstlane(min(s.r0 + kTile, s_hi[s.e]));
-                s.row0 = 0;
-                s.nst = g.r1 ? 2 * nk : nk;
-            } else {
-                s.row0 = m_t * kTile;
-                s.r0 = __builtin_amdgcn_readfirstlane(s_lo[s.e]);
-                s.r_end = __builtin_amdgcn_readfirstlane(s_hi[s.e]);
-                s.nst = (s.r_end - s.r0 + kBK - 1) / kBK;
-            }
-            return true;
+            is_tile = __builtin_amdgcn_readfirstlane(is_tile);
+            s.e = __builtin_amdgcn_readfirstlane(s.e);
+            s.r0 = __builtin_amdgcn_readfirstlane(s.r0);
+            s.r_end = __builtin_amdgcn_readfirstlane(s.r_end);
+            s.row0 = __builtin_amdgcn_readfirstlane(s.row0);
+            s.col0 = __builtin_amdgcn_readfirstlane(s.col0);
+            s.nh = __builtin_amdgcn_readfirstlane(s.nh);
+            if (is_tile == kEnd) return false;
+            ++n;
+            if (is_tile == kIsTile) return true;
         }
     };
 
-    int L = slot;
-    Seg cur;
-    if (!locate(L, cur)) return;
-
-    const uint32_t lds0 = lds_u32(smem);
-    // sorted ids of 64 rows from r into LDS (rows past max_pad read the last one; checked where used)
-    auto load_ids = [&](int r, const int* dst) __attribute__((always_inline)) {
-        dma4(g.sorted_ids + min(r + lane, g.max_pad - 1), lds_u32(dst));
-    };
-    // those a segment needs before its first stage's loads: by the waves that hold them
-    auto first_ids = [&](const Seg& s, int b) __attribute__((always_inline)) {
-        constexpr int W = DGRAD ? kTile / 64 : 2;
-        if (wave < W) load_ids(s.r0 + wave * 64, s_id[b] + wave * 64);
-    };
+    const uint32_t lds0 = lds_u32(smem), lds_id = lds_u32(s_id);
+    const char* zero = reinterpret_cast<const char*>(kZero16);
+    const int half = lane >> 5;
     // row of an operand for sorted row r with id p; < 0: no pair
     auto source = [&](int p, int r, int r_end, int tok) __attribute__((always_inline)) {
         return r < r_end && p >= 0 && p < g.P ? (tok ? fast_div(p, g.top_k) : r) : -1;
     };
 
-    // ---- loads of stage t of a segment into LDS buffer b: 8 waves x 8 instructions of 1 KB
-    auto issue = [&](const Seg& s, int sbuf, int t, int b) __attribute__((always_inline)) {
-        const uint32_t dst_r = lds0 + b * (kStage * 2) + wave * 4096, dst_c = dst_r + kPart * 2;
-        const int half = lane >> 5;
-        const char* zero = reinterpret_cast<const char*>(kZero16);
-        if constexpr (DGRAD) {
-            const bool second = t >= nk;
-            const int k0 = (second ? t - nk : t) * kBK;
-            const uint16_t* R = second ? g.r1 : g.r0;
-            const uint16_t* C = (second ? g.c1 : g.c0) + static_cast<size_t>(s.e) * N * K;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {   // dy: 8 tile rows of 128 bytes
-                const int row = wave * 32 + q * 8 + (lane >> 3);
-                const int src = source(s_id[sbuf][row], s.r0 + row, s.r_end, g.r_tok);
-                const size_t at = src >= 0 ? src : (g.r_tok ? 0 : s.r0);
-                const int n = k0 + (((lane & 7) ^ ((row >> 1) & 7)) << 3);
-                dma16(n < N ? reinterpret_cast<const char*>(R + at * N + n) : zero, dst_r + q * 1024);
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {   // W: 2 contraction rows of 512 bytes
-                const int row = wave * 8 + q * 2 + half;
-                const int chunk = (lane & 31) ^ (((row & 3) << 2) | (((row >> 3) & 1) << 1));
-                const int col = min(s.col0 + chunk * 8, K - 8);  // columns past K are never stored
-                const int n = k0 + row;
-                dma16(n < N ? reinterpret_cast<const char*>(C + static_cast<size_t>(n) * K + col) : zero, dst_c + q * 1024);
-            }
-        } else {
-            const int* ids = t < 2 ? s_id[sbuf] + t * kBK : s_ring[t & 1];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int row = wave * 8 + q * 2 + half;
-                const int chunk = (lane & 31) ^ (((row & 3) << 2) | (((row >> 3) & 1) << 1));
-                const int r = s.r0 + t * kBK + row, p = ids[row];
-                const int ry = source(p, r, s.r_end, g.r_tok), rx = source(p, r, s.r_end, g.c_tok);
-                const int n = min(s.row0 + chunk * 8, N - 8), k = min(s.col0 + chunk * 8, K - 8);
-                dma16(ry >= 0 ? reinterpret_cast<const char*>(g.r0 + static_cast<size_t>(ry) * N + n) : zero, dst_r + q * 1024);
-                dma16(rx >= 0 ? reinterpret_cast<const char*>(g.c0 + static_cast<size_t>(rx) * K + k) : zero, dst_c + q * 1024);
-            }
+    // ---- the issuing cursor, 3 or 4 halves ahead of the one that is computed.  i_left halves can be issued before
+    // the cursor has to be moved (move()): to the half that ends past N and to the second pair (dgrad), to the next 16
+    // ids (wgrad), to the next segment, and behind the last one to halves of zeros that nobody reads, so that the main
+    // loop needs no tests.
+    int i_n = 0, i_seq = 0, i_h = 0, i_left = 0, i_since = 0, i_slot = 0, id_par = 1;
+    Seg is, in;                 // the segment whose halves are loaded, and the next one with any
+    bool i_next;
+    auto next_seg = [&](Seg& s) __attribute__((always_inline)) -> bool {
+        for (;;) {
+            if (!find(i_n, s)) return false;
+            if (s.nh > 0) return true;
         }
     };
+    // Ids that this wave's loads need, straight into LDS (rows past max_pad read the last id; checked where
+    // used).  dgrad: the wave's 32 rows of tile number seq.  wgrad: its 4 rows of each of 16 halves.
+    auto load_ids = [&](const Seg& s, int batch, int seq, int par) __attribute__((always_inline)) {
+        if constexpr (DGRAD) {
+            if (lane < 32)
+                dma4(g.sorted_ids + min(s.r0 + wave * 32 + lane, g.max_pad - 1),
+                     lds_id + ((seq & (kSegs - 1)) * kTile + wave * 32) * 4);
+        } else {
+            const int r = s.r0 + (batch * 16 + (lane >> 2)) * kBK + wave * 4 + (lane & 3);
+            dma4(g.sorted_ids + min(r, g.max_pad - 1), lds_id + (wave * 2 + par) * 256);
+        }
+    };
+    // this lane's sources, loads q of each operand.  dgrad: of the coming half, and how far to the next.  wgrad: the
+    // bytes from a row's start.
+    const char* rp[2];
+    const char* cp[2];
+    uint32_t step_r = 0;
+    uint64_t step_c = 0;
+    int at[2], chunk_c[2], col_r[2], col_c[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) chunk_c[q] = ((lane & 31) ^ (((q * 2 + half) << 2) | (((wave >> 1) & 1) << 1))) * 8;
+    const int k_r = ((lane & 3) ^ ((lane >> 4) & 3)) * 8;   // dgrad: first n of this lane's chunk of a row of dy
+    const ulonglong2* row_p = s_ptr;   // wgrad: the row addresses of the coming half
+    auto move = [&]() {
+        if constexpr (DGRAD) {
+            if (i_h == nkh || i_h == 0) {           // a pair begins
+                const uint16_t* R = i_h ? g.r1 : g.r0;
+                const uint16_t* C = i_h ? g.c1 : g.c0;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    rp[q] = reinterpret_cast<const char*>(R + static_cast<size_t>(at[q]) * N + k_r);
+                    cp[q] = reinterpret_cast<const char*>(C + (static_cast<size_t>(is.e) * N + wave * 4 + q * 2 + half) * K +
+                                                          min(is.col0 + chunk_c[q], K - 8));  // columns past K are never stored
+                }
+                step_r = kBK * 2;
+                step_c = static_cast<uint64_t>(kBK * 2) * K;
+            }
+            const int h = i_h >= nkh ? i_h - nkh : i_h;
+            i_left = N / kBK - h;                   // whole halves
+            if (i_left <= 0) {                      // the one that ends past N: zeros there, of both operands
+                i_left = 1;
+                const int rest = N - h * kBK;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    if (k_r >= rest) rp[q] = zero;
+                    if (wave * 4 + q * 2 + half >= rest) cp[q] = zero;
+                }
+            }
+            i_h += i_left;
+        } else {
+            // the row addresses of 16 halves, a row per lane
+            id_par ^= 1;
+            const int p = s_id[(wave * 2 + id_par) * 64 + lane];
+            const int r = is.r0 + (i_h + (lane >> 2)) * kBK + wave * 4 + (lane & 3);
+            const bool real = r < is.r_end && p >= 0 && p < g.P;
+            const int tok = fast_div(p, g.top_k);
+            const uint64_t z = reinterpret_cast<uint64_t>(zero);
+            const uint64_t y = reinterpret_cast<uint64_t>(g.r0 + static_cast<size_t>(real ? (g.r_tok ? tok : r) : 0) * N);
+            const uint64_t x = reinterpret_cast<uint64_t>(g.c0 + static_cast<size_t>(real ? (g.c_tok ? tok : r) : 0) * K);
+            s_ptr[wave * 64 + lane] = real ? ulonglong2{y, x} : ulonglong2{z, z};
+            row_p = s_ptr + wave * 64 + half;
+            const int b = i_h / 16 + 1;
+            if (b * 16 < is.nh) load_ids(is, b, 0, id_par ^ 1);
+            else if (i_next) load_ids(in, 0, 0, id_par ^ 1);
+            i_left = min(16, is.nh - i_h);
+            i_h += i_left;
+        }
+    };
+    // the cursor moves: within the segment (i_h: the first half not yet given out), or to the next
+    auto next = [&]() {
+        if (i_h > 0 && i_h < is.nh) {
+            if (!DGRAD && i_since < 3) wait_vmcnt<0>();
+            i_since = 0;
+            move();
+            return;
+        }
+        if (i_h > 0) {
+            if (!i_next) {
+                if constexpr (DGRAD) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) rp[q] = cp[q] = zero;
+                    step_r = 0;
+                    step_c = 0;
+                } else {
+                    s_ptr[wave * 64 + lane] = ulonglong2{reinterpret_cast<uint64_t>(zero), reinterpret_cast<uint64_t>(zero)};
+                    row_p = s_ptr + wave * 64 + half;
+                }
+                i_left = 0x7fffffff;   // (at most 4 are computed and issued from here on)
+                return;
+            }
+            is = in;
+            i_h = 0;
+            ++i_seq;
+            i_next = next_seg(in);
+        }
+        // its ids: this wave's own loads of them, at least 3 halves ago (then the waits of the main loop cover them)
+        if (i_since < 3) wait_vmcnt<0>();
+        i_since = 0;
+        if constexpr (DGRAD) {
+            const int* ids = s_id + (i_seq & (kSegs - 1)) * kTile;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int row = wave * 32 + q * 16 + (lane >> 2);
+                const int src = source(ids[row], is.r0 + row, is.r_end, g.r_tok);
+                at[q] = src >= 0 ? src : (g.r_tok ? 0 : is.r0);   // a row that is always there; not stored
+            }
+            if (i_next) load_ids(in, 0, i_seq + 1, 0);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                col_r[q] = min(is.row0 + chunk_c[q], N - 8) * 2;   // (columns past the ends are never stored)
+                col_c[q] = min(is.col0 + chunk_c[q], K - 8) * 2;
+            }
+        }
+        move();
+    };
+
+    // Sources of the coming half (in the shadow of the MFMAs); then a load of each operand per q.
+    // wgrad: rows[q] are the addresses of the row of load q, read from LDS beforehand.
+    const char* src_r[2];
+    const char* src_c[2];
+    ulonglong2 rows[2];
+    uint32_t dst_r;
+    auto read_rows = [&]() __attribute__((always_inline)) {
+        if constexpr (!DGRAD) {
+            rows[0] = row_p[0];
+            rows[1] = row_p[2];
+        }
+    };
+    auto sources = [&](int q) __attribute__((always_inline)) {
+        if constexpr (DGRAD) {
+            src_r[q] = rp[q];
+            src_c[q] = cp[q];
+            rp[q] += step_r;
+            cp[q] += step_c;
+        } else {
+            const bool real = rows[q].x != reinterpret_cast<uint64_t>(zero);
+            src_r[q] = reinterpret_cast<const char*>(rows[q].x) + static_cast<uint32_t>(real ? col_r[q] : 0);
+            src_c[q] = reinterpret_cast<const char*>(rows[q].y) + static_cast<uint32_t>(real ? col_c[q] : 0);
+            if (q == 1) row_p += 4;
+        }
+        if (q == 1) {
+            dst_r = lds0 + i_slot + wave * 2048;
+            i_slot = (i_slot + kSlotB) & (kSlots * kSlotB - 1);
+        }
+    };
+    auto load_r = [&](int q) __attribute__((always_inline)) { dma16(src_r[q], dst_r + q * 1024); };
+    auto load_c = [&](int q) __attribute__((always_inline)) { dma16(src_c[q], dst_r + kPartB + q * 1024); };
 
     const int wm = wave >> 1, wn = wave & 1;   // the wave's 64 rows and 128 columns
+    const int group = wave >> 2;               // the two waves of a SIMD (w and w + 4) are in different groups
     const int fr = lane & 31, fc = lane >> 5;
-    // fragment offsets in bytes within a stage.  Transposed reads: lane i of group gr of 16 lanes reads 8 bytes
+    // fragment offsets in bytes within a slot.  Transposed reads: lane i of group gr of 16 lanes reads 8 bytes
     // of contraction row (gr / 2) * 8 + i / 4 (+ 4 in the second read), columns (gr % 2) * 16 + (i % 4) * 4.
     const int i16 = lane & 15, gr = lane >> 4;
     auto tr_off = [&](int block) __attribute__((always_inline)) {   // 32 columns from block * 32
@@ -247,153 +395,248 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     };
     int c_off[4], r_off[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) c_off[j] = kPart * 2 + tr_off(wn * 4 + j);
+    for (int j = 0; j < 4; ++j) c_off[j] = kPartB + tr_off(wn * 4 + j);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) r_off[i] = DGRAD ? (wm * 64 + i * 32 + fr) * 128 : tr_off(wm * 2 + i);
-    const int fswz = (fr >> 1) & 7;
+    for (int i = 0; i < 2; ++i) r_off[i] = DGRAD ? (wm * 64 + i * 32 + fr) * 64 : tr_off(wm * 2 + i);
+    const int fswz = (fr >> 2) & 3;
 
     f32x16 acc[2][4];
-    bf16x8 fa[2][2], fb[2][4];
+    bf16x8 fa[2][2], fb[2][4];   // [k-step][block]
     auto tr_read = [&](const char* p) __attribute__((always_inline)) {
         typedef __attribute__((address_space(3))) s16x4 lds4;
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p));
         const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + 4 * 512));
         return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     };
-    auto read = [&](int b, int kk, int set) __attribute__((always_inline)) {
-        const char* st = reinterpret_cast<const char*>(smem + b * kStage);
+    auto read = [&](int slot_at) __attribute__((always_inline)) {
+        const char* st = smem + slot_at;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if constexpr (DGRAD)
-                fa[set][i] = *reinterpret_cast<const bf16x8*>(st + r_off[i] + (((kk * 2 + fc) ^ fswz) << 4));
-            else
-                fa[set][i] = tr_read(st + r_off[i] + kk * (16 * 512));
+        for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if constexpr (DGRAD)
+                    fa[kk][i] = *reinterpret_cast<const bf16x8*>(st + r_off[i] + (((kk * 2 + fc) ^ fswz) << 4));
+                else
+                    fa[kk][i] = tr_read(st + r_off[i] + kk * (16 * 512));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) fb[kk][j] = tr_read(st + c_off[j] + kk * (16 * 512));
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) fb[set][j] = tr_read(st + c_off[j] + kk * (16 * 512));
     };
-    auto mfma = [&](int set) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[set][j], fa[set][i], acc[i][j], 0, 0, 0);
+    auto barrier = [&]() __attribute__((always_inline)) {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
     };
 
-    int sbuf = 0;   // LDS id buffer of the current segment
-    int b = 0;      // LDS buffer of its stage 0
-    first_ids(cur, 0);
-    wait_vmcnt<0>();
-    __syncthreads();
-    if (cur.nst > 0) issue(cur, 0, 0, 0);
-
-    while (true) {
-        int L2 = L + per_xcd;
-        Seg nxt;
-        const bool more = locate(L2, nxt);
-        // Stage t becomes readable: every wave waits for its own loads, then the barrier makes the stage
-        // visible and frees the other buffer for stage t + 1.
-        auto ready = [&](int t) __attribute__((always_inline)) {
-            wait_vmcnt<0>();
-            __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
-            __builtin_amdgcn_s_barrier();
-            if (t + 1 < cur.nst) issue(cur, sbuf, t + 1, (b + t + 1) & 1);
-            if constexpr (!DGRAD)
-                if (t + 2 < cur.nst && wave == 7) load_ids(cur.r0 + (t + 2) * kBK, s_ring[t & 1]);
-            if (t == 0 && more && cur.nst >= 2) first_ids(nxt, sbuf ^ 1);
+    constexpr int kStores = F32 ? 32 : 16;   // store instructions of an epilogue, whatever is masked
+    int c_slot = 0, c_seq = 0;               // slot of the half that is computed; tiles done
+    // the 16 MFMAs of a half, with the loads of a later one spread among them; the first half of a segment starts
+    // from zero
+    auto compute = [&](auto first_c) __attribute__((always_inline)) {
+        constexpr bool FIRST = decltype(first_c)::value;
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+            const int kk = n >> 3, i = (n >> 2) & 1, j = n & 3;
+            const f32x16 z = {};
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[kk][j], fa[kk][i], FIRST && kk == 0 ? z : acc[i][j], 0, 0, 0);
+            if (n == 0) sources(0);
+            if (n == 1) sources(1);
+            if (n == 3) { __builtin_amdgcn_sched_barrier(0); load_r(0); }
+            if (n == 7) { __builtin_amdgcn_sched_barrier(0); load_c(0); }
+            if (n == 10) { __builtin_amdgcn_sched_barrier(0); load_r(1); }
+            if (n == 13) { __builtin_amdgcn_sched_barrier(0); load_c(1); }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(0);
+    };
+    // One half.  At the barriers this wave's loads of the next half have landed: vmcnt counts in order, and what may be
+    // in flight are the loads of two later halves (4 each) and, where an epilogue came not more than two halves ago
+    // (AFTER), its stores.  (The first group needs the wait at the second barrier only, the second group at the first;
+    // at the other one it asks for what has landed before, or for what the next half will need.)
+    auto one_half = [&](auto first_c, auto after_c) __attribute__((always_inline)) {
+        auto landed = [&]() __attribute__((always_inline)) {
+            if (decltype(after_c)::value && c_seq > 0) wait_vmcnt<8 + kStores>();
+            else wait_vmcnt<8>();
         };
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-        if (cur.nst > 0) {
-            ready(0);
-            read(b, 0, 0);
-            for (int t = 0; t < cur.nst; ++t) {
-                const int bt = (b + t) & 1;
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    if (kk < 3) {
-                        read(bt, kk + 1, (kk + 1) & 1);
-                    } else if (t + 1 < cur.nst) {
-                        ready(t + 1);
-                        read(bt ^ 1, 0, 0);
-                    }
-                    mfma(kk & 1);
-                }
-            }
+        read(c_slot);
+        read_rows();
+        __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the slot is read
+        landed();
+        barrier();
+        compute(first_c);
+        landed();
+        barrier();
+        c_slot = (c_slot + kSlotB) & (kSlots * kSlotB - 1);
+        ++i_since;
+    };
+
+    const bool any = next_seg(is);
+    if (any) {
+        load_ids(is, 0, 0, 0);
+        i_next = next_seg(in);
+        next();
+        for (int q = 0; q < 3 + group; ++q) {
+            read_rows();
+            sources(0);
+            sources(1);
+            load_r(0); load_r(1); load_c(0); load_c(1);
+            if (--i_left == 0) next();   // (i_since stays 0: nothing has been waited for)
         }
-        // ---- the next segment's first stage, before this one's epilogue
-        if (more) {
-            if (cur.nst < 2) {      // its ids were not loaded on the way
-                __syncthreads();
-                first_ids(nxt, sbuf ^ 1);
-                wait_vmcnt<0>();
-                __syncthreads();
+        wait_vmcnt<8>();
+        barrier();
+        if (group) barrier();
+    }
+    int c_n = 0;
+    Seg cs;
+    while (find(c_n, cs)) {
+        if (cs.nh == 0) {   // an expert without rows
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+        } else {
+            one_half(std::true_type{}, std::true_type{});
+            if (--i_left == 0) next();
+            int left = cs.nh - 1;
+            if (left > 0) {
+                one_half(std::false_type{}, std::true_type{});
+                if (--i_left == 0) next();
+                --left;
             }
-            if (nxt.nst > 0) issue(nxt, sbuf ^ 1, 0, (b + cur.nst) & 1);
+            while (left > 0) {
+                const int run = min(left, i_left);
+                for (int r = 0; r < run; ++r) one_half(std::false_type{}, std::false_type{});
+                left -= run;
+                i_left -= run;
+                if (i_left == 0) next();
+            }
         }
 
         // ---- epilogue: value v of block [i][j] is output row i * 32 + fr, column j * 32 + (v / 4) * 8 + fc * 4 +
-        // v % 4 of the wave's tile; the half waves swap quads, so that a lane gets 8 adjacent columns
+        // v % 4 of the wave's tile.  The half waves swap quads, so that a lane gets 8 adjacent columns (16 bytes of
+        // bf16, 32 of fp32) at (2 p + fc) * 8 of a block's 32.  Then four lanes, four rows, exchange four such 16-byte
+        // pieces: lane b of them gets piece b of each row, and with the other half wave's a store instruction writes
+        // 8 rows of 128 adjacent bytes (without it, 32 rows of 32).  Masked lanes store past the buffer's end, which
+        // the hardware drops: the number of stores is always the same.
+        constexpr int ES = F32 ? 4 : 2;
+        const size_t first = (DGRAD ? static_cast<size_t>(cs.r0) : static_cast<size_t>(cs.e) * N + cs.row0) * K + cs.col0;
+        const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<char*>(uniform_ptr(static_cast<const char*>(g.out) + first * ES)), 0, 0x7fffffff, 0x00020000);
+        const char* base = g.base ? static_cast<const char*>(g.base) + first * ES : nullptr;
+        // (opaque to the compiler, which would else keep the offsets below in registers through the main loop)
+        int ln = lane, wv = wave;
+        asm volatile("" : "+v"(ln), "+s"(wv));
+        const int quad = ln & 3, fr = ln & 31, fc = ln >> 5, wm = wv >> 1, wn = wv & 1;
+        auto row_ok = [&](int rl) __attribute__((always_inline)) -> bool {
+            if constexpr (DGRAD) return source(s_id[(c_seq & (kSegs - 1)) * kTile + rl], cs.r0 + rl, cs.r_end, 0) >= 0;
+            else return cs.row0 + rl < N;
+        };
+        auto eight = [&](int i, int j, int p, float (&o)[8]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int rl = wm * 64 + i * 32 + fr;
-            bool ok;
-            size_t at;
-            if constexpr (DGRAD) {
-                ok = source(s_id[sbuf][rl], cur.r0 + rl, cur.r_end, 0) >= 0;
-                at = static_cast<size_t>(cur.r0 + rl) * K;
-            } else {
-                ok = cur.row0 + rl < N;
-                at = (static_cast<size_t>(cur.e) * N + cur.row0 + rl) * K;
+            for (int x = 0; x < 4; ++x) {
+                const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[i][j][8 * p + x]),
+                                                                __float_as_uint(acc[i][j][8 * p + 4 + x]), false, false);
+                o[x] = __uint_as_float(r[0]);
+                o[4 + x] = __uint_as_float(r[1]);
+            }
+        };
+        // 4 x 4 transposition of dwords over four neighbouring lanes
+        auto transpose = [&](uint32_t (&v)[4]) __attribute__((always_inline)) {
+            const bool b0 = quad & 1, b1 = quad & 2;
+#pragma unroll
+            for (int h = 0; h < 4; h += 2) {
+                const uint32_t x = __builtin_amdgcn_update_dpp(0, v[h], 0xB1, 0xF, 0xF, false);      // quad_perm [1,0,3,2]
+                const uint32_t y = __builtin_amdgcn_update_dpp(0, v[h + 1], 0xB1, 0xF, 0xF, false);
+                v[h] = b0 ? y : v[h];
+                v[h + 1] = b0 ? v[h + 1] : x;
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t x = __builtin_amdgcn_update_dpp(0, v[h], 0x4E, 0xF, 0xF, false);      // quad_perm [2,3,0,1]
+                const uint32_t y = __builtin_amdgcn_update_dpp(0, v[h + 2], 0x4E, 0xF, 0xF, false);
+                v[h] = b1 ? y : v[h];
+                v[h + 2] = b1 ? v[h + 2] : x;
+            }
+        };
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    float o[8];
+        for (int i = 0; i < 2; ++i) {
+            if (!F32 && !DGRAD && base) {   // bf16 with a base, which is added before the rounding
+                const int rl = wm * 64 + i * 32 + fr;
+                const bool ok = row_ok(rl);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[i][j][8 * p + x]),
-                                                                        __float_as_uint(acc[i][j][8 * p + 4 + x]), false, false);
-                        o[x] = __uint_as_float(r[0]);
-                        o[4 + x] = __uint_as_float(r[1]);
-                    }
-                    const int col = cur.col0 + wn * 128 + j * 32 + p * 16 + fc * 8;
-                    if (!ok || col >= K) continue;
-                    if constexpr (F32) {
-                        float* c = static_cast<float*>(g.out) + at + col;
-                        f32x4 a{o[0], o[1], o[2], o[3]}, d{o[4], o[5], o[6], o[7]};
-                        if (g.base) {
-                            const float* s = static_cast<const float*>(g.base) + at + col;
-                            a += *reinterpret_cast<const f32x4*>(s);
-                            d += *reinterpret_cast<const f32x4*>(s + 4);
-                        }
-                        *reinterpret_cast<f32x4*>(c) = a;
-                        *reinterpret_cast<f32x4*>(c + 4) = d;
-                    } else {
-                        if (!DGRAD && g.base) {
-                            const u32x4 s = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(g.base) + at + col);
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        __builtin_amdgcn_sched_barrier(0);
+                        float o[8];
+                        eight(i, j, p, o);
+                        const int col = wn * 128 + j * 32 + p * 16 + fc * 8;
+                        const bool in_out = ok && cs.col0 + col < K;
+                        const uint32_t off = (static_cast<uint32_t>(rl) * K + col) * ES;
+                        if (in_out) {
+                            const u32x4 s = *reinterpret_cast<const u32x4*>(base + off);
 #pragma unroll
                             for (int x = 0; x < 4; ++x) {
                                 o[2 * x] += __uint_as_float(s[x] << 16);
                                 o[2 * x + 1] += __uint_as_float(s[x] & 0xffff0000u);
                             }
                         }
-                        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(g.out) + at + col) =
-                            u32x4{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7])};
+                        const u32x4 v{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7])};
+                        __builtin_amdgcn_raw_buffer_store_b128(v, out, in_out ? off : 0x80000000u, 0, 0);
+                    }
+                continue;
+            }
+            bool ok[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) ok[x] = row_ok(wm * 64 + i * 32 + (fr & ~3) + x);
+#pragma unroll
+            for (int jg = 0; jg < (F32 ? 4 : 2); ++jg) {
+                __builtin_amdgcn_sched_barrier(0);   // one group at a time: else more registers than there are
+                uint32_t v[4][4];   // [dword][piece], then [dword][row]
+#pragma unroll
+                for (int q = 0; q < (F32 ? 2 : 4); ++q) {
+                    float o[8];
+                    if constexpr (F32) {        // pieces 2 p and 2 p + 1 of block jg
+                        eight(i, jg, q, o);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            v[x][2 * q] = __float_as_uint(o[x]);
+                            v[x][2 * q + 1] = __float_as_uint(o[4 + x]);
+                        }
+                    } else {                    // piece 2 (j % 2) + p
+                        eight(i, jg * 2 + (q >> 1), q & 1, o);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) v[x][q] = pack_bf16x2(o[2 * x], o[2 * x + 1]);
                     }
                 }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) transpose(v[x]);
+                const int col = wn * 128 + (F32 ? jg * 32 + (quad >> 1) * 16 + fc * 8 + (quad & 1) * 4
+                                                : jg * 64 + (quad >> 1) * 32 + (quad & 1) * 16 + fc * 8);
+                const bool c_ok = cs.col0 + col < K;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const uint32_t off = (static_cast<uint32_t>(wm * 64 + i * 32 + (fr & ~3) + x) * K + col) * ES;
+                    const bool in_out = c_ok && ok[x];
+                    u32x4 w{v[0][x], v[1][x], v[2][x], v[3][x]};
+                    if constexpr (F32) {
+                        if (base && in_out)
+                            w = __builtin_bit_cast(u32x4, __builtin_bit_cast(f32x4, w) + *reinterpret_cast<const f32x4*>(base + off));
+                    }
+                    __builtin_amdgcn_raw_buffer_store_b128(w, out, in_out ? off : 0x80000000u, 0, 0);
+                }
+            }
         }
-        if (!more) break;
-        b = (b + cur.nst) & 1;
-        sbuf ^= 1;
-        L = L2;
-        cur = nxt;
+        ++c_seq;
     }
+    if (any && !group) barrier();   // the other group's last
+    wait_vmcnt<0>();                // the halves of zeros: nothing may land in LDS after the end
 }
 
 FastDiv make_div(uint32_t d) {
