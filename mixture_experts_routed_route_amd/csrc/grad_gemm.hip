@@ -42,7 +42,9 @@ constexpr int kTab = 128;      // entries of a workgroup's list that are located
 constexpr int kSegs = 8;       // dgrad: tiles whose row ids are held
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ float lo_f32(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi_f32(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
 // division by a launch constant d >= 1 of numbers below 2^31 (round-up reciprocal: exact there)
 struct FastDiv {
@@ -253,7 +255,7 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     uint64_t step_c = 0;
     int at[2], chunk_c[2], col_r[2], col_c[2];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) chunk_c[q] = ((lane & 31) ^ (((q * 2 + half) << 2) | (((wave >> 1) & 1) << 1))) * 8;
+    for (int q = 0; q < 2; ++q) chunk_c[q] = ((lane & 31) ^ (((q * 2 + half) << 2) | ((((wave >> 1) ^ (wave >> 2)) & 1) << 1))) * 8;
     const int k_r = ((lane & 3) ^ ((lane >> 4) & 3)) * 8;   // dgrad: first n of this lane's chunk of a row of dy
     const ulonglong2* row_p = s_ptr;   // wgrad: the row addresses of the coming half
     auto move = [&]() {
@@ -382,46 +384,43 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     auto load_r = [&](int q) __attribute__((always_inline)) { dma16(src_r[q], dst_r + q * 1024); };
     auto load_c = [&](int q) __attribute__((always_inline)) { dma16(src_c[q], dst_r + kPartB + q * 1024); };
 
-    const int wm = wave >> 1, wn = wave & 1;   // the wave's 64 rows and 128 columns
+    int c_slot = 0, c_seq = 0;               // slot of the half that is computed; tiles done
+    // A wave's rows are i * 64 + wm * 16 (i < 4), its columns (j / 2) * 64 + wn * 32 + (j % 2) * 16 (j < 8), 16 each:
+    // tiles of few rows or columns then leave the same share of blocks to every wave.
+    constexpr int kStores = F32 ? 32 : 16;   // store instructions of an epilogue, whatever is masked
+    const int wm = wave >> 1, wn = wave & 1;
     const int group = wave >> 2;               // the two waves of a SIMD (w and w + 4) are in different groups
-    const int fr = lane & 31, fc = lane >> 5;
-    // fragment offsets in bytes within a slot.  Transposed reads: lane i of group gr of 16 lanes reads 8 bytes
-    // of contraction row (gr / 2) * 8 + i / 4 (+ 4 in the second read), columns (gr % 2) * 16 + (i % 4) * 4.
+    // Fragment offsets in bytes within a slot.  A lane of the 16x16x32 MFMA holds 8 contraction indices from
+    // 8 * (lane / 16) of row or column lane % 16.  Transposed reads: lane i16 of group gr of 16 lanes reads 8 bytes of
+    // contraction row gr * 8 + i16 / 4 (+ 4 in the second read), columns (i16 % 4) * 4.
     const int i16 = lane & 15, gr = lane >> 4;
-    auto tr_off = [&](int block) __attribute__((always_inline)) {   // 32 columns from block * 32
-        const int row = (gr >> 1) * 8 + (i16 >> 2);
-        const int chunk = ((block ^ (i16 >> 2)) << 2) + ((((gr & 1) ^ (gr >> 1)) << 1) | ((i16 & 3) >> 1));
-        return row * 512 + chunk * 16 + (i16 & 1) * 8;
+    auto tr_off = [&](int block) __attribute__((always_inline)) {   // 16 columns from block * 16, block < 8
+        const int row = gr * 8 + (i16 >> 2), bit = (gr ^ (gr >> 1)) & 1;
+        return row * 512 + (((((block >> 1) ^ (i16 >> 2)) << 2) | (((block & 1) ^ bit) << 1) | ((i16 & 3) >> 1)) << 4) + (i16 & 1) * 8;
     };
-    int c_off[4], r_off[2];
+    int c_off[4], r_off[2];      // blocks 8 further on lie 256 bytes further on
 #pragma unroll
-    for (int j = 0; j < 4; ++j) c_off[j] = kPartB + tr_off(wn * 4 + j);
+    for (int j = 0; j < 4; ++j) c_off[j] = kPartB + tr_off((j >> 1) * 4 + wn * 2 + (j & 1));
 #pragma unroll
-    for (int i = 0; i < 2; ++i) r_off[i] = DGRAD ? (wm * 64 + i * 32 + fr) * 64 : tr_off(wm * 2 + i);
-    const int fswz = (fr >> 2) & 3;
+    for (int i = 0; i < 2; ++i) r_off[i] = DGRAD ? (wm * 16 + i16) * 64 + ((gr ^ (i16 >> 2)) << 4) : tr_off(i * 4 + wm);
 
-    f32x16 acc[2][4];
-    bf16x8 fa[2][2], fb[2][4];   // [k-step][block]
+    f32x4 acc[4][8];
+    bf16x8 fa[4], fb[8];
     auto tr_read = [&](const char* p) __attribute__((always_inline)) {
         typedef __attribute__((address_space(3))) s16x4 lds4;
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p));
         const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + 4 * 512));
         return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     };
-    auto read = [&](int slot_at) __attribute__((always_inline)) {
-        const char* st = smem + slot_at;
+    auto read = [&](auto rf_c, auto cf_c) __attribute__((always_inline)) {
+        const char* st = smem + c_slot;
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if constexpr (DGRAD)
-                    fa[kk][i] = *reinterpret_cast<const bf16x8*>(st + r_off[i] + (((kk * 2 + fc) ^ fswz) << 4));
-                else
-                    fa[kk][i] = tr_read(st + r_off[i] + kk * (16 * 512));
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) fb[kk][j] = tr_read(st + c_off[j] + kk * (16 * 512));
+        for (int i = 0; i < decltype(rf_c)::value; ++i) {
+            if constexpr (DGRAD) fa[i] = *reinterpret_cast<const bf16x8*>(st + r_off[0] + i * 4096);
+            else fa[i] = tr_read(st + r_off[i & 1] + (i >> 1) * 256);
         }
+#pragma unroll
+        for (int j = 0; j < decltype(cf_c)::value; ++j) fb[j] = tr_read(st + c_off[j & 3] + (j >> 2) * 256);
     };
     auto barrier = [&]() __attribute__((always_inline)) {
         __builtin_amdgcn_sched_barrier(0);
@@ -431,43 +430,40 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    constexpr int kStores = F32 ? 32 : 16;   // store instructions of an epilogue, whatever is masked
-    int c_slot = 0, c_seq = 0;               // slot of the half that is computed; tiles done
-    // the 16 MFMAs of a half, with the loads of a later one spread among them; the first half of a segment starts
-    // from zero
-    auto compute = [&](auto first_c) __attribute__((always_inline)) {
-        constexpr bool FIRST = decltype(first_c)::value;
+    // The MFMAs of a half, RF x CF blocks, with the loads of a later half spread among them; FIRST: from zero.
+    auto compute = [&](auto rf_c, auto cf_c, auto first_c) __attribute__((always_inline)) {
+        constexpr int CF = decltype(cf_c)::value, M = decltype(rf_c)::value * CF;
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int n = 0; n < 16; ++n) {
-            const int kk = n >> 3, i = (n >> 2) & 1, j = n & 3;
-            const f32x16 z = {};
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[kk][j], fa[kk][i], FIRST && kk == 0 ? z : acc[i][j], 0, 0, 0);
+        for (int n = 0; n < M; ++n) {
+            const int i = n / CF, j = n % CF;
+            const f32x4 z = {};
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], decltype(first_c)::value ? z : acc[i][j], 0, 0, 0);
             if (n == 0) sources(0);
-            if (n == 1) sources(1);
-            if (n == 3) { __builtin_amdgcn_sched_barrier(0); load_r(0); }
-            if (n == 7) { __builtin_amdgcn_sched_barrier(0); load_c(0); }
-            if (n == 10) { __builtin_amdgcn_sched_barrier(0); load_r(1); }
-            if (n == 13) { __builtin_amdgcn_sched_barrier(0); load_c(1); }
+            if (n == M / 8) sources(1);
+            if (n == M / 4 - 1) { __builtin_amdgcn_sched_barrier(0); load_r(0); }
+            if (n == M / 2 - 1) { __builtin_amdgcn_sched_barrier(0); load_c(0); }
+            if (n == M * 11 / 16 - 1) { __builtin_amdgcn_sched_barrier(0); load_r(1); }
+            if (n == M * 7 / 8 - 1) { __builtin_amdgcn_sched_barrier(0); load_c(1); }
         }
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_setprio(0);
     };
     // One half.  At the barriers this wave's loads of the next half have landed: vmcnt counts in order, and what may be
     // in flight are the loads of two later halves (4 each) and, where an epilogue came not more than two halves ago
-    // (AFTER), its stores.  (The first group needs the wait at the second barrier only, the second group at the first;
+    // (after), its stores.  (The first group needs the wait at the second barrier only, the second group at the first;
     // at the other one it asks for what has landed before, or for what the next half will need.)
-    auto one_half = [&](auto first_c, auto after_c) __attribute__((always_inline)) {
+    auto one_half = [&](auto rf_c, auto cf_c, auto first_c, bool after) __attribute__((always_inline)) {
         auto landed = [&]() __attribute__((always_inline)) {
-            if (decltype(after_c)::value && c_seq > 0) wait_vmcnt<8 + kStores>();
+            if (after) wait_vmcnt<8 + kStores>();
             else wait_vmcnt<8>();
         };
-        read(c_slot);
+        read(rf_c, cf_c);
         read_rows();
         __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the slot is read
         landed();
         barrier();
-        compute(first_c);
+        compute(rf_c, cf_c, first_c);
         landed();
         barrier();
         c_slot = (c_slot + kSlotB) & (kSlots * kSlotB - 1);
@@ -493,146 +489,124 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     int c_n = 0;
     Seg cs;
     while (find(c_n, cs)) {
-        if (cs.nh == 0) {   // an expert without rows
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-        } else {
-            one_half(std::true_type{}, std::true_type{});
+        const int n_rows = DGRAD ? cs.r_end - cs.r0 : N - cs.row0, n_cols = K - cs.col0;
+        using I1 = std::integral_constant<int, 1>;
+        using I2 = std::integral_constant<int, 2>;
+        using I4 = std::integral_constant<int, 4>;
+        using I8 = std::integral_constant<int, 8>;
+        const bool again = c_seq > 0;
+        if (cs.nh > 0 && n_rows > 128 && n_cols > 128) {
+            one_half(I4{}, I8{}, std::true_type{}, again);
             if (--i_left == 0) next();
             int left = cs.nh - 1;
             if (left > 0) {
-                one_half(std::false_type{}, std::true_type{});
+                one_half(I4{}, I8{}, std::false_type{}, again);
                 if (--i_left == 0) next();
                 --left;
             }
             while (left > 0) {
                 const int run = min(left, i_left);
-                for (int r = 0; r < run; ++r) one_half(std::false_type{}, std::false_type{});
+                for (int r = 0; r < run; ++r) one_half(I4{}, I8{}, std::false_type{}, false);
                 left -= run;
                 i_left -= run;
                 if (i_left == 0) next();
             }
+        } else {
+            // fewer blocks hold rows or columns (or the expert has no rows)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            auto some = [&](auto rf_c, auto cf_c) __attribute__((always_inline)) {
+                for (int h = 0; h < cs.nh; ++h) {
+                    one_half(rf_c, cf_c, std::false_type{}, again && h < 2);
+                    if (--i_left == 0) next();
+                }
+            };
+            if (n_rows > 128) some(I4{}, I4{});
+            else if (n_rows > 64) some(I2{}, I8{});
+            else some(I1{}, I8{});
         }
 
-        // ---- epilogue: value v of block [i][j] is output row i * 32 + fr, column j * 32 + (v / 4) * 8 + fc * 4 +
-        // v % 4 of the wave's tile.  The half waves swap quads, so that a lane gets 8 adjacent columns (16 bytes of
-        // bf16, 32 of fp32) at (2 p + fc) * 8 of a block's 32.  Then four lanes, four rows, exchange four such 16-byte
-        // pieces: lane b of them gets piece b of each row, and with the other half wave's a store instruction writes
-        // 8 rows of 128 adjacent bytes (without it, 32 rows of 32).  Masked lanes store past the buffer's end, which
-        // the hardware drops: the number of stores is always the same.
-        constexpr int ES = F32 ? 4 : 2;
+        // ---- epilogue.  Value v of block [i][j] is output row i16 of the block's rows and column gr * 4 + v of its
+        // columns.  bf16: two blocks of neighbouring columns are exchanged between the 16-lane groups gr and gr ^ 1, so
+        // that a lane gets 8 adjacent columns; a store instruction writes 16 rows of 64 adjacent bytes either way.
+        // Masked lanes store past the buffer's end, which the hardware drops: the number of stores is always the same.
+        // base: the loads of 64 rows are in flight while those before are added and stored.
+        constexpr int ES = F32 ? 4 : 2, PW = F32 ? 8 : 4;   // bytes of a value, 16-byte pieces of a row and lane
         const size_t first = (DGRAD ? static_cast<size_t>(cs.r0) : static_cast<size_t>(cs.e) * N + cs.row0) * K + cs.col0;
-        const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<char*>(uniform_ptr(static_cast<const char*>(g.out) + first * ES)), 0, 0x7fffffff, 0x00020000);
-        const char* base = g.base ? static_cast<const char*>(g.base) + first * ES : nullptr;
+        auto resource = [&](const void* p) __attribute__((always_inline)) {
+            return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(uniform_ptr(static_cast<const char*>(p) + first * ES)), 0,
+                                                     0x7fffffff, 0x00020000);
+        };
+        const __amdgpu_buffer_rsrc_t out = resource(g.out);
         // (opaque to the compiler, which would else keep the offsets below in registers through the main loop)
         int ln = lane, wv = wave;
         asm volatile("" : "+v"(ln), "+s"(wv));
-        const int quad = ln & 3, fr = ln & 31, fc = ln >> 5, wm = wv >> 1, wn = wv & 1;
-        auto row_ok = [&](int rl) __attribute__((always_inline)) -> bool {
-            if constexpr (DGRAD) return source(s_id[(c_seq & (kSegs - 1)) * kTile + rl], cs.r0 + rl, cs.r_end, 0) >= 0;
-            else return cs.row0 + rl < N;
-        };
-        auto eight = [&](int i, int j, int p, float (&o)[8]) __attribute__((always_inline)) {
+        const int er = ln & 15, eg = ln >> 4, em = wv >> 1, en = wv & 1;
+        uint32_t ok = 0;   // rows i of this lane that are stored
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[i][j][8 * p + x]),
-                                                                __float_as_uint(acc[i][j][8 * p + 4 + x]), false, false);
-                o[x] = __uint_as_float(r[0]);
-                o[4 + x] = __uint_as_float(r[1]);
-            }
-        };
-        // 4 x 4 transposition of dwords over four neighbouring lanes
-        auto transpose = [&](uint32_t (&v)[4]) __attribute__((always_inline)) {
-            const bool b0 = quad & 1, b1 = quad & 2;
-#pragma unroll
-            for (int h = 0; h < 4; h += 2) {
-                const uint32_t x = __builtin_amdgcn_update_dpp(0, v[h], 0xB1, 0xF, 0xF, false);      // quad_perm [1,0,3,2]
-                const uint32_t y = __builtin_amdgcn_update_dpp(0, v[h + 1], 0xB1, 0xF, 0xF, false);
-                v[h] = b0 ? y : v[h];
-                v[h + 1] = b0 ? v[h + 1] : x;
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t x = __builtin_amdgcn_update_dpp(0, v[h], 0x4E, 0xF, 0xF, false);      // quad_perm [2,3,0,1]
-                const uint32_t y = __builtin_amdgcn_update_dpp(0, v[h + 2], 0x4E, 0xF, 0xF, false);
-                v[h] = b1 ? y : v[h];
-                v[h + 2] = b1 ? v[h + 2] : x;
-            }
-        };
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (!F32 && !DGRAD && base) {   // bf16 with a base, which is added before the rounding
-                const int rl = wm * 64 + i * 32 + fr;
-                const bool ok = row_ok(rl);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        __builtin_amdgcn_sched_barrier(0);
-                        float o[8];
-                        eight(i, j, p, o);
-                        const int col = wn * 128 + j * 32 + p * 16 + fc * 8;
-                        const bool in_out = ok && cs.col0 + col < K;
-                        const uint32_t off = (static_cast<uint32_t>(rl) * K + col) * ES;
-                        if (in_out) {
-                            const u32x4 s = *reinterpret_cast<const u32x4*>(base + off);
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                o[2 * x] += __uint_as_float(s[x] << 16);
-                                o[2 * x + 1] += __uint_as_float(s[x] & 0xffff0000u);
-                            }
-                        }
-                        const u32x4 v{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7])};
-                        __builtin_amdgcn_raw_buffer_store_b128(v, out, in_out ? off : 0x80000000u, 0, 0);
-                    }
-                continue;
-            }
-            bool ok[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) ok[x] = row_ok(wm * 64 + i * 32 + (fr & ~3) + x);
-#pragma unroll
-            for (int jg = 0; jg < (F32 ? 4 : 2); ++jg) {
-                __builtin_amdgcn_sched_barrier(0);   // one group at a time: else more registers than there are
-                uint32_t v[4][4];   // [dword][piece], then [dword][row]
-#pragma unroll
-                for (int q = 0; q < (F32 ? 2 : 4); ++q) {
-                    float o[8];
-                    if constexpr (F32) {        // pieces 2 p and 2 p + 1 of block jg
-                        eight(i, jg, q, o);
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            v[x][2 * q] = __float_as_uint(o[x]);
-                            v[x][2 * q + 1] = __float_as_uint(o[4 + x]);
-                        }
-                    } else {                    // piece 2 (j % 2) + p
-                        eight(i, jg * 2 + (q >> 1), q & 1, o);
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) v[x][q] = pack_bf16x2(o[2 * x], o[2 * x + 1]);
-                    }
-                }
-#pragma unroll
-                for (int x = 0; x < 4; ++x) transpose(v[x]);
-                const int col = wn * 128 + (F32 ? jg * 32 + (quad >> 1) * 16 + fc * 8 + (quad & 1) * 4
-                                                : jg * 64 + (quad >> 1) * 32 + (quad & 1) * 16 + fc * 8);
-                const bool c_ok = cs.col0 + col < K;
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const uint32_t off = (static_cast<uint32_t>(wm * 64 + i * 32 + (fr & ~3) + x) * K + col) * ES;
-                    const bool in_out = c_ok && ok[x];
-                    u32x4 w{v[0][x], v[1][x], v[2][x], v[3][x]};
-                    if constexpr (F32) {
-                        if (base && in_out)
-                            w = __builtin_bit_cast(u32x4, __builtin_bit_cast(f32x4, w) + *reinterpret_cast<const f32x4*>(base + off));
-                    }
-                    __builtin_amdgcn_raw_buffer_store_b128(w, out, in_out ? off : 0x80000000u, 0, 0);
-                }
-            }
+        for (int i = 0; i < 4; ++i) {
+            const int rl = i * 64 + em * 16 + er;
+            bool in;
+            if constexpr (DGRAD) in = source(s_id[(c_seq & (kSegs - 1)) * kTile + rl], cs.r0 + rl, cs.r_end, 0) >= 0;
+            else in = cs.row0 + rl < N;
+            ok |= in ? 1u << i : 0u;
         }
+        auto offset = [&](int i, int q) __attribute__((always_inline)) -> uint32_t {   // of piece q of row i
+            const int col = F32 ? (q >> 1) * 64 + en * 32 + (q & 1) * 16 + eg * 4 : q * 64 + en * 32 + (eg & 1) * 16 + (eg >> 1) * 8;
+            const bool in = (ok >> i & 1) && cs.col0 + col < K;
+            return in ? (static_cast<uint32_t>(i * 64 + em * 16 + er) * K + col) * ES : 0x80000000u;
+        };
+        auto exchange = [&](u32x4& w) __attribute__((always_inline)) {   // its own inverse
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+                const auto r = __builtin_amdgcn_permlane16_swap(w[d], w[2 + d], false, false);
+                w[d] = r[0];
+                w[2 + d] = r[1];
+            }
+        };
+        auto finish = [&](auto base_c) __attribute__((always_inline)) {
+            constexpr bool BASE = decltype(base_c)::value;
+            __amdgpu_buffer_rsrc_t in = out;
+            u32x4 old[2][PW];
+            auto fetch = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+                for (int q = 0; q < PW; ++q) old[i & 1][q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(in, offset(i, q), 0, 0));
+            };
+            if constexpr (BASE) {
+                in = resource(g.base);
+                fetch(0);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (BASE)
+                    if (i < 3) fetch(i + 1);
+#pragma unroll
+                for (int q = 0; q < PW; ++q) {
+                    u32x4 w;
+                    if constexpr (F32) {
+                        f32x4 v = acc[i][q];
+                        if constexpr (BASE) v += __builtin_bit_cast(f32x4, old[i & 1][q]);
+                        w = __builtin_bit_cast(u32x4, v);
+                    } else {
+                        f32x4 a = acc[i][2 * q], b = acc[i][2 * q + 1];
+                        if constexpr (BASE) {
+                            u32x4 o = old[i & 1][q];
+                            exchange(o);    // back to the blocks' columns
+                            a += f32x4{lo_f32(o[0]), hi_f32(o[0]), lo_f32(o[1]), hi_f32(o[1])};
+                            b += f32x4{lo_f32(o[2]), hi_f32(o[2]), lo_f32(o[3]), hi_f32(o[3])};
+                        }
+                        w = u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])};
+                        exchange(w);
+                    }
+                    __builtin_amdgcn_raw_buffer_store_b128(w, out, offset(i, q), 0, 0);
+                }
+            }
+        };
+        if (!DGRAD && g.base) finish(std::true_type{});
+        else finish(std::false_type{});
         ++c_seq;
     }
     if (any && !group) barrier();   // the other group's last
