@@ -67,7 +67,10 @@ int64_t moe_align_max_padded(int64_t num_pairs, int32_t num_experts, int32_t blo
     return max_padded(num_pairs, num_experts, block_size);
 }
 
-int64_t moe_grouped_gemm_workspace_bytes(void) { return moe::gemm_bf16_workspace_bytes(); }
+int64_t moe_grouped_gemm_workspace_bytes(void) {
+    const int64_t forward = moe::gemm_bf16_workspace_bytes(), gradients = moe::grad_gemm_workspace_bytes();
+    return forward > gradients ? forward : gradients;   // (both 64 MiB and the counters)
+}
 
 int64_t moe_align_workspace_bytes(int64_t num_pairs, int32_t num_experts) {
     if (num_pairs < 0 || num_experts < 1) return -1;
@@ -1034,8 +1037,7 @@ moe_status moe_grouped_gemm_dgrad(const uint16_t* dy0, const moe_weight* w0, con
     return launched(who, moe::launch_dgrad(dy0, static_cast<const uint16_t*>(w0->data), dy1,
                                            w1 ? static_cast<const uint16_t*>(w1->data) : nullptr, dx, sorted_ids,
                                            expert_offsets, static_cast<int>(num_pairs), top_k, num_experts, n, k,
-                                           static_cast<int>(max_pad), by_token ? 1 : 0, workspace, workspace_bytes,
-                                           static_cast<hipStream_t>(stream)));
+                                           static_cast<int>(max_pad), by_token ? 1 : 0, workspace, static_cast<hipStream_t>(stream)));
 }
 
 moe_status moe_grouped_gemm_wgrad(const uint16_t* dy, const uint16_t* x, void* dw, const void* base, int32_t dw_fp32,
@@ -1059,7 +1061,7 @@ moe_status moe_grouped_gemm_wgrad(const uint16_t* dy, const uint16_t* x, void* d
     return launched(who, moe::launch_wgrad(dy, x, dw, base, dw_fp32 != 0, sorted_ids, expert_offsets,
                                            static_cast<int>(num_pairs), top_k, num_experts, n, k,
                                            static_cast<int>(max_pad), dy_by_token ? 1 : 0, x_by_token ? 1 : 0, workspace,
-                                           workspace_bytes, static_cast<hipStream_t>(stream)));
+                                           static_cast<hipStream_t>(stream)));
 }
 
 moe_status moe_route_backward(const int32_t* topk_ids, const float* topk_w, const float* d_topk_w,

@@ -37,11 +37,15 @@ constexpr int kNT = 512;
 constexpr int kPartB = kTile * kBK * 2;  // bytes of one operand in a slot
 constexpr int kSlotB = 2 * kPartB;
 constexpr int kMaxE = 256;
-constexpr int kBand = 8;       // row tiles per band of the tile order
+constexpr int kBand = 4;       // row tiles per band of the tile order
 constexpr int kTab = 128;      // entries of a workgroup's list that are located in advance
+constexpr int kMaxPieces = 256;  // workgroups of a launch whose tiles are cut along the contraction
+constexpr int kMaxSplit = 8;     // pieces of a tile
+constexpr int kMinPiece = 8;     // halves of a piece
 constexpr int kSegs = 8;       // dgrad: tiles whose row ids are held
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ float lo_f32(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
@@ -67,11 +71,13 @@ struct GradArgs {
     FastDiv top_k;
     int P, E, N, K, max_pad;
     int r_tok, c_tok;     // operand rows by token
+    int32_t* cnt;         // workspace, or NULL: counters [kMaxPieces], zero between calls
+    float* part;          // and partial tiles [kMaxPieces][kTile * kTile]
 };
 
 struct Seg {
     int e, r0, r_end;   // dgrad: expert, first sorted row, end of rows; wgrad: expert, its span
-    int row0, col0;     // first output row (wgrad: of N) and column
+    int row0, col0;     // wgrad: first output row, of N (dgrad: first half); first output column
     int nh;             // halves
 };
 enum { kEnd, kSkip, kIsTile };
@@ -83,6 +89,9 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     __shared__ int s_lo[kMaxE], s_hi[kMaxE], s_tb[kMaxE + 1], s_order[kMaxE];
     __shared__ int s_scan[kNT / 64];
     __shared__ int4 s_tab[kTab], s_tab2[kTab];
+    __shared__ int s_mine[64];    // wgrad, unequal experts: this workgroup's tiles
+    __shared__ int s_arrived;
+    __shared__ __attribute__((aligned(1024))) char s_stage[kNT / 64 * 1024];   // a wave's results on their way out
     // sorted ids.  dgrad: of the rows of the last kSegs tiles.  wgrad: per wave, of its rows (4 per half) of 16 halves, twice
     __shared__ __attribute__((aligned(16))) int s_id[DGRAD ? kSegs * kTile : kNT / 64 * 2 * 64];
     // wgrad: per wave, the rows' addresses in the two operands (the zeros' where a row holds no pair)
@@ -120,43 +129,40 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     }
     const int n_tiles = (K + kTile - 1) / kTile;     // column tiles
     const int r_tiles = (N + kTile - 1) / kTile;     // wgrad: row tiles of an expert's matrix
+    const int nkh = (N + kBK - 1) / kBK;             // dgrad: halves of one pair
     const int per_xcd = gridDim.x >> 3;
     const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
-
-    // ---- this XCD's list of tiles, entries i = slot, slot + per_xcd, ...
-    // dgrad: an eighth of the tiles.  wgrad: units of up to 32 tiles of one expert, dealt to the XCDs in turn by
-    // falling length.
     const int m_real = DGRAD ? __builtin_amdgcn_readfirstlane(s_tb[E]) : 0;
-    const long long T = DGRAD ? static_cast<long long>(m_real) * n_tiles : 0;
-    const int l_lo = DGRAD ? static_cast<int>(T * xcd / 8) : 0;
     const int tiles_e = r_tiles * n_tiles;
+    const int T = DGRAD ? m_real * n_tiles : E * tiles_e;
+    auto halves_of = [&](int e) __attribute__((always_inline)) { return (s_hi[e] - s_lo[e] + kBK - 1) / kBK; };
+
+    // ---- Few tiles (and a workspace): each is cut along the contraction into `pieces`, one per workgroup, which meet
+    // through fp32 partial tiles in the workspace.
+    int pieces = 1;
+    if (g.part && T > 0 && 2 * T <= static_cast<int>(gridDim.x)) {
+        const int most = DGRAD ? (g.r1 ? 2 * nkh : nkh) : halves_of(s_order[0]);
+        pieces = min(min(min(static_cast<int>(gridDim.x), kMaxPieces) / T, kMaxSplit), most / kMinPiece);
+        pieces = max(__builtin_amdgcn_readfirstlane(pieces), 1);
+    }
+
+    // ---- this workgroup's list of tiles.  An XCD's tiles are dealt to its workgroups in turn, entries slot,
+    // slot + per_xcd, ...; dgrad: an eighth of the tiles each.  wgrad: units of up to 32 tiles of one expert, dealt to
+    // the XCDs by falling length, back and forth.
+    const int l_lo = DGRAD ? static_cast<int>(static_cast<long long>(T) * xcd / 8) : 0;
     int unit = 1, units_e = 1;
     if constexpr (!DGRAD) {
-        const int most = static_cast<int>(min<long long>(32, max<long long>(1, static_cast<long long>(E) * tiles_e / 64)));
-        units_e = (tiles_e + most - 1) / most;
+        units_e = (tiles_e + 31) / 32;
+        if (T < 2048) units_e = min(tiles_e, max(units_e, tiles_e / max(T / 64, 1)));   // few tiles: over all XCDs
         unit = (tiles_e + units_e - 1) / units_e;
     }
-    const int units = E * units_e;
-    const int l_n = DGRAD ? static_cast<int>(T * (xcd + 1) / 8) - l_lo : (units + 7) / 8 * unit;
-
-    const int nkh = (N + kBK - 1) / kBK;             // dgrad: halves of one pair
-    // entry number n of this workgroup: kTile, kSkip (no tile) or kEnd
-    auto locate = [&](int n, Seg& s) __attribute__((always_inline)) -> int {
-        const int i = slot + n * per_xcd;
-        if (i >= l_n) return kEnd;
-        int idx, m_lim, e = 0;
-        if constexpr (DGRAD) {
-            idx = l_lo + i;
-            m_lim = m_real;
-        } else {
-            const int v = i / unit;
-            const int u = v * 8 + ((v & 1) ? 7 - xcd : xcd);
-            idx = (u % units_e) * unit + i % unit;
-            if (u >= units || idx >= tiles_e) return kSkip;
-            m_lim = r_tiles;
-            e = s_order[u / units_e];
-        }
+    const int units = E * units_e, xcd_units = (units + 7) / 8;
+    const int l_n = DGRAD ? static_cast<int>(static_cast<long long>(T) * (xcd + 1) / 8) - l_lo : xcd_units * unit;
+    auto unit_at = [&](int v) __attribute__((always_inline)) { return v * 8 + ((v & 1) ? 7 - xcd : xcd); };
+    // tile idx (dgrad: of all; wgrad: of expert e)
+    auto tile_at = [&](int idx, int e, Seg& s) __attribute__((always_inline)) {
         // bands of kBand row tiles, row tiles fastest: tiles that run together share operands in L2
+        const int m_lim = DGRAD ? m_real : r_tiles;
         const int band = idx / (kBand * n_tiles);
         const int at = idx - band * kBand * n_tiles;
         const int rows = min(kBand, m_lim - band * kBand);
@@ -165,6 +171,7 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
         s.col0 = n_t * kTile;
         if constexpr (DGRAD) {
             int hi = E - 1;  // e: the largest expert whose first row tile is <= m_t
+            e = 0;
             while (e < hi) {
                 const int mid = (e + hi + 1) >> 1;
                 if (s_tb[mid] <= m_t) e = mid; else hi = mid - 1;
@@ -177,9 +184,81 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
             s.row0 = m_t * kTile;
             s.r0 = s_lo[e];
             s.r_end = s_hi[e];
-            s.nh = (s.r_end - s.r0 + kBK - 1) / kBK;
+            s.nh = halves_of(e);
         }
         s.e = e;
+    };
+    // wgrad, experts of very different lengths: dealing in turn would give the workgroups with the longest tiles as many
+    // others as the rest.  Instead every unit's tiles, unit by unit by falling length, go to the workgroups of the XCD
+    // that have least so far.  (A step of the first wave per unit, so for few units only; 128 experts of 2048 x 768 with
+    // 8 to 8192 rows.)
+    bool levelled = false;
+    if constexpr (!DGRAD) {
+        constexpr int kEpilogue = F32 ? 12 : 6;   // a tile's end in halves
+        const int longest = halves_of(s_order[0]), shortest = halves_of(s_order[E - 1]);
+        levelled = pieces == 1 && longest > 2 * shortest + kEpilogue && xcd_units <= 64 && unit <= per_xcd && per_xcd <= 64 &&
+                   xcd_units * unit > per_xcd;
+        levelled = __builtin_amdgcn_readfirstlane(levelled);
+        if (levelled) {
+            if (wave == 0) {
+                int load = lane < per_xcd ? 0 : 0x3fffffff, n = 0;
+                for (int v = 0; v < xcd_units; ++v) {
+                    const int u = unit_at(v);
+                    if (u >= units) break;
+                    const int e = s_order[u / units_e], first = (u % units_e) * unit;
+                    const int tiles = min(unit, tiles_e - first);
+                    int rank = 0;
+                    for (int t = 0; t < per_xcd; ++t) {
+                        const int other = __builtin_amdgcn_readlane(load, t);
+                        rank += other < load || (other == load && t < lane);
+                    }
+                    if (rank < tiles) {
+                        load += halves_of(e) + kEpilogue;
+                        if (lane == slot) s_mine[n] = v << 8 | rank;
+                        ++n;
+                    }
+                }
+                if (lane == slot && n < 64) s_mine[n] = -1;
+            }
+            __syncthreads();
+        }
+    }
+    // entry number n of this workgroup: kIsTile, kSkip (no tile) or kEnd
+    auto locate = [&](int n, Seg& s) __attribute__((always_inline)) -> int {
+        if (pieces > 1) {   // piece blockIdx / T of tile blockIdx % T
+            const int t = blockIdx.x % T, j = blockIdx.x / T;
+            if (n > 0 || j >= pieces) return kEnd;
+            tile_at(DGRAD ? t : t % tiles_e, DGRAD ? 0 : t / tiles_e, s);
+            const int h0 = s.nh * j / pieces, h1 = s.nh * (j + 1) / pieces;
+            if constexpr (DGRAD) {
+                s.row0 = h0;
+            } else {
+                s.r0 += h0 * kBK;
+                s.r_end = min(s.r_end, s.r0 + (h1 - h0) * kBK);
+            }
+            s.nh = h1 - h0;
+            return kIsTile;
+        }
+        if constexpr (DGRAD) {
+            const int i = slot + n * per_xcd;
+            if (i >= l_n) return kEnd;
+            tile_at(l_lo + i, 0, s);
+        } else {
+            int v, j;
+            if (levelled) {
+                if (n >= 64 || s_mine[n] < 0) return kEnd;
+                v = s_mine[n] >> 8;
+                j = s_mine[n] & 255;
+            } else {
+                const int i = slot + n * per_xcd;
+                if (i >= l_n) return kEnd;
+                v = i / unit;
+                j = i % unit;
+            }
+            const int u = unit_at(v), idx = (u % units_e) * unit + j;
+            if (u >= units || idx >= tiles_e) return kSkip;
+            tile_at(idx, s_order[u / units_e], s);
+        }
         return kIsTile;
     };
     // the first entries, located once by a thread each (a dependent chain of divisions and searches)
@@ -214,6 +293,12 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
         }
     };
 
+    // address of row `row` of an operand of `width` columns (one 32 x 32 bit product)
+    auto row_address = [](const uint16_t* p, int row, int width) __attribute__((always_inline)) {
+        uint32_t bytes = static_cast<uint32_t>(width) * 2;
+        asm volatile("" : "+s"(bytes));   // (keeps the compiler from widening it first)
+        return reinterpret_cast<uint64_t>(p) + static_cast<uint64_t>(static_cast<uint32_t>(row)) * bytes;
+    };
     const uint32_t lds0 = lds_u32(smem), lds_id = lds_u32(s_id);
     const char* zero = reinterpret_cast<const char*>(kZero16);
     const int half = lane >> 5;
@@ -258,23 +343,26 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     for (int q = 0; q < 2; ++q) chunk_c[q] = ((lane & 31) ^ (((q * 2 + half) << 2) | ((((wave >> 1) ^ (wave >> 2)) & 1) << 1))) * 8;
     const int k_r = ((lane & 3) ^ ((lane >> 4) & 3)) * 8;   // dgrad: first n of this lane's chunk of a row of dy
     const ulonglong2* row_p = s_ptr;   // wgrad: the row addresses of the coming half
-    auto move = [&]() {
+    // what can be issued from half i_h of the segment on
+    auto move = [&](bool first) __attribute__((always_inline)) {
         if constexpr (DGRAD) {
-            if (i_h == nkh || i_h == 0) {           // a pair begins
-                const uint16_t* R = i_h ? g.r1 : g.r0;
-                const uint16_t* C = i_h ? g.c1 : g.c0;
+            const int at_h = is.row0 + i_h;          // of both pairs' halves
+            const bool second = at_h >= nkh;
+            const int h = second ? at_h - nkh : at_h;
+            if (first || h == 0) {                   // the segment or a pair begins
+                const uint16_t* R = (second ? g.r1 : g.r0) + k_r + h * kBK;
+                const uint16_t* C = (second ? g.c1 : g.c0) + (static_cast<size_t>(is.e) * N + h * kBK + wave * 4 + half) * K;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    rp[q] = reinterpret_cast<const char*>(R + static_cast<size_t>(at[q]) * N + k_r);
-                    cp[q] = reinterpret_cast<const char*>(C + (static_cast<size_t>(is.e) * N + wave * 4 + q * 2 + half) * K +
+                    rp[q] = reinterpret_cast<const char*>(R + static_cast<size_t>(at[q]) * N);
+                    cp[q] = reinterpret_cast<const char*>(C + static_cast<size_t>(q * 2) * K +
                                                           min(is.col0 + chunk_c[q], K - 8));  // columns past K are never stored
                 }
                 step_r = kBK * 2;
                 step_c = static_cast<uint64_t>(kBK * 2) * K;
             }
-            const int h = i_h >= nkh ? i_h - nkh : i_h;
-            i_left = N / kBK - h;                   // whole halves
-            if (i_left <= 0) {                      // the one that ends past N: zeros there, of both operands
+            i_left = min(N / kBK - h, is.nh - i_h);  // whole halves
+            if (i_left <= 0) {                       // the one that ends past N: zeros there, of both operands
                 i_left = 1;
                 const int rest = N - h * kBK;
 #pragma unroll
@@ -283,7 +371,6 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
                     if (wave * 4 + q * 2 + half >= rest) cp[q] = zero;
                 }
             }
-            i_h += i_left;
         } else {
             // the row addresses of 16 halves, a row per lane
             id_par ^= 1;
@@ -291,65 +378,64 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
             const int r = is.r0 + (i_h + (lane >> 2)) * kBK + wave * 4 + (lane & 3);
             const bool real = r < is.r_end && p >= 0 && p < g.P;
             const int tok = fast_div(p, g.top_k);
-            const uint64_t z = reinterpret_cast<uint64_t>(zero);
-            const uint64_t y = reinterpret_cast<uint64_t>(g.r0 + static_cast<size_t>(real ? (g.r_tok ? tok : r) : 0) * N);
-            const uint64_t x = reinterpret_cast<uint64_t>(g.c0 + static_cast<size_t>(real ? (g.c_tok ? tok : r) : 0) * K);
-            s_ptr[wave * 64 + lane] = real ? ulonglong2{y, x} : ulonglong2{z, z};
+            s_ptr[wave * 64 + lane] = real ? ulonglong2{row_address(g.r0, g.r_tok ? tok : r, N), row_address(g.c0, g.c_tok ? tok : r, K)}
+                                           : ulonglong2{reinterpret_cast<uint64_t>(zero), reinterpret_cast<uint64_t>(zero)};
             row_p = s_ptr + wave * 64 + half;
             const int b = i_h / 16 + 1;
-            if (b * 16 < is.nh) load_ids(is, b, 0, id_par ^ 1);
-            else if (i_next) load_ids(in, 0, 0, id_par ^ 1);
+            const bool same = b * 16 < is.nh;
+            if (same || i_next) load_ids(same ? is : in, same ? b : 0, 0, id_par ^ 1);
             i_left = min(16, is.nh - i_h);
-            i_h += i_left;
         }
+        i_h += i_left;
     };
     // the cursor moves: within the segment (i_h: the first half not yet given out), or to the next
-    auto next = [&]() {
-        if (i_h > 0 && i_h < is.nh) {
-            if (!DGRAD && i_since < 3) wait_vmcnt<0>();
-            i_since = 0;
-            move();
-            return;
-        }
-        if (i_h > 0) {
-            if (!i_next) {
-                if constexpr (DGRAD) {
+    auto next = [&](bool start) __attribute__((always_inline)) {
+        const bool first = start || i_h >= is.nh;
+        if (first) {
+            if (!start) {
+                if (!i_next) {
+                    if constexpr (DGRAD) {
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) rp[q] = cp[q] = zero;
-                    step_r = 0;
-                    step_c = 0;
-                } else {
-                    s_ptr[wave * 64 + lane] = ulonglong2{reinterpret_cast<uint64_t>(zero), reinterpret_cast<uint64_t>(zero)};
-                    row_p = s_ptr + wave * 64 + half;
+                        for (int q = 0; q < 2; ++q) rp[q] = cp[q] = zero;
+                        step_r = 0;
+                        step_c = 0;
+                    } else {
+                        s_ptr[wave * 64 + lane] = ulonglong2{reinterpret_cast<uint64_t>(zero), reinterpret_cast<uint64_t>(zero)};
+                        row_p = s_ptr + wave * 64 + half;
+                    }
+                    i_left = 0x7fffffff;   // (at most 4 are computed and issued from here on)
+                    return;
                 }
-                i_left = 0x7fffffff;   // (at most 4 are computed and issued from here on)
-                return;
+                is = in;
+                ++i_seq;
+                i_next = next_seg(in);
             }
-            is = in;
             i_h = 0;
-            ++i_seq;
-            i_next = next_seg(in);
         }
-        // its ids: this wave's own loads of them, at least 3 halves ago (then the waits of the main loop cover them)
-        if (i_since < 3) wait_vmcnt<0>();
-        i_since = 0;
-        if constexpr (DGRAD) {
-            const int* ids = s_id + (i_seq & (kSegs - 1)) * kTile;
+        // the ids: this wave's own loads of them, at least 3 halves ago (then the waits of the main loop cover them)
+        if (!DGRAD || first) {
+            if (i_since < 3) wait_vmcnt<0>();
+            i_since = 0;
+        }
+        if (first) {
+            if constexpr (DGRAD) {
+                const int* ids = s_id + (i_seq & (kSegs - 1)) * kTile;
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int row = wave * 32 + q * 16 + (lane >> 2);
-                const int src = source(ids[row], is.r0 + row, is.r_end, g.r_tok);
-                at[q] = src >= 0 ? src : (g.r_tok ? 0 : is.r0);   // a row that is always there; not stored
-            }
-            if (i_next) load_ids(in, 0, i_seq + 1, 0);
-        } else {
+                for (int q = 0; q < 2; ++q) {
+                    const int row = wave * 32 + q * 16 + (lane >> 2);
+                    const int src = source(ids[row], is.r0 + row, is.r_end, g.r_tok);
+                    at[q] = src >= 0 ? src : (g.r_tok ? 0 : is.r0);   // a row that is always there; not stored
+                }
+                if (i_next) load_ids(in, 0, i_seq + 1, 0);
+            } else {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                col_r[q] = min(is.row0 + chunk_c[q], N - 8) * 2;   // (columns past the ends are never stored)
-                col_c[q] = min(is.col0 + chunk_c[q], K - 8) * 2;
+                for (int q = 0; q < 2; ++q) {
+                    col_r[q] = min(is.row0 + chunk_c[q], N - 8) * 2;   // (columns past the ends are never stored)
+                    col_c[q] = min(is.col0 + chunk_c[q], K - 8) * 2;
+                }
             }
         }
-        move();
+        move(first);
     };
 
     // Sources of the coming half (in the shadow of the MFMAs); then a load of each operand per q.
@@ -449,10 +535,11 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_setprio(0);
     };
-    // One half.  At the barriers this wave's loads of the next half have landed: vmcnt counts in order, and what may be
-    // in flight are the loads of two later halves (4 each) and, where an epilogue came not more than two halves ago
-    // (after), its stores.  (The first group needs the wait at the second barrier only, the second group at the first;
-    // at the other one it asks for what has landed before, or for what the next half will need.)
+    // One half, in two phases with a barrier at the end of each; the first group computes while the second reads.  At the
+    // barriers this wave's loads of the next half have landed: vmcnt counts in order, and what may be in flight are the
+    // loads of two later halves (4 each) and, in the two halves that follow an epilogue (after), its stores.  (The first
+    // group needs the wait at the second barrier only, the second group at the first; at the other one it asks for what
+    // has landed before, or for what the next half will need.)
     auto one_half = [&](auto rf_c, auto cf_c, auto first_c, bool after) __attribute__((always_inline)) {
         auto landed = [&]() __attribute__((always_inline)) {
             if (after) wait_vmcnt<8 + kStores>();
@@ -469,39 +556,139 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
         c_slot = (c_slot + kSlotB) & (kSlots * kSlotB - 1);
         ++i_since;
     };
+    using I1 = std::integral_constant<int, 1>;
+    using I2 = std::integral_constant<int, 2>;
+    using I4 = std::integral_constant<int, 4>;
+    using I8 = std::integral_constant<int, 8>;
 
+    // ---- Epilogue of tile cs.  Value v of block [i][j] is output row i16 of the block's rows and column gr * 4 + v of its
+    // columns.  Four neighbouring lanes, four rows, would store to four places, which the address unit takes one by one
+    // (16 rows of 64 bytes an instruction: 280 cycles each, and 1.4 x the time of the whole product where tiles are short);
+    // so 16 rows of 64 bytes at a time go through 1 KB of LDS of the wave's own, from which lane l reads 16 bytes
+    // of row l / 4 (110 cycles).  The 16-byte chunk c of row r is at c ^ (r / 4 & 3): no bank conflicts either way.
+    // Masked lanes store past the buffer's end, which the hardware drops: the number of stores is always the same.
+    // base: the loads of 16 rows are in flight while those before are added and stored.
+    Seg cs = {};
+    auto finish = [&]() __attribute__((always_inline)) {
+        constexpr int ES = F32 ? 4 : 2, PW = F32 ? 8 : 4;   // bytes of a value, 64-byte pieces of a wave's row
+        const size_t first = (DGRAD ? static_cast<size_t>(cs.r0) : static_cast<size_t>(cs.e) * N + cs.row0) * K + cs.col0;
+        auto resource = [&](const void* p) __attribute__((always_inline)) {
+            return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(uniform_ptr(static_cast<const char*>(p) + first * ES)), 0,
+                                                     0x7fffffff, 0x00020000);
+        };
+        const __amdgpu_buffer_rsrc_t out = resource(g.out);
+        // (opaque to the compiler, which would else keep the offsets below in registers through the main loop)
+        int ln = lane, wv = wave;
+        asm volatile("" : "+v"(ln), "+s"(wv));
+        const int em = wv >> 1, en = wv & 1, sr = ln >> 2;   // the row of this lane's pieces
+        char* const stage = s_stage + wv * 1024;
+        char* const mine = stage + sr * 64 + ((ln & 3) ^ (sr >> 2 & 3)) * 16;
+        const int br = ln & 15, bg = ln >> 4;                // row and columns of its values of a block
+        auto of_block = [&](int chunk) __attribute__((always_inline)) { return stage + br * 64 + (chunk ^ (br >> 2)) * 16; };
+        uint32_t ok = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int rl = i * 64 + em * 16 + sr;
+            bool in;
+            if constexpr (DGRAD) in = source(s_id[(c_seq & (kSegs - 1)) * kTile + rl], cs.r0 + rl, cs.r_end, 0) >= 0;
+            else in = cs.row0 + rl < N;
+            ok |= in ? 1u << i : 0u;
+        }
+        const int col0 = F32 ? en * 32 + (ln & 3) * 4 : en * 32 + (ln & 3) * 8;
+        const uint32_t off0 = (static_cast<uint32_t>(em * 16 + sr) * K + col0) * ES, row64 = static_cast<uint32_t>(K) * (64 * ES);
+        auto offset = [&](int i, int q) __attribute__((always_inline)) -> uint32_t {   // of piece q of row i
+            const int col = F32 ? (q >> 1) * 64 + (q & 1) * 16 : q * 64;
+            const uint32_t at = off0 + i * row64 + col * ES;
+            const bool in = static_cast<bool>(ok >> i & 1) & (cs.col0 + col0 + col < K);
+            return in ? at : 0x80000000u;
+        };
+        auto store = [&](auto base_c) __attribute__((always_inline)) {
+            constexpr bool BASE = decltype(base_c)::value;
+            constexpr int STEPS = PW;   // 4 rows of PW pieces, 4 pieces a step
+            __amdgpu_buffer_rsrc_t in = out;
+            u32x4 old[2][4], w[2][4];
+            auto of_step = [&](int n, int q) __attribute__((always_inline)) { return F32 ? offset(n >> 1, (n & 1) * 4 + q) : offset(n, q); };
+            auto fetch = [&](int n) __attribute__((always_inline)) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) old[n & 1][q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(in, of_step(n, q), 0, 0));
+            };
+            auto through_lds = [&](int n) __attribute__((always_inline)) {
+                const int i = F32 ? n >> 1 : n;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if constexpr (F32) {
+                        *reinterpret_cast<f32x4*>(of_block(bg)) = acc[i][(n & 1) * 4 + q];
+                    } else {
+                        f32x4 a = acc[i][2 * q], b = acc[i][2 * q + 1];
+                        char* const lo = of_block(bg >> 1) + (bg & 1) * 8;
+                        char* const hi = of_block(2 + (bg >> 1)) + (bg & 1) * 8;
+                        if constexpr (BASE) {   // added before the rounding, in the blocks' layout
+                            *reinterpret_cast<u32x4*>(mine) = old[n & 1][q];
+                            const u32x2 x = *reinterpret_cast<const u32x2*>(lo), y = *reinterpret_cast<const u32x2*>(hi);
+                            a += f32x4{lo_f32(x[0]), hi_f32(x[0]), lo_f32(x[1]), hi_f32(x[1])};
+                            b += f32x4{lo_f32(y[0]), hi_f32(y[0]), lo_f32(y[1]), hi_f32(y[1])};
+                        }
+                        *reinterpret_cast<u32x2*>(lo) = u32x2{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3])};
+                        *reinterpret_cast<u32x2*>(hi) = u32x2{pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])};
+                    }
+                    w[n & 1][q] = *reinterpret_cast<const u32x4*>(mine);
+                }
+            };
+            if constexpr (BASE) {
+                in = resource(g.base);
+                fetch(0);
+            }
+            through_lds(0);
+#pragma unroll
+            for (int n = 0; n < STEPS; ++n) {   // a step's results leave while the next one's come from LDS
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (BASE)
+                    if (n + 1 < STEPS) fetch(n + 1);
+                u32x4 sum[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    sum[q] = w[n & 1][q];
+                    if constexpr (F32 && BASE) sum[q] = __builtin_bit_cast(u32x4, __builtin_bit_cast(f32x4, sum[q]) + __builtin_bit_cast(f32x4, old[n & 1][q]));
+                }
+                if (n + 1 < STEPS) through_lds(n + 1);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) __builtin_amdgcn_raw_buffer_store_b128(sum[q], out, of_step(n, q), 0, 0);
+            }
+        };
+        if (!DGRAD && g.base) store(std::true_type{});
+        else store(std::false_type{});
+        ++c_seq;
+    };
+
+    // ---- main loop
+    int c_n = 0;
     const bool any = next_seg(is);
     if (any) {
         load_ids(is, 0, 0, 0);
         i_next = next_seg(in);
-        next();
+        next(true);
+#pragma nounroll
         for (int q = 0; q < 3 + group; ++q) {
             read_rows();
             sources(0);
             sources(1);
             load_r(0); load_r(1); load_c(0); load_c(1);
-            if (--i_left == 0) next();   // (i_since stays 0: nothing has been waited for)
+            if (--i_left == 0) next(false);   // (i_since stays 0: nothing has been waited for)
         }
         wait_vmcnt<8>();
         barrier();
         if (group) barrier();
     }
-    int c_n = 0;
-    Seg cs;
     while (find(c_n, cs)) {
         const int n_rows = DGRAD ? cs.r_end - cs.r0 : N - cs.row0, n_cols = K - cs.col0;
-        using I1 = std::integral_constant<int, 1>;
-        using I2 = std::integral_constant<int, 2>;
-        using I4 = std::integral_constant<int, 4>;
-        using I8 = std::integral_constant<int, 8>;
         const bool again = c_seq > 0;
         if (cs.nh > 0 && n_rows > 128 && n_cols > 128) {
             one_half(I4{}, I8{}, std::true_type{}, again);
-            if (--i_left == 0) next();
+            if (--i_left == 0) next(false);
             int left = cs.nh - 1;
             if (left > 0) {
                 one_half(I4{}, I8{}, std::false_type{}, again);
-                if (--i_left == 0) next();
+                if (--i_left == 0) next(false);
                 --left;
             }
             while (left > 0) {
@@ -509,7 +696,7 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
                 for (int r = 0; r < run; ++r) one_half(I4{}, I8{}, std::false_type{}, false);
                 left -= run;
                 i_left -= run;
-                if (i_left == 0) next();
+                if (i_left == 0) next(false);
             }
         } else {
             // fewer blocks hold rows or columns (or the expert has no rows)
@@ -520,97 +707,60 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
             auto some = [&](auto rf_c, auto cf_c) __attribute__((always_inline)) {
                 for (int h = 0; h < cs.nh; ++h) {
                     one_half(rf_c, cf_c, std::false_type{}, again && h < 2);
-                    if (--i_left == 0) next();
+                    if (--i_left == 0) next(false);
                 }
             };
             if (n_rows > 128) some(I4{}, I4{});
             else if (n_rows > 64) some(I2{}, I8{});
             else some(I1{}, I8{});
         }
-
-        // ---- epilogue.  Value v of block [i][j] is output row i16 of the block's rows and column gr * 4 + v of its
-        // columns.  bf16: two blocks of neighbouring columns are exchanged between the 16-lane groups gr and gr ^ 1, so
-        // that a lane gets 8 adjacent columns; a store instruction writes 16 rows of 64 adjacent bytes either way.
-        // Masked lanes store past the buffer's end, which the hardware drops: the number of stores is always the same.
-        // base: the loads of 64 rows are in flight while those before are added and stored.
-        constexpr int ES = F32 ? 4 : 2, PW = F32 ? 8 : 4;   // bytes of a value, 16-byte pieces of a row and lane
-        const size_t first = (DGRAD ? static_cast<size_t>(cs.r0) : static_cast<size_t>(cs.e) * N + cs.row0) * K + cs.col0;
-        auto resource = [&](const void* p) __attribute__((always_inline)) {
-            return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(uniform_ptr(static_cast<const char*>(p) + first * ES)), 0,
-                                                     0x7fffffff, 0x00020000);
-        };
-        const __amdgpu_buffer_rsrc_t out = resource(g.out);
-        // (opaque to the compiler, which would else keep the offsets below in registers through the main loop)
-        int ln = lane, wv = wave;
-        asm volatile("" : "+v"(ln), "+s"(wv));
-        const int er = ln & 15, eg = ln >> 4, em = wv >> 1, en = wv & 1;
-        uint32_t ok = 0;   // rows i of this lane that are stored
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int rl = i * 64 + em * 16 + er;
-            bool in;
-            if constexpr (DGRAD) in = source(s_id[(c_seq & (kSegs - 1)) * kTile + rl], cs.r0 + rl, cs.r_end, 0) >= 0;
-            else in = cs.row0 + rl < N;
-            ok |= in ? 1u << i : 0u;
-        }
-        auto offset = [&](int i, int q) __attribute__((always_inline)) -> uint32_t {   // of piece q of row i
-            const int col = F32 ? (q >> 1) * 64 + en * 32 + (q & 1) * 16 + eg * 4 : q * 64 + en * 32 + (eg & 1) * 16 + (eg >> 1) * 8;
-            const bool in = (ok >> i & 1) && cs.col0 + col < K;
-            return in ? (static_cast<uint32_t>(i * 64 + em * 16 + er) * K + col) * ES : 0x80000000u;
-        };
-        auto exchange = [&](u32x4& w) __attribute__((always_inline)) {   // its own inverse
-#pragma unroll
-            for (int d = 0; d < 2; ++d) {
-                const auto r = __builtin_amdgcn_permlane16_swap(w[d], w[2 + d], false, false);
-                w[d] = r[0];
-                w[2 + d] = r[1];
-            }
-        };
-        auto finish = [&](auto base_c) __attribute__((always_inline)) {
-            constexpr bool BASE = decltype(base_c)::value;
-            __amdgpu_buffer_rsrc_t in = out;
-            u32x4 old[2][PW];
-            auto fetch = [&](int i) __attribute__((always_inline)) {
-#pragma unroll
-                for (int q = 0; q < PW; ++q) old[i & 1][q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(in, offset(i, q), 0, 0));
-            };
-            if constexpr (BASE) {
-                in = resource(g.base);
-                fetch(0);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                __builtin_amdgcn_sched_barrier(0);
-                if constexpr (BASE)
-                    if (i < 3) fetch(i + 1);
-#pragma unroll
-                for (int q = 0; q < PW; ++q) {
-                    u32x4 w;
-                    if constexpr (F32) {
-                        f32x4 v = acc[i][q];
-                        if constexpr (BASE) v += __builtin_bit_cast(f32x4, old[i & 1][q]);
-                        w = __builtin_bit_cast(u32x4, v);
-                    } else {
-                        f32x4 a = acc[i][2 * q], b = acc[i][2 * q + 1];
-                        if constexpr (BASE) {
-                            u32x4 o = old[i & 1][q];
-                            exchange(o);    // back to the blocks' columns
-                            a += f32x4{lo_f32(o[0]), hi_f32(o[0]), lo_f32(o[1]), hi_f32(o[1])};
-                            b += f32x4{lo_f32(o[2]), hi_f32(o[2]), lo_f32(o[3]), hi_f32(o[3])};
-                        }
-                        w = u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])};
-                        exchange(w);
-                    }
-                    __builtin_amdgcn_raw_buffer_store_b128(w, out, offset(i, q), 0, 0);
-                }
-            }
-        };
-        if (!DGRAD && g.base) finish(std::true_type{});
-        else finish(std::false_type{});
-        ++c_seq;
+        if (pieces > 1) break;      // a piece is not a tile yet
+        finish();
     }
     if (any && !group) barrier();   // the other group's last
     wait_vmcnt<0>();                // the halves of zeros: nothing may land in LDS after the end
+
+    // ---- A piece of a tile: its partial sums through the workspace.  They are written and read with device-coherent
+    // accesses (sc1), complete (vmcnt) before the piece is counted on the tile's counter.  The last piece to arrive adds
+    // all of them in the pieces' order, so that the result does not depend on which it is, stores the tile and resets the
+    // counter.  Nobody waits for anybody.
+    if (pieces > 1 && static_cast<int>(blockIdx.x) < pieces * T) {
+        constexpr int kSc1 = 16;
+        const int t = blockIdx.x % T;
+        const __amdgpu_buffer_rsrc_t part = __builtin_amdgcn_make_buffer_rsrc(g.part, 0, kMaxPieces * kTile * kTile * 4, 0x00020000);
+        auto at_part = [&](int piece) __attribute__((always_inline)) {   // [piece][16-byte chunk][thread]
+            return (static_cast<uint32_t>(piece) * T + t) * (kTile * kTile * 4) + tid * 16;
+        };
+        uint32_t o = at_part(blockIdx.x / T);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[i][j]), part, o + (i * 8 + j) * (kNT * 16), 0, kSc1);
+        wait_vmcnt<0>();
+        __syncthreads();
+        if (tid == 0) s_arrived = __hip_atomic_fetch_add(&g.cnt[t], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        if (s_arrived != pieces - 1) return;
+        if (tid == 0) __hip_atomic_store(&g.cnt[t], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma nounroll
+        for (int piece = 0; piece < pieces; ++piece) {
+            o = at_part(piece);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                u32x4 v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(part, o + (i * 8 + j) * (kNT * 16), 0, kSc1));
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[i][j] += __builtin_bit_cast(f32x4, v[j]);
+            }
+        }
+        finish();
+    }
 }
 
 FastDiv make_div(uint32_t d) {
@@ -636,25 +786,33 @@ hipError_t device_cus(int& cus) {
     return hipSuccess;
 }
 
-// one workgroup per compute unit (128 KB of LDS each), in whole rounds over the 8 XCDs, or one per tile
-hipError_t grid_for(int64_t tiles, int& grid) {
+// One workgroup per compute unit (128 KB of LDS each), in whole rounds over the 8 XCDs; one per tile where there are
+// fewer and no workspace to cut them in.
+hipError_t grid_for(int64_t tiles, bool ws, int& grid) {
     int cus = 0;
     const hipError_t err = device_cus(cus);
     if (err != hipSuccess) return err;
     const int64_t most = cus / 8 * 8 > 8 ? cus / 8 * 8 : 8, want = (tiles + 7) / 8 * 8;
-    grid = static_cast<int>(want < most ? want : most);
+    grid = static_cast<int>(ws || want > most ? most : want);
     return hipSuccess;
 }
 
+// the workspace of the grouped GEMMs: counters, then partial tiles (the entry points check its size)
+constexpr int64_t kCounterBytes = 4096;
+int32_t* counters(void* ws) { return static_cast<int32_t*>(ws); }
+float* partials(void* ws) { return ws ? reinterpret_cast<float*>(static_cast<char*>(ws) + kCounterBytes) : nullptr; }
+
 }  // namespace
+
+int64_t grad_gemm_workspace_bytes() { return kCounterBytes + static_cast<int64_t>(kMaxPieces) * kTile * kTile * 4; }
 
 hipError_t launch_dgrad(const uint16_t* dy0, const uint16_t* w0, const uint16_t* dy1, const uint16_t* w1, uint16_t* dx,
                         const int32_t* sorted_ids, const int32_t* offsets, int P, int top_k, int E, int N, int K,
-                        int max_pad, int by_token, void* ws, int64_t ws_bytes, hipStream_t s) {
-    GradArgs g{dy0, dy1, w0, w1, dx, nullptr, sorted_ids, offsets, make_div(top_k), P, E, N, K, max_pad, by_token, 0};
+                        int max_pad, int by_token, void* ws, hipStream_t s) {
+    GradArgs g{dy0, dy1, w0, w1, dx, nullptr, sorted_ids, offsets, make_div(top_k), P, E, N, K, max_pad, by_token, 0, counters(ws), partials(ws)};
     const int64_t m = static_cast<int64_t>(max_pad) / kTile + (P < E ? P : E), n = (K + kTile - 1) / kTile;
     int grid = 0;
-    const hipError_t err = grid_for(m * n, grid);
+    const hipError_t err = grid_for(m * n, ws != nullptr, grid);
     if (err != hipSuccess) return err;
     grad_gemm_kernel<true, false><<<grid, kNT, 0, s>>>(g);
     return hipGetLastError();
@@ -662,10 +820,10 @@ hipError_t launch_dgrad(const uint16_t* dy0, const uint16_t* w0, const uint16_t*
 
 hipError_t launch_wgrad(const uint16_t* dy, const uint16_t* x, void* dw, const void* base, bool f32,
                         const int32_t* sorted_ids, const int32_t* offsets, int P, int top_k, int E, int N, int K,
-                        int max_pad, int dy_by_token, int x_by_token, void* ws, int64_t ws_bytes, hipStream_t s) {
-    GradArgs g{dy, nullptr, x, nullptr, dw, base, sorted_ids, offsets, make_div(top_k), P, E, N, K, max_pad, dy_by_token, x_by_token};
+                        int max_pad, int dy_by_token, int x_by_token, void* ws, hipStream_t s) {
+    GradArgs g{dy, nullptr, x, nullptr, dw, base, sorted_ids, offsets, make_div(top_k), P, E, N, K, max_pad, dy_by_token, x_by_token, counters(ws), partials(ws)};
     int grid = 0;
-    const hipError_t err = grid_for(static_cast<int64_t>(E) * ((N + kTile - 1) / kTile) * ((K + kTile - 1) / kTile), grid);
+    const hipError_t err = grid_for(static_cast<int64_t>(E) * ((N + kTile - 1) / kTile) * ((K + kTile - 1) / kTile), ws != nullptr, grid);
     if (err != hipSuccess) return err;
     if (f32) grad_gemm_kernel<false, true><<<grid, kNT, 0, s>>>(g);
     else grad_gemm_kernel<false, false><<<grid, kNT, 0, s>>>(g);

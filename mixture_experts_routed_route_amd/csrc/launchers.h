@@ -117,13 +117,15 @@ hipError_t launch_silu_mul_backward(const uint16_t* g, const uint16_t* u, const 
                                     hipStream_t s);
 hipError_t launch_route_backward(const int32_t* ids, const float* w, const float* dw, const float* logits, int T, int E,
                                  int k, float* out, hipStream_t s);
-// grad_gemm.hip: grouped products for the gradients of inputs (dy1 NULL: one pair) and of weights
+// grad_gemm.hip: grouped products for the gradients of inputs (dy1 NULL: one pair) and of weights (ws: optional, at
+// least grad_gemm_workspace_bytes(), its counters zero before the first use)
+int64_t grad_gemm_workspace_bytes();
 hipError_t launch_dgrad(const uint16_t* dy0, const uint16_t* w0, const uint16_t* dy1, const uint16_t* w1, uint16_t* dx,
                         const int32_t* sorted_ids, const int32_t* offsets, int P, int top_k, int E, int N, int K,
-                        int max_pad, int by_token, void* ws, int64_t ws_bytes, hipStream_t s);
+                        int max_pad, int by_token, void* ws, hipStream_t s);
 hipError_t launch_wgrad(const uint16_t* dy, const uint16_t* x, void* dw, const void* base, bool f32,
                         const int32_t* sorted_ids, const int32_t* offsets, int P, int top_k, int E, int N, int K,
-                        int max_pad, int dy_by_token, int x_by_token, void* ws, int64_t ws_bytes, hipStream_t s);
+                        int max_pad, int dy_by_token, int x_by_token, void* ws, hipStream_t s);
 
 // probes.hip (ceiling probes, not steps of the path)
 hipError_t launch_probe_stream_read(const void* src, int64_t bytes, uint32_t* sink, int blocks, hipStream_t s);
