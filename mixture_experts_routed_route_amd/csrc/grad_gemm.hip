@@ -82,13 +82,22 @@ struct Seg {
 };
 enum { kEnd, kSkip, kIsTile };
 
+// a tile as the main loop wants it, located in advance
+struct __attribute__((aligned(16))) Entry {
+    int r0, r_end, row0, col0;   // as in Seg
+    int nh, e;                   // halves (-1: no more tiles), expert
+    uint64_t out;                // first value of the tile's results
+    uint64_t w;                  // dgrad: first value of the expert's matrix
+};
+
 // DGRAD: bf16 out; else wgrad with bf16 (F32 false) or fp32 results
 template <bool DGRAD, bool F32>
 __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     __shared__ __attribute__((aligned(1024))) char smem[kSlots * kSlotB];
     __shared__ int s_lo[kMaxE], s_hi[kMaxE], s_tb[kMaxE + 1], s_order[kMaxE];
     __shared__ int s_scan[kNT / 64];
-    __shared__ int4 s_tab[kTab], s_tab2[kTab];
+    __shared__ Entry s_tab[kTab];
+    __shared__ int s_n, s_ends;   // entries in it, and whether they are all
     __shared__ int s_mine[64];    // wgrad, unequal experts: this workgroup's tiles
     __shared__ int s_arrived;
     __shared__ __attribute__((aligned(1024))) char s_stage[kNT / 64 * 1024];   // a wave's results on their way out
@@ -202,6 +211,7 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
         if (levelled) {
             if (wave == 0) {
                 int load = lane < per_xcd ? 0 : 0x3fffffff, n = 0;
+                s_mine[lane] = -1;
                 for (int v = 0; v < xcd_units; ++v) {
                     const int u = unit_at(v);
                     if (u >= units) break;
@@ -218,7 +228,6 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
                         ++n;
                     }
                 }
-                if (lane == slot && n < 64) s_mine[n] = -1;
             }
             __syncthreads();
         }
@@ -261,40 +270,41 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
         }
         return kIsTile;
     };
+    auto entry_of = [&](const Seg& t) __attribute__((always_inline)) {
+        const uint64_t row = DGRAD ? static_cast<uint64_t>(t.r0) : static_cast<uint64_t>(t.e) * N + t.row0;
+        return Entry{t.r0, t.r_end, t.row0, t.col0, t.nh, t.e, row * K + t.col0, static_cast<uint64_t>(t.e) * N * K};
+    };
     // the first entries, located once by a thread each (a dependent chain of divisions and searches)
-    if (tid < kTab) {
-        Seg s = {};
-        const int is_tile = locate(tid, s);
-        s_tab[tid] = int4{is_tile, s.e, s.r0, s.r_end};
-        s_tab2[tid] = int4{s.row0, s.col0, s.nh, 0};
-    }
-    __syncthreads();
-    // the next tile at or after entry n; false: none.  n moves past it.
-    auto find = [&](int& n, Seg& s) __attribute__((always_inline)) -> bool {
-        for (;;) {
-            int is_tile;
-            if (n < kTab) {
-                const int4 a = s_tab[n], b = s_tab2[n];
-                is_tile = a.x;
-                s = Seg{a.y, a.z, a.w, b.x, b.y, b.z};
-            } else {
-                is_tile = locate(n, s);
-            }
-            is_tile = __builtin_amdgcn_readfirstlane(is_tile);
-            s.e = __builtin_amdgcn_readfirstlane(s.e);
-            s.r0 = __builtin_amdgcn_readfirstlane(s.r0);
-            s.r_end = __builtin_amdgcn_readfirstlane(s.r_end);
-            s.row0 = __builtin_amdgcn_readfirstlane(s.row0);
-            s.col0 = __builtin_amdgcn_readfirstlane(s.col0);
-            s.nh = __builtin_amdgcn_readfirstlane(s.nh);
-            if (is_tile == kEnd) return false;
-            ++n;
-            if (is_tile == kIsTile) return true;
+    {
+        Seg t = {};
+        const int is_tile = tid < kTab ? locate(tid, t) : kEnd;
+        const int at = block_inclusive_scan<kNT / 64>(is_tile == kIsTile ? 1 : 0, s_scan, kTab / 64) - 1;
+        if (is_tile == kIsTile) s_tab[at] = entry_of(t);
+        if (tid == kTab - 1) {
+            s_n = at + 1;
+            s_ends = is_tile == kEnd;
         }
+        __syncthreads();
+    }
+    const int tab_n = __builtin_amdgcn_readfirstlane(s_n);
+    const bool tab_ends = __builtin_amdgcn_readfirstlane(s_ends);
+    // tile number n of this workgroup, for n = 0, 1, ... in turn (raw: the place in the list behind the table)
+    auto tile = [&](int n, int& raw) __attribute__((always_inline)) {
+        Entry t;
+        t.nh = -1;
+        if (n < tab_n) {
+            t = s_tab[n];
+        } else if (!tab_ends) {
+            Seg x = {};
+            int is_tile;
+            do is_tile = __builtin_amdgcn_readfirstlane(locate(raw++, x)); while (is_tile == kSkip);
+            if (is_tile == kIsTile) t = entry_of(x);
+        }
+        return t;
     };
 
     // address of row `row` of an operand of `width` columns (one 32 x 32 bit product)
-    auto row_address = [](const uint16_t* p, int row, int width) __attribute__((always_inline)) {
+    auto row_address = [](const void* p, int row, int width) __attribute__((always_inline)) {
         uint32_t bytes = static_cast<uint32_t>(width) * 2;
         asm volatile("" : "+s"(bytes));   // (keeps the compiler from widening it first)
         return reinterpret_cast<uint64_t>(p) + static_cast<uint64_t>(static_cast<uint32_t>(row)) * bytes;
@@ -311,24 +321,23 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     // the cursor has to be moved (move()): to the half that ends past N and to the second pair (dgrad), to the next 16
     // ids (wgrad), to the next segment, and behind the last one to halves of zeros that nobody reads, so that the main
     // loop needs no tests.
-    int i_n = 0, i_seq = 0, i_h = 0, i_left = 0, i_since = 0, i_slot = 0, id_par = 1;
-    Seg is, in;                 // the segment whose halves are loaded, and the next one with any
-    bool i_next;
-    auto next_seg = [&](Seg& s) __attribute__((always_inline)) -> bool {
-        for (;;) {
-            if (!find(i_n, s)) return false;
-            if (s.nh > 0) return true;
-        }
+    int i_n = 1, i_raw = kTab, i_seq = 0, i_h = 0, i_left = 0, i_since = 0, i_slot = 0, id_par = 1;
+    Entry is = tile(0, i_raw), in = {};      // the tile whose halves are loaded, and the next one (uniform)
+    int is_nh = __builtin_amdgcn_readfirstlane(is.nh);
+    bool i_next = false;
+    auto look_ahead = [&]() __attribute__((always_inline)) {   // tiles without halves come last
+        in = tile(i_n++, i_raw);
+        i_next = __builtin_amdgcn_readfirstlane(in.nh) > 0;
     };
     // Ids that this wave's loads need, straight into LDS (rows past max_pad read the last id; checked where
     // used).  dgrad: the wave's 32 rows of tile number seq.  wgrad: its 4 rows of each of 16 halves.
-    auto load_ids = [&](const Seg& s, int batch, int seq, int par) __attribute__((always_inline)) {
+    auto load_ids = [&](int r0, int batch, int seq, int par) __attribute__((always_inline)) {
         if constexpr (DGRAD) {
             if (lane < 32)
-                dma4(g.sorted_ids + min(s.r0 + wave * 32 + lane, g.max_pad - 1),
+                dma4(g.sorted_ids + min(r0 + wave * 32 + lane, g.max_pad - 1),
                      lds_id + ((seq & (kSegs - 1)) * kTile + wave * 32) * 4);
         } else {
-            const int r = s.r0 + (batch * 16 + (lane >> 2)) * kBK + wave * 4 + (lane & 3);
+            const int r = r0 + (batch * 16 + (lane >> 2)) * kBK + wave * 4 + (lane & 3);
             dma4(g.sorted_ids + min(r, g.max_pad - 1), lds_id + (wave * 2 + par) * 256);
         }
     };
@@ -339,29 +348,31 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     uint32_t step_r = 0;
     uint64_t step_c = 0;
     int at[2], chunk_c[2], col_r[2], col_c[2];
+    uint32_t lane_c[2];         // dgrad: bytes from a half's first row of W to this lane's
 #pragma unroll
     for (int q = 0; q < 2; ++q) chunk_c[q] = ((lane & 31) ^ (((q * 2 + half) << 2) | ((((wave >> 1) ^ (wave >> 2)) & 1) << 1))) * 8;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) lane_c[q] = static_cast<uint32_t>(wave * 4 + q * 2 + half) * (static_cast<uint32_t>(K) * 2);
     const int k_r = ((lane & 3) ^ ((lane >> 4) & 3)) * 8;   // dgrad: first n of this lane's chunk of a row of dy
     const ulonglong2* row_p = s_ptr;   // wgrad: the row addresses of the coming half
     // what can be issued from half i_h of the segment on
     auto move = [&](bool first) __attribute__((always_inline)) {
         if constexpr (DGRAD) {
-            const int at_h = is.row0 + i_h;          // of both pairs' halves
+            const int at_h = __builtin_amdgcn_readfirstlane(is.row0) + i_h;   // of both pairs' halves
             const bool second = at_h >= nkh;
             const int h = second ? at_h - nkh : at_h;
-            if (first || h == 0) {                   // the segment or a pair begins
-                const uint16_t* R = (second ? g.r1 : g.r0) + k_r + h * kBK;
-                const uint16_t* C = (second ? g.c1 : g.c0) + (static_cast<size_t>(is.e) * N + h * kBK + wave * 4 + half) * K;
+            if (first || h == 0) {                   // the tile or a pair begins
+                const char* R = reinterpret_cast<const char*>((second ? g.r1 : g.r0) + h * kBK);
+                const char* C = reinterpret_cast<const char*>((second ? g.c1 : g.c0) + is.w + static_cast<uint64_t>(h * kBK) * K);
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    rp[q] = reinterpret_cast<const char*>(R + static_cast<size_t>(at[q]) * N);
-                    cp[q] = reinterpret_cast<const char*>(C + static_cast<size_t>(q * 2) * K +
-                                                          min(is.col0 + chunk_c[q], K - 8));  // columns past K are never stored
+                    rp[q] = reinterpret_cast<const char*>(row_address(R, at[q], N)) + k_r * 2;
+                    cp[q] = C + lane_c[q] + min(is.col0 + chunk_c[q], K - 8) * 2;  // columns past K are never stored
                 }
                 step_r = kBK * 2;
                 step_c = static_cast<uint64_t>(kBK * 2) * K;
             }
-            i_left = min(N / kBK - h, is.nh - i_h);  // whole halves
+            i_left = min(N / kBK - h, is_nh - i_h);  // whole halves
             if (i_left <= 0) {                       // the one that ends past N: zeros there, of both operands
                 i_left = 1;
                 const int rest = N - h * kBK;
@@ -382,15 +393,15 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
                                            : ulonglong2{reinterpret_cast<uint64_t>(zero), reinterpret_cast<uint64_t>(zero)};
             row_p = s_ptr + wave * 64 + half;
             const int b = i_h / 16 + 1;
-            const bool same = b * 16 < is.nh;
-            if (same || i_next) load_ids(same ? is : in, same ? b : 0, 0, id_par ^ 1);
-            i_left = min(16, is.nh - i_h);
+            const bool same = b * 16 < is_nh;
+            if (same || i_next) load_ids(same ? is.r0 : in.r0, same ? b : 0, 0, id_par ^ 1);
+            i_left = min(16, is_nh - i_h);
         }
         i_h += i_left;
     };
     // the cursor moves: within the segment (i_h: the first half not yet given out), or to the next
     auto next = [&](bool start) __attribute__((always_inline)) {
-        const bool first = start || i_h >= is.nh;
+        const bool first = start || i_h >= is_nh;
         if (first) {
             if (!start) {
                 if (!i_next) {
@@ -407,9 +418,10 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
                     return;
                 }
                 is = in;
+                is_nh = __builtin_amdgcn_readfirstlane(is.nh);
                 ++i_seq;
-                i_next = next_seg(in);
             }
+            look_ahead();
             i_h = 0;
         }
         // the ids: this wave's own loads of them, at least 3 halves ago (then the waits of the main loop cover them)
@@ -426,7 +438,7 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
                     const int src = source(ids[row], is.r0 + row, is.r_end, g.r_tok);
                     at[q] = src >= 0 ? src : (g.r_tok ? 0 : is.r0);   // a row that is always there; not stored
                 }
-                if (i_next) load_ids(in, 0, i_seq + 1, 0);
+                if (i_next) load_ids(in.r0, 0, i_seq + 1, 0);
             } else {
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
@@ -568,12 +580,11 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     // of row l / 4 (110 cycles).  The 16-byte chunk c of row r is at c ^ (r / 4 & 3): no bank conflicts either way.
     // Masked lanes store past the buffer's end, which the hardware drops: the number of stores is always the same.
     // base: the loads of 16 rows are in flight while those before are added and stored.
-    Seg cs = {};
+    Entry cs = {};
     auto finish = [&]() __attribute__((always_inline)) {
         constexpr int ES = F32 ? 4 : 2, PW = F32 ? 8 : 4;   // bytes of a value, 64-byte pieces of a wave's row
-        const size_t first = (DGRAD ? static_cast<size_t>(cs.r0) : static_cast<size_t>(cs.e) * N + cs.row0) * K + cs.col0;
         auto resource = [&](const void* p) __attribute__((always_inline)) {
-            return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(uniform_ptr(static_cast<const char*>(p) + first * ES)), 0,
+            return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(uniform_ptr(static_cast<const char*>(p) + cs.out * ES)), 0,
                                                      0x7fffffff, 0x00020000);
         };
         const __amdgpu_buffer_rsrc_t out = resource(g.out);
@@ -661,11 +672,9 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     };
 
     // ---- main loop
-    int c_n = 0;
-    const bool any = next_seg(is);
+    const bool any = is_nh > 0;
     if (any) {
-        load_ids(is, 0, 0, 0);
-        i_next = next_seg(in);
+        load_ids(is.r0, 0, 0, 0);
         next(true);
 #pragma nounroll
         for (int q = 0; q < 3 + group; ++q) {
@@ -679,13 +688,18 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
         barrier();
         if (group) barrier();
     }
-    while (find(c_n, cs)) {
-        const int n_rows = DGRAD ? cs.r_end - cs.r0 : N - cs.row0, n_cols = K - cs.col0;
-        const bool again = c_seq > 0;
-        if (cs.nh > 0 && n_rows > 128 && n_cols > 128) {
+    int c_raw = kTab;
+    for (int n = 0;; ++n) {
+        cs = tile(n, c_raw);
+        const int nh = __builtin_amdgcn_readfirstlane(cs.nh);
+        if (nh < 0) break;
+        const int n_rows = __builtin_amdgcn_readfirstlane(DGRAD ? cs.r_end - cs.r0 : N - cs.row0);
+        const int n_cols = __builtin_amdgcn_readfirstlane(K - cs.col0);
+        const bool again = n > 0;
+        if (nh > 0 && n_rows > 128 && n_cols > 128) {
             one_half(I4{}, I8{}, std::true_type{}, again);
             if (--i_left == 0) next(false);
-            int left = cs.nh - 1;
+            int left = nh - 1;
             if (left > 0) {
                 one_half(I4{}, I8{}, std::false_type{}, again);
                 if (--i_left == 0) next(false);
@@ -705,7 +719,7 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
             auto some = [&](auto rf_c, auto cf_c) __attribute__((always_inline)) {
-                for (int h = 0; h < cs.nh; ++h) {
+                for (int h = 0; h < nh; ++h) {
                     one_half(rf_c, cf_c, std::false_type{}, again && h < 2);
                     if (--i_left == 0) next(false);
                 }
