@@ -49,7 +49,8 @@ extern "C" {
  * rows are not written.  Without sorted_ids every row r is pair r.
  *   gate, up, out  bf16 [rows, n]; out may be gate or up
  *   p_drop         in [0, 1); rng may be NULL where it is 0
- * n % 8 == 0.  rows == 0, or num_pairs == 0 with sorted_ids, enqueues nothing. */
+ * n % 8 == 0, rows * n up to 2^35 (MOE_EUNSUPPORTED above).  rows == 0, or num_pairs == 0 with sorted_ids,
+ * enqueues nothing. */
 moe_status moe_silu_mul_dropout(const uint16_t* gate, const uint16_t* up, uint16_t* out, const int32_t* sorted_ids,
                                 int64_t num_pairs, int64_t rows, int32_t n, double p_drop, const int64_t* rng,
                                 moe_stream stream);
@@ -64,7 +65,8 @@ moe_status moe_silu_mul_dropout(const uint16_t* gate, const uint16_t* up, uint16
  *   topk_w fp32 [num_pairs]; without sorted_ids every row r is pair r, and num_pairs >= rows.
  * Each of d_gate, d_up and h_weighted may be one of gate, up and d (not two of them the same buffer).
  * Rows without a pair are not written, nor are the d_topk_w of pairs without a row (an expert id out of
- * range).  n % 8 == 0.  rows == 0, or num_pairs == 0 with sorted_ids, enqueues nothing. */
+ * range).  n % 8 == 0, rows below 2^24 (MOE_EUNSUPPORTED above).  rows == 0, or num_pairs == 0 with sorted_ids,
+ * enqueues nothing. */
 moe_status moe_silu_mul_backward(const uint16_t* gate, const uint16_t* up, const uint16_t* d, const float* topk_w,
                                  const int32_t* sorted_ids, int64_t num_pairs, int64_t rows, int32_t n,
                                  double p_drop, const int64_t* rng, uint16_t* d_gate, uint16_t* d_up,
@@ -74,8 +76,8 @@ moe_status moe_silu_mul_backward(const uint16_t* gate, const uint16_t* up, const
  * e: the gradient of the input of y = x W^T.  Exact bf16 products, fp32 sums, one rounding to bf16.
  *   dy0, dy1   bf16 [max_pad, N] by sorted row, or (by_token) [num_pairs / top_k, N] by token
  *   w0, w1     MOE_W_BF16 weights [E, N, K]; w1 and dy1 are NULL without a second pair
- *   dx         bf16 [max_pad, K]; sentinel and padding rows are not written
- * N and K multiples of 8, num_experts <= 256 (MOE_EUNSUPPORTED above).
+ *   dx         bf16 [max_pad, K], no operand's buffer; sentinel and padding rows are not written
+ * N and K multiples of 8, up to 2^20, num_experts <= 256 (MOE_EUNSUPPORTED above).
  * workspace: NULL, or one of moe_grouped_gemm (the same buffer, zero-filled before its first use; every call
  * leaves its counters at zero; calls that share one must not overlap).  With it, launches of few tiles divide
  * the sum over n among workgroups.  num_pairs == 0 enqueues nothing. */
@@ -89,9 +91,9 @@ moe_status moe_grouped_gemm_dgrad(const uint16_t* dy0, const moe_weight* w0, con
  * the weights of y = x W^T.  Exact bf16 products, fp32 sums.  Experts without rows get base, or zeros.
  *   dy         bf16 [max_pad, N] by sorted row, or (dy_by_token) [num_pairs / top_k, N] by token
  *   x          bf16 [max_pad, K] by sorted row, or (x_by_token) [num_pairs / top_k, K] by token
- *   dw         [E, N, K], bf16 (one rounding, after base is added) or, with dw_fp32, fp32
+ *   dw         [E, N, K], bf16 (one rounding, after base is added) or, with dw_fp32, fp32; not dy's or x's buffer
  *   base       NULL, or of dw's type and shape; may be dw (gradients summed over batches)
- * N and K multiples of 8, num_experts <= 256 (MOE_EUNSUPPORTED above).  workspace: as for
+ * N and K multiples of 8, up to 2^20, num_experts <= 256 (MOE_EUNSUPPORTED above).  workspace: as for
  * moe_grouped_gemm_dgrad; with it, launches of few tiles divide long sums over rows among workgroups.
  * num_pairs == 0 writes base or zeros. */
 moe_status moe_grouped_gemm_wgrad(const uint16_t* dy, const uint16_t* x, void* dw, const void* base, int32_t dw_fp32,

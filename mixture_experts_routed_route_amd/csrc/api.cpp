@@ -1034,6 +1034,8 @@ moe_status moe_grouped_gemm_dgrad(const uint16_t* dy0, const moe_weight* w0, con
         REQUIRE_PTR(who, dy1);
         REQUIRE_PTR(who, w1->data);
     }
+    // (rows are read for one tile after they were written for another)
+    REQUIRE(dx != dy0 && dx != dy1, "%s: dx is one buffer with an operand", who);
     return launched(who, moe::launch_dgrad(dy0, static_cast<const uint16_t*>(w0->data), dy1,
                                            w1 ? static_cast<const uint16_t*>(w1->data) : nullptr, dx, sorted_ids,
                                            expert_offsets, static_cast<int>(num_pairs), top_k, num_experts, n, k,
@@ -1058,6 +1060,7 @@ moe_status moe_grouped_gemm_wgrad(const uint16_t* dy, const uint16_t* x, void* d
         REQUIRE_PTR(who, sorted_ids);
         REQUIRE_PTR(who, expert_offsets);
     }
+    REQUIRE(num_pairs == 0 || (dw != dy && dw != x), "%s: dw is one buffer with an operand", who);
     return launched(who, moe::launch_wgrad(dy, x, dw, base, dw_fp32 != 0, sorted_ids, expert_offsets,
                                            static_cast<int>(num_pairs), top_k, num_experts, n, k,
                                            static_cast<int>(max_pad), dy_by_token ? 1 : 0, x_by_token ? 1 : 0, workspace,

@@ -448,9 +448,15 @@ class MoeLayer:
             raise ValueError("train_backward: accumulate needs grads")
         if d_out.shape != b.out.shape or x.shape != b.out.shape:
             raise ValueError(f"train_backward: d_out is {tuple(d_out.shape)} and x {tuple(x.shape)}; need {tuple(b.out.shape)}")
+        if d_out.dtype != torch.bfloat16 or not d_out.is_contiguous():
+            raise ValueError("train_backward: d_out must be contiguous bfloat16")
         if grads is None:
             grads = tuple(torch.empty_like(w.w) for w in (self.gate, self.up, self.down))
         dg, du, dd = grads
+        for t, w in zip(grads, (self.gate, self.up, self.down)):  # before anything is added or replaced
+            if tuple(t.shape) != tuple(w.shape) or t.dtype not in (torch.bfloat16, torch.float32) or not t.is_contiguous():
+                raise ValueError(f"train_backward: grads needs contiguous bf16 or fp32 of the weights' shapes; got {t.dtype} "
+                                 f"{tuple(t.shape)} for {tuple(w.shape)}")
         base = lambda t: t if accumulate else None
         r = b.routing
         b.forward_done = False

@@ -96,6 +96,17 @@ def test_invalid(L, call, what):
     assert rc == -1 and re.search(what, L.moe_last_error().decode()), L.moe_last_error()
 
 
+F2 = ctypes.c_void_p(2 << 20)
+
+
+@pytest.mark.parametrize("call,what", [
+    (dgrad(), "dx is one buffer"), (dgrad(dx=F2, dy1=F2, w1=W), "dx is one buffer"),
+    (wgrad(dw=F2, dy=F2), "dw is one buffer"), (wgrad(dw=F2, x=F2), "dw is one buffer")])
+def test_results_over_operands(L, call, what):
+    """Rows are read for one tile after another tile was written: refused."""
+    test_invalid(L, call, what)
+
+
 @pytest.mark.parametrize("call,what", UNSUPPORTED)
 def test_unsupported(L, call, what):
     rc = getattr(L, call[0])(*call[1])
@@ -189,6 +200,12 @@ def test_layer_refuses(L):
         layer().train_backward(bf(T, H), bf(T, H), b, accumulate=True)
     with pytest.raises(ValueError, match="d_out"):
         layer().train_backward(bf(T - 1, H), bf(T, H), b)
+    for wrong in ((bf(E, I, H), bf(E, I, H), bf(E, I, H)), (bf(E, I, H), bf(E, I, H).half(), bf(E, H, I)),
+                  (bf(E, H, I).transpose(1, 2), bf(E, I, H), bf(E, H, I))):   # before anything is added to the others
+        with pytest.raises(ValueError, match="grads"):
+            layer().train_backward(bf(T, H), bf(T, H), b, grads=wrong, accumulate=True)
+    with pytest.raises(ValueError, match="contiguous bfloat16"):
+        layer().train_backward(bf(T, H).float(), bf(T, H), b)
     assert b.forward_done
 
 
