@@ -177,6 +177,13 @@ __global__ __launch_bounds__(kThreads) void silu_mul_backward_kernel(const uint1
 // is bound by latency and the bytes of d_logits, and w_j * (d_w_j - dot) cancels where one weight is near 1.
 constexpr int kRouteTokens = kThreads / kWave;
 
+__device__ __forceinline__ double read_lane(double v, int lane) {   // lane uniform
+    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v));
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(b), lane);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(b >> 32), lane);
+    return __longlong_as_double(static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo));
+}
+
 template <bool FULL>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(const int32_t* __restrict__ ids,
                                                                   const float* __restrict__ w,
@@ -194,12 +201,13 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(const int32_t*
         const int j = lane + 64 * i;
         id[i] = -1;
         wd[i] = wj[i] = 0.0;
-        if (j < k) {
+        if (j < k) {   // (three loads at once; what a dropped pair holds is not used)
             const int e = ids[p0 + j];
+            const float a = w[p0 + j], d = dw[p0 + j];
             if (e >= 0 && e < E) {
                 id[i] = e;
-                wj[i] = w[p0 + j];
-                wd[i] = dw[p0 + j];
+                wj[i] = a;
+                wd[i] = d;
             }
         }
         dot += wj[i] * wd[i];
@@ -226,20 +234,20 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(const int32_t*
         for (int i = 0; i < 4; ++i) pr[i] /= sum;
     }
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) dot += __shfl_xor(dot, o);
+    for (int o = 32; o >= 1; o >>= 1)
+        if (o < k) dot += __shfl_xor(dot, o);   // (lanes past k hold zeros)
+    dot = read_lane(dot, 0);
     // each expert gathers the pairs that name it (an id may come twice)
     double acc[4] = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const double v = FULL ? wd[i] : wj[i] * (wd[i] - dot);
-        for (int j = 64 * i; j < min(k, 64 * i + 64); ++j) {
-            const int e = __shfl(id[i], j & 63);
-            const double x = __shfl(v, j & 63);
-            if (e >= 0 && (e & 63) == lane) {
+        for (int j = 64 * i; j < min(k, 64 * i + 64); ++j) {   // (scalar reads of lane j: no trip through LDS)
+            const int e = __builtin_amdgcn_readlane(id[i], j & 63);
+            const double x = lane == (e & 63) ? read_lane(v, j & 63) : 0.0;
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if ((e >> 6) == q) acc[q] += x;
-            }
+            for (int q = 0; q < 4; ++q)
+                if (e >= 0 && (e >> 6) == q) acc[q] += x;
         }
     }
 #pragma unroll
