@@ -41,7 +41,7 @@ constexpr int kBand = 4;       // row tiles per band of the tile order
 constexpr int kTab = 128;      // entries of a workgroup's list that are located in advance
 constexpr int kMaxPieces = 256;  // workgroups of a launch whose tiles are cut along the contraction
 constexpr int kMaxSplit = 8;     // pieces of a tile
-constexpr int kMinPiece = 8;     // halves of a piece
+constexpr int kMinPiece = 16;    // halves of a piece
 constexpr int kSegs = 8;       // dgrad: tiles whose row ids are held
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -98,7 +98,6 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     __shared__ int s_scan[kNT / 64];
     __shared__ Entry s_tab[kTab];
     __shared__ int s_n, s_ends;   // entries in it, and whether they are all
-    __shared__ int s_mine[64];    // wgrad, unequal experts: this workgroup's tiles
     __shared__ int s_arrived;
     __shared__ __attribute__((aligned(1024))) char s_stage[kNT / 64 * 1024];   // a wave's results on their way out
     // sorted ids.  dgrad: of the rows of the last kSegs tiles.  wgrad: per wave, of its rows (4 per half) of 16 halves, twice
@@ -197,41 +196,6 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
         }
         s.e = e;
     };
-    // wgrad, experts of very different lengths: dealing in turn would give the workgroups with the longest tiles as many
-    // others as the rest.  Instead every unit's tiles, unit by unit by falling length, go to the workgroups of the XCD
-    // that have least so far.  (A step of the first wave per unit, so for few units only; 128 experts of 2048 x 768 with
-    // 8 to 8192 rows.)
-    bool levelled = false;
-    if constexpr (!DGRAD) {
-        constexpr int kEpilogue = F32 ? 12 : 6;   // a tile's end in halves
-        const int longest = halves_of(s_order[0]), shortest = halves_of(s_order[E - 1]);
-        levelled = pieces == 1 && longest > 2 * shortest + kEpilogue && xcd_units <= 64 && unit <= per_xcd && per_xcd <= 64 &&
-                   xcd_units * unit > per_xcd;
-        levelled = __builtin_amdgcn_readfirstlane(levelled);
-        if (levelled) {
-            if (wave == 0) {
-                int load = lane < per_xcd ? 0 : 0x3fffffff, n = 0;
-                s_mine[lane] = -1;
-                for (int v = 0; v < xcd_units; ++v) {
-                    const int u = unit_at(v);
-                    if (u >= units) break;
-                    const int e = s_order[u / units_e], first = (u % units_e) * unit;
-                    const int tiles = min(unit, tiles_e - first);
-                    int rank = 0;
-                    for (int t = 0; t < per_xcd; ++t) {
-                        const int other = __builtin_amdgcn_readlane(load, t);
-                        rank += other < load || (other == load && t < lane);
-                    }
-                    if (rank < tiles) {
-                        load += halves_of(e) + kEpilogue;
-                        if (lane == slot) s_mine[n] = v << 8 | rank;
-                        ++n;
-                    }
-                }
-            }
-            __syncthreads();
-        }
-    }
     // entry number n of this workgroup: kIsTile, kSkip (no tile) or kEnd
     auto locate = [&](int n, Seg& s) __attribute__((always_inline)) -> int {
         if (pieces > 1) {   // piece blockIdx / T of tile blockIdx % T
@@ -253,18 +217,9 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
             if (i >= l_n) return kEnd;
             tile_at(l_lo + i, 0, s);
         } else {
-            int v, j;
-            if (levelled) {
-                if (n >= 64 || s_mine[n] < 0) return kEnd;
-                v = s_mine[n] >> 8;
-                j = s_mine[n] & 255;
-            } else {
-                const int i = slot + n * per_xcd;
-                if (i >= l_n) return kEnd;
-                v = i / unit;
-                j = i % unit;
-            }
-            const int u = unit_at(v), idx = (u % units_e) * unit + j;
+            const int i = slot + n * per_xcd;
+            if (i >= l_n) return kEnd;
+            const int u = unit_at(i / unit), idx = (u % units_e) * unit + i % unit;
             if (u >= units || idx >= tiles_e) return kSkip;
             tile_at(idx, s_order[u / units_e], s);
         }
