@@ -948,6 +948,8 @@ moe_status check_grad(const char* who, int64_t num_pairs, int32_t top_k, int32_t
                 max_pad < INT32_MAX,
             "%s: max_pad %lld must be >= %lld and a multiple of block_size", who, static_cast<long long>(max_pad),
             static_cast<long long>(max_padded(num_pairs, num_experts, block_size)));
+    // (the kernels look up to 543 rows past a span's end, in 32 bits)
+    if (max_pad > INT32_MAX - 1024) return fail(MOE_EUNSUPPORTED, "%s: max_pad %lld > 2^31 - 1025", who, static_cast<long long>(max_pad));
     if (workspace != nullptr) {
         const int64_t need = moe_grouped_gemm_workspace_bytes();
         REQUIRE_PTR(who, workspace);

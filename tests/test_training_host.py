@@ -97,6 +97,12 @@ def test_invalid(L, call, what):
 
 
 F2 = ctypes.c_void_p(2 << 20)
+FAR = (1 << 31) - 1024   # a multiple of every block size; the rows past a span's end would pass 32 bits
+
+
+@pytest.mark.parametrize("call", [dgrad(dx=F2, mp=FAR), wgrad(dw=F2, mp=FAR)])
+def test_rows_past_32_bits(L, call):
+    test_unsupported(L, call, "max_pad")
 
 
 @pytest.mark.parametrize("call,what", [
