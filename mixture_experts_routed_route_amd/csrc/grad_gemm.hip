@@ -20,13 +20,13 @@
 // random data the card's power limit sets the clock, and a loop of the former alone reaches 2060 TFLOP/s
 // against 1812.
 //
-// What bounds it: at 8 x (1024 x 4096 x 14336), 0.96 TFLOP, dgrad takes 889 to 920 us (1.08 PFLOP/s) and
-// wgrad 876 us (1.10); eight library products of these layouts take 798 to 849 and 1020 us.  Matrix
+// What bounds it: at 8 x (1024 x 4096 x 14336), 0.96 TFLOP, dgrad takes 887 us (1.08 PFLOP/s) and
+// wgrad 864 us (1.11); eight library products of these layouts take 798 to 849 and 1020 us.  Matrix
 // cores are busy for 59% of the cycles at a clock that falls to 1.7 GHz under the load, LDS without bank
 // conflicts (2 to 8% of the cycles).  The loads' path is what the rest waits for: without the loads in the
 // main loop the same products take 618 and 820 us.  Their average latency is 450 cycles, far less than
 // they are issued ahead; dgrad's rows of dy come in pieces of 64 bytes, half a line each.  Tiles of few halves are bound
-// by their ends (wgrad of 64 experts of 192 rows, 1408 x 4096: 272 us, 2.9 TB/s): an epilogue is 3000 cycles per group,
+// by their ends (wgrad of 64 experts of 192 rows, 1408 x 4096: 263 us, 3.0 TB/s): an epilogue is 3000 cycles per group,
 // as much as two halves, and moving the loads to the next tile as much again.
 //
 // Tried and slower: two workgroups of 4 waves per CU with tiles of 128 x 256 and three slots, so that one's
@@ -520,7 +520,7 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     // loads of two later halves (4 each) and, in the two halves that follow an epilogue (after), its stores.  (The first
     // group needs the wait at the second barrier only, the second group at the first; at the other one it asks for what
     // has landed before, or for what the next half will need.)
-    auto one_half = [&](auto rf_c, auto cf_c, auto first_c, bool after) __attribute__((always_inline)) {
+    auto one_half = [&](auto rf_c, auto cf_c, auto first_c, bool after, bool close) __attribute__((always_inline)) {
         auto landed = [&]() __attribute__((always_inline)) {
             if (after) wait_vmcnt<8 + kStores>();
             else wait_vmcnt<8>();
@@ -531,8 +531,10 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
         landed();
         barrier();
         compute(rf_c, cf_c, first_c);
-        landed();
-        barrier();
+        if (close) {
+            landed();
+            barrier();
+        }
         c_slot = (c_slot + kSlotB) & (kSlots * kSlotB - 1);
         ++i_since;
     };
@@ -663,18 +665,23 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
         const int nh = halves(cs);
         const int n_rows = DGRAD ? cs.r_end - cs.r0 : N - cs.at, n_cols = K - column(cs);
         const bool again = n > 0;
-        if (nh > 0 && n_rows > 128 && n_cols > 128) {
-            one_half(I4{}, I8{}, std::true_type{}, again);
+        const bool whole = nh > 0 && n_rows > 128 && n_cols > 128;
+        // The second group's last barrier of a whole tile comes after its epilogue, which so runs beside the first group's
+        // instead of after it (wgrad of 8 experts of 1024 rows, 14336 x 4096: 874 -> 864 us; 64 experts of 192 rows,
+        // 1408 x 4096: 270 -> 263 us; not for parts of tiles, where the test in every half costs 2%).
+        const bool open = whole && group && pieces == 1;
+        if (whole) {
+            one_half(I4{}, I8{}, std::true_type{}, again, nh > 1 || !open);
             if (--i_left == 0) next(false);
             int left = nh - 1;
             if (left > 0) {
-                one_half(I4{}, I8{}, std::false_type{}, again);
+                one_half(I4{}, I8{}, std::false_type{}, again, left > 1 || !open);
                 if (--i_left == 0) next(false);
                 --left;
             }
             while (left > 0) {
                 const int run = min(left, i_left);
-                for (int r = 0; r < run; ++r) one_half(I4{}, I8{}, std::false_type{}, false);
+                for (int r = 1; r <= run; ++r) one_half(I4{}, I8{}, std::false_type{}, false, r < left || !open);
                 left -= run;
                 i_left -= run;
                 if (i_left == 0) next(false);
@@ -688,7 +695,7 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
                 for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
             auto some = [&](auto rf_c, auto cf_c) __attribute__((always_inline)) {
                 for (int h = 0; h < nh; ++h) {
-                    one_half(rf_c, cf_c, std::false_type{}, again && h < 2);
+                    one_half(rf_c, cf_c, std::false_type{}, again && h < 2, true);
                     if (--i_left == 0) next(false);
                 }
             };
@@ -698,6 +705,7 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
         }
         if (pieces > 1) break;      // a piece is not a tile yet
         finish();
+        if (open) barrier();
     }
     if (any && !group) barrier();   // the other group's last
     wait_vmcnt<0>();                // the halves of zeros: nothing may land in LDS after the end
