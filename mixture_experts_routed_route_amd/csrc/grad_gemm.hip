@@ -22,16 +22,16 @@
 //
 // What bounds it: at 8 x (1024 x 4096 x 14336), 0.96 TFLOP, dgrad takes 887 us (1.08 PFLOP/s) and
 // wgrad 864 us (1.11); eight library products of these layouts take 798 to 849 and 1020 us.  Matrix
-// cores are busy for 59% of the cycles at a clock that falls to 1.7 GHz under the load, LDS without bank
-// conflicts (2 to 8% of the cycles).  The loads' path is what the rest waits for: without the loads in the
+// cores are busy for 59% of the cycles at a clock that falls to 1.7 GHz under the load; bank conflicts take 2 to 8%
+// of the cycles.  The loads' path is what the rest waits for: without the loads in the
 // main loop the same products take 618 and 820 us.  Their average latency is 450 cycles, far less than
 // they are issued ahead; dgrad's rows of dy come in pieces of 64 bytes, half a line each.  Tiles of few halves are bound
 // by their ends (wgrad of 64 experts of 192 rows, 1408 x 4096: 263 us, 3.0 TB/s): an epilogue is 3000 cycles per group,
 // as much as two halves, and moving the loads to the next tile as much again.
 //
 // Tried and slower: two workgroups of 4 waves per CU with tiles of 128 x 256 and three slots, so that one's
-// epilogue runs beside the other's products (dgrad 1000 to 1085 us, wgrad 1030, ragged 277; a third more
-// bytes through L2), the same with fragments read one half ahead (1057, 1069, 285).
+// epilogue runs beside the other's products (dgrad 1000 to 1085 us, wgrad 1030, ragged 277; half as many
+// bytes more through L2), the same with fragments read one half ahead (1057, 1069, 285).
 //
 // LDS layout.  Operands read by columns: row of 512 bytes, 16-byte chunk c of contraction row q at
 // chunk c ^ ((q & 3) << 2 | ((q >> 3 ^ q >> 4) & 1) << 1): the 4 rows of each 16 lanes that one transposing read
