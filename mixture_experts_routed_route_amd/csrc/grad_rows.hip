@@ -52,7 +52,7 @@ __device__ __forceinline__ float lo_f32(uint32_t v) { return __uint_as_float(v <
 __device__ __forceinline__ float hi_f32(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
 // HBM-bound: 6 bytes per value.  The rows' 16-byte chunks are dealt to threads in one flat sequence, so that
-// narrow rows leave no lanes idle.  65536 real rows of 768 columns with dropout: 47 us, 6.4 TB/s (302 MB); a copy of
+// narrow rows leave no lanes idle.  65536 real rows of 768 columns with dropout: 54 us, 5.6 TB/s (302 MB); a copy of
 // 1 GiB reaches 4.8.  The ten rounds of the generator, 40 multiplications for 8 values, hide behind the loads.
 // 64 tokens x 128: 3 us, the launch itself.
 template <bool DROP>
@@ -104,7 +104,7 @@ __device__ __forceinline__ void back1(float g, float u, float d, float w, float 
 
 // HBM-bound: 12 bytes per value.  TPR threads per row, since d_topk_w is a sum over the row; added in a fixed order.
 // Inputs may be outputs: every thread loads all it needs of its columns before it stores any.
-// 8192 real rows of 14336 columns: 268 us, 5.3 TB/s (1.41 GB); 11994 of 1408 with dropout: 33 us, 6.1 TB/s (203 MB).
+// 8192 real rows of 14336 columns: 268 us, 5.3 TB/s (1.41 GB); 11994 of 1408 with dropout: 44 us, 4.6 TB/s (203 MB).
 template <bool DROP, int TPR>
 __global__ __launch_bounds__(kThreads) void silu_mul_backward_kernel(const uint16_t* g, const uint16_t* u,
                                                                      const uint16_t* d,

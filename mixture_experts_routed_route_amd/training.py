@@ -12,27 +12,38 @@ from typing import Optional, Tuple
 
 import torch
 
-from .ops import Bf16Weight, Routing, _check_routing, _need, _numel_at_least, _rows_at_least
+from .ops import Bf16Weight, Routing, _check_routing, _numel_at_least
 from .serving import _index, _launch, _ptr
 
 __all__ = ["moe_silu_mul_dropout", "moe_silu_mul_backward", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad",
            "moe_route_backward"]
 
 
+# Messages are made when a check fails only: made beforehand they took half of a small call's time.
+def _shape(t: Optional[torch.Tensor], shape: Tuple[int, ...], who: str, name: str) -> None:
+    if t is not None and t.shape != shape:
+        raise ValueError(f"{who}: {name} is not of shape {shape} (got {tuple(t.shape)})")
+
+
 def _check_p(p: float, rng: Optional[torch.Tensor], who: str) -> float:
     p = float(p)
-    _need(0.0 <= p < 1.0, f"{who}: p is {p}; needs [0, 1)")
-    _need(rng is not None or p == 0.0, f"{who}: dropout needs rng")
-    _need(rng is None or tuple(rng.shape) == (2,), f"{who}: rng needs seed and offset, shape (2,)")
+    if not 0.0 <= p < 1.0:
+        raise ValueError(f"{who}: p is {p}; needs [0, 1)")
+    if rng is None and p != 0.0:
+        raise ValueError(f"{who}: dropout needs rng")
+    if rng is not None and rng.shape != (2,):
+        raise ValueError(f"{who}: rng needs seed and offset, shape (2,)")
     return p
 
 
 def _rows(t: torch.Tensor, routing: Optional[Routing], who: str, name: str) -> Tuple[int, int]:
     """Rows and columns of a call over sorted rows (all rows without a routing)."""
-    _need(t.dim() == 2, f"{who}: {name} is {tuple(t.shape)}; needs [rows, n]")
-    if routing is not None:
-        _numel_at_least(routing.sorted_ids, t.shape[0], f"{who}: routing.sorted_ids")
-    return tuple(t.shape)
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{who}: {name} is {tuple(shape)}; needs [rows, n]")
+    if routing is not None and routing.sorted_ids.numel() < shape[0]:
+        _numel_at_least(routing.sorted_ids, shape[0], f"{who}: routing.sorted_ids")
+    return shape
 
 
 def moe_silu_mul_dropout(gate: torch.Tensor, up: torch.Tensor, routing: Optional[Routing] = None, p: float = 0.0,
@@ -48,8 +59,8 @@ def moe_silu_mul_dropout(gate: torch.Tensor, up: torch.Tensor, routing: Optional
     p = _check_p(p, rng, who)
     if out is None:
         out = torch.empty_like(gate)
-    for t, name in ((up, "up"), (out, "out")):
-        _need(tuple(t.shape) == (rows, n), f"{who}: {name} is {tuple(t.shape)}; needs {(rows, n)}")
+    _shape(up, (rows, n), who, "up")
+    _shape(out, (rows, n), who, "out")
     bf = torch.bfloat16
     i = _index(gate, bf, "gate")
     _launch(who, i, gate.data_ptr(), _ptr(up, bf, "up", i), _ptr(out, bf, "out", i),
@@ -78,9 +89,10 @@ def moe_silu_mul_backward(gate: torch.Tensor, up: torch.Tensor, d: torch.Tensor,
     h_weighted = torch.empty_like(gate) if h_weighted is None else h_weighted
     d_topk_w = torch.zeros_like(topk_w) if d_topk_w is None else d_topk_w
     for t, name in ((up, "up"), (d, "d"), (d_gate, "d_gate"), (d_up, "d_up"), (h_weighted, "h_weighted")):
-        _need(tuple(t.shape) == (rows, n), f"{who}: {name} is {tuple(t.shape)}; needs {(rows, n)}")
-    _numel_at_least(topk_w, pairs, f"{who}: topk_w")
-    _numel_at_least(d_topk_w, pairs, f"{who}: d_topk_w")
+        _shape(t, (rows, n), who, name)
+    if topk_w.numel() < pairs or d_topk_w.numel() < pairs:
+        _numel_at_least(topk_w, pairs, f"{who}: topk_w")
+        _numel_at_least(d_topk_w, pairs, f"{who}: d_topk_w")
     bf, f32 = torch.bfloat16, torch.float32
     i = _index(gate, bf, "gate")
     _launch(who, i, gate.data_ptr(), _ptr(up, bf, "up", i), _ptr(d, bf, "d", i), _ptr(topk_w, f32, "topk_w", i),
@@ -91,8 +103,11 @@ def moe_silu_mul_backward(gate: torch.Tensor, up: torch.Tensor, d: torch.Tensor,
 
 
 def _operand(t: torch.Tensor, width: int, by_token: bool, routing: Routing, who: str, name: str) -> None:
-    _need(t.dim() == 2 and t.shape[1] == width, f"{who}: {name} is {tuple(t.shape)}; its width must be {width}")
-    _rows_at_least(t, routing.num_pairs // routing.top_k if by_token else routing.max_pad, f"{who}: {name}")
+    shape, rows = t.shape, routing.num_pairs // routing.top_k if by_token else routing.max_pad
+    if len(shape) != 2 or shape[1] != width:
+        raise ValueError(f"{who}: {name} is {tuple(shape)}; its width must be {width}")
+    if shape[0] < rows:
+        raise ValueError(f"{who}: {name} has {tuple(shape)}; needs >= {rows} rows")
 
 
 def moe_grouped_gemm_dgrad(dy: torch.Tensor, w: Bf16Weight, routing: Routing, dy1: Optional[torch.Tensor] = None,
@@ -106,19 +121,22 @@ def moe_grouped_gemm_dgrad(dy: torch.Tensor, w: Bf16Weight, routing: Routing, dy
     [T, N] by token.  ``workspace`` (from ``gemm_workspace``) lets launches of few tiles divide the sum over
     N; calls that share one must not overlap."""
     who = "moe_grouped_gemm_dgrad"
-    for x in (w, w1):
-        _need(x is None or isinstance(x, Bf16Weight), f"{who}: gradients go through bf16 weights only")
+    if not isinstance(w, Bf16Weight) or not (w1 is None or isinstance(w1, Bf16Weight)):
+        raise ValueError(f"{who}: gradients go through bf16 weights only")
     E, N, K = w.shape
-    _need(E == routing.num_experts, f"{who}: the weights hold {E} experts, the routing {routing.num_experts}")
-    _need((dy1 is None) == (w1 is None), f"{who}: dy1 and w1 go together")
-    _need(w1 is None or tuple(w1.shape) == (E, N, K), f"{who}: the two weights must have one shape")
+    if E != routing.num_experts:
+        raise ValueError(f"{who}: the weights hold {E} experts, the routing {routing.num_experts}")
+    if (dy1 is None) != (w1 is None):
+        raise ValueError(f"{who}: dy1 and w1 go together")
+    if w1 is not None and tuple(w1.shape) != (E, N, K):
+        raise ValueError(f"{who}: the two weights must have one shape")
     _operand(dy, N, by_token, routing, who, "dy")
     if dy1 is not None:
         _operand(dy1, N, by_token, routing, who, "dy1")
     if out is None:
         out = torch.empty((routing.max_pad, K), dtype=torch.bfloat16, device=dy.device)
-    _need(out.dim() == 2 and out.shape[1] == K and out.shape[0] >= routing.max_pad,
-          f"{who}: out is {tuple(out.shape)}; needs [>= {routing.max_pad}, {K}]")
+    if out.dim() != 2 or out.shape[1] != K or out.shape[0] < routing.max_pad:
+        raise ValueError(f"{who}: out is {tuple(out.shape)}; needs [>= {routing.max_pad}, {K}]")
     _check_routing(routing)
     bf = torch.bfloat16
     i = _index(dy, bf, "dy")
@@ -147,15 +165,17 @@ def moe_grouped_gemm_wgrad(dy: torch.Tensor, x: torch.Tensor, routing: Routing, 
     ``out``: gradients summed over batches.  ``workspace``: as for ``moe_grouped_gemm_dgrad``, to divide long
     sums over rows."""
     who = "moe_grouped_gemm_wgrad"
-    _need(dy.dim() == 2 and x.dim() == 2, f"{who}: dy is {tuple(dy.shape)}, x {tuple(x.shape)}; need two dimensions")
+    if dy.dim() != 2 or x.dim() != 2:
+        raise ValueError(f"{who}: dy is {tuple(dy.shape)}, x {tuple(x.shape)}; need two dimensions")
     E, N, K = routing.num_experts, dy.shape[1], x.shape[1]
     _operand(dy, N, dy_by_token, routing, who, "dy")
     _operand(x, K, x_by_token, routing, who, "x")
     if out is None:
         out = torch.empty((E, N, K), dtype=torch.bfloat16 if base is None else base.dtype, device=dy.device)
-    _need(out.dtype in (torch.bfloat16, torch.float32), f"{who}: out must be bfloat16 or float32 (got {out.dtype})")
-    for t, name in ((out, "out"), (base, "base")):
-        _need(t is None or tuple(t.shape) == (E, N, K), f"{who}: {name} is not of shape {(E, N, K)}")
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{who}: out must be bfloat16 or float32 (got {out.dtype})")
+    _shape(out, (E, N, K), who, "out")
+    _shape(base, (E, N, K), who, "base")
     _check_routing(routing)
     bf = torch.bfloat16
     i = _index(dy, bf, "dy")
@@ -172,15 +192,16 @@ def moe_route_backward(topk_ids: torch.Tensor, topk_w: torch.Tensor, d_topk_w: t
     """Gradient of the router's logits, fp32 [T, num_experts], from the gradient ``d_topk_w`` of the weights that
     ``moe_route`` returned: renormalised over the chosen, or (with its ``logits``) not."""
     who = "moe_route_backward"
-    _need(topk_ids.dim() == 2, f"{who}: topk_ids is {tuple(topk_ids.shape)}; needs [T, k]")
+    if topk_ids.dim() != 2:
+        raise ValueError(f"{who}: topk_ids is {tuple(topk_ids.shape)}; needs [T, k]")
     T, k = topk_ids.shape
     E = int(num_experts)
-    for t, name in ((topk_w, "topk_w"), (d_topk_w, "d_topk_w")):
-        _need(tuple(t.shape) == (T, k), f"{who}: {name} is {tuple(t.shape)}; needs {(T, k)}")
+    _shape(topk_w, (T, k), who, "topk_w")
+    _shape(d_topk_w, (T, k), who, "d_topk_w")
     if out is None:
         out = torch.empty((T, E), dtype=torch.float32, device=topk_ids.device)
-    for t, name in ((logits, "logits"), (out, "out")):
-        _need(t is None or tuple(t.shape) == (T, E), f"{who}: {name} is not of shape {(T, E)}")
+    _shape(logits, (T, E), who, "logits")
+    _shape(out, (T, E), who, "out")
     f32 = torch.float32
     i = _index(topk_ids, torch.int32, "topk_ids")
     _launch(who, i, topk_ids.data_ptr(), _ptr(topk_w, f32, "topk_w", i), _ptr(d_topk_w, f32, "d_topk_w", i),
