@@ -123,12 +123,13 @@ __global__ __launch_bounds__(kThreads) void silu_mul_backward_kernel(const uint1
     const int64_t off = row * n;
     const int t = threadIdx.x % TPR;
     float dot = 0.f;
-    for (int c0 = t * 8; c0 < n; c0 += 2 * TPR * 8) {
+    const uint32_t cols = n;   // (c0 goes up to 2 * TPR * 8 past n: in signed 32 bits it would wrap in rows next to 2^31)
+    for (uint32_t c0 = t * 8; c0 < cols; c0 += 2 * TPR * 8) {
         u32x4 gv[2], uv[2], dv[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            const int c = c0 + b * TPR * 8;
-            if (c < n) {
+            const uint32_t c = c0 + b * TPR * 8;
+            if (c < cols) {
                 gv[b] = *reinterpret_cast<const u32x4*>(g + off + c);
                 uv[b] = *reinterpret_cast<const u32x4*>(u + off + c);
                 dv[b] = *reinterpret_cast<const u32x4*>(d + off + c);
@@ -136,8 +137,8 @@ __global__ __launch_bounds__(kThreads) void silu_mul_backward_kernel(const uint1
         }
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            const int c = c0 + b * TPR * 8;
-            if (c >= n) continue;
+            const uint32_t c = c0 + b * TPR * 8;
+            if (c >= cols) continue;
             float f[8];
             if constexpr (DROP) keep8(Rng(rng), c >> 3, p, below, scale, f);
             u32x4 og, ou, oh;
