@@ -104,6 +104,14 @@ class TrainBuffers:
     forward_done: bool = False
 
 
+def _operand(t: torch.Tensor, name: str, shape, dtypes, device) -> None:
+    """Refuses what a call that takes ``t`` would refuse it for."""
+    if t.shape != shape or t.dtype not in dtypes or t.device != device or not t.is_contiguous() or t.data_ptr() % 16:
+        types = " or ".join(str(d).removeprefix("torch.") for d in dtypes)
+        raise ValueError(f"train_backward: {name} must be contiguous {types} {tuple(shape)} on {device}, 16-byte aligned; got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
 class MoeLayer:
     def __init__(self, num_experts: int, hidden: int, inter: int, top_k: int, block_size: int, gate, up, down,
                  lora: Optional[LoraTables] = None, renormalize: bool = True, lora_cap: Optional[int] = None,
@@ -446,17 +454,23 @@ class MoeLayer:
             raise ValueError("train_backward: without renormalised routing weights the logits are needed")
         if accumulate and grads is None:
             raise ValueError("train_backward: accumulate needs grads")
-        if d_out.shape != b.out.shape or x.shape != b.out.shape:
-            raise ValueError(f"train_backward: d_out is {tuple(d_out.shape)} and x {tuple(x.shape)}; need {tuple(b.out.shape)}")
-        if d_out.dtype != torch.bfloat16 or not d_out.is_contiguous():
-            raise ValueError("train_backward: d_out must be contiguous bfloat16")
+        bf, f32, device = (torch.bfloat16,), (torch.float32,), b.out.device
+        # every operand before anything is added or replaced: a step that ends halfway could not be made again
+        _operand(d_out, "d_out", b.out.shape, bf, device)
+        _operand(x, "x", b.out.shape, bf, device)
+        if not self.renormalize:
+            _operand(logits, "logits", b.d_logits.shape, f32, device)
+        weights = self.gate, self.up, self.down
+        shapes = (self.E, self.I, self.H), (self.E, self.I, self.H), (self.E, self.H, self.I)
+        for w, shape in zip(weights, shapes):
+            if not isinstance(w, Bf16Weight):
+                raise ValueError("train_backward: gradients go through bf16 weights only")
+            _operand(w.w, "one of the weights", shape, bf, device)
         if grads is None:
-            grads = tuple(torch.empty_like(w.w) for w in (self.gate, self.up, self.down))
+            grads = tuple(torch.empty_like(w.w) for w in weights)
         dg, du, dd = grads
-        for t, w in zip(grads, (self.gate, self.up, self.down)):  # before anything is added or replaced
-            if tuple(t.shape) != tuple(w.shape) or t.dtype not in (torch.bfloat16, torch.float32) or not t.is_contiguous():
-                raise ValueError(f"train_backward: grads needs contiguous bf16 or fp32 of the weights' shapes; got {t.dtype} "
-                                 f"{tuple(t.shape)} for {tuple(w.shape)}")
+        for t, shape in zip(grads, shapes):
+            _operand(t, "one of grads", shape, bf + f32, device)
         base = lambda t: t if accumulate else None
         r = b.routing
         b.forward_done = False

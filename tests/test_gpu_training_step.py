@@ -1,0 +1,49 @@
+"""The layer's training step after calls that it refuses: the sums hold what they held, and the step can still be made."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def m():
+    if not torch.cuda.is_available():
+        pytest.skip("no HIP device")
+    import mixture_experts_routed_route_amd as m
+    m.lib()
+    return m
+
+
+def make(m, T, H, I, E, k, seed=0, renormalize=True):
+    g = torch.Generator().manual_seed(seed)
+    bf = lambda s, *shape: (s * torch.randn(shape, generator=g)).bfloat16().cuda()
+    w = [m.Bf16Weight(bf(H ** -0.5, E, I, H)), m.Bf16Weight(bf(H ** -0.5, E, I, H)), m.Bf16Weight(bf(I ** -0.5, E, H, I))]
+    return (m.MoeLayer(E, H, I, k, 16, *w, renormalize=renormalize), torch.randn((T, E), generator=g).cuda(), bf(1.0, T, H),
+            bf(1.0, T, H))
+
+
+def sums(layer, value=0.0):
+    return tuple(torch.full(w.shape, value, device="cuda") for w in (layer.gate, layer.up, layer.down))
+
+
+def test_refused_calls_add_nothing(m):
+    T, H, I, E, k = 40, 72, 136, 5, 2
+    layer, logits, x, d_out = make(m, T, H, I, E, k, renormalize=False)
+    b = layer.train_plan(T, "cuda", dropout=0.1)
+    want = sums(layer, 0.5)
+    layer.train_forward(logits, x, b)
+    want_x, want_l, _ = (t.clone() if isinstance(t, torch.Tensor) else t
+                         for t in layer.train_backward(d_out, x, b, logits, grads=want, accumulate=True))
+    total = sums(layer, 0.5)
+    layer.train_forward(logits, x, b)
+    for wrong in (dict(x=x.float()), dict(x=x.t().contiguous().t()), dict(x=x.cpu()), dict(logits=logits[:, 1:]),
+                  dict(logits=torch.zeros((T, E + 1), device="cuda")), dict(logits=logits.double()), dict(logits=logits.cpu()),
+                  dict(d_out=d_out.cpu()), dict(grads=(total[0], total[1].cpu(), total[2])),
+                  dict(grads=(total[0].half(), *total[1:]))):
+        args = {**dict(d_out=d_out, x=x, logits=logits, grads=total), **wrong}
+        with pytest.raises(ValueError):
+            layer.train_backward(args["d_out"], args["x"], b, args["logits"], grads=args["grads"], accumulate=True)
+        assert all((t == 0.5).all() for t in total)
+    d_x, d_l, _ = layer.train_backward(d_out, x, b, logits, grads=total, accumulate=True)
+    assert torch.equal(d_x, want_x) and torch.equal(d_l, want_l)
+    assert all(torch.equal(p, q) for p, q in zip(total, want))

@@ -1,0 +1,93 @@
+"""Refusals of the layer's training step, CPU side: what a later call of the step would refuse is refused before the first
+one, so that no gradient holds a batch that the others do not."""
+import pytest
+import torch
+
+import mixture_experts_routed_route_amd as m
+
+T, H, I, E, K, BS = 8, 64, 32, 4, 2, 16
+
+
+def bf(*shape, device="cpu"):
+    return torch.zeros(shape, dtype=torch.bfloat16, device=device)
+
+
+def layer(**kw):
+    w = lambda *s: m.Bf16Weight(bf(*s))
+    return m.MoeLayer(E, H, I, K, BS, w(E, I, H), w(E, I, H), w(E, H, I), **kw)
+
+
+def unaligned(*shape):
+    n = torch.Size(shape).numel()
+    t = torch.zeros(n + 8, dtype=torch.float32)
+    at = next(i for i in range(1, 8) if (t.data_ptr() + 4 * i) % 16)
+    return t[at:at + n].view(shape)
+
+
+def ready(a):
+    """Buffers as they stand between a forward and its backward."""
+    b = a.train_plan(T, "cpu")
+    b.forward_done, b.forward_of = True, a
+    return b
+
+
+def sums(dtype=torch.float32):
+    return [torch.full(s, 3.0, dtype=dtype) for s in ((E, I, H), (E, I, H), (E, H, I))]
+
+
+def refused(a, b, what, d_out=None, x=None, logits=None, grads=None):
+    grads = sums() if grads is None else grads
+    before = [g.clone() if g.device.type == "cpu" else None for g in grads]
+    with pytest.raises(ValueError, match=what):
+        a.train_backward(bf(T, H) if d_out is None else d_out, bf(T, H) if x is None else x, b, logits, grads=grads,
+                         accumulate=True)
+    assert b.forward_done   # the step can still be made
+    assert all(c is None or torch.equal(g, c) for g, c in zip(grads, before))
+
+
+@pytest.mark.parametrize("x", [bf(T, H).float(), bf(H, T).t(), bf(T, H, device="meta"), bf(T, H + 8)[:, :H], bf(T + 1, H)])
+def test_x(x):
+    a = layer()
+    refused(a, ready(a), "train_backward: x ", x=x)
+
+
+@pytest.mark.parametrize("d_out", [bf(T, H, device="meta"), bf(H, T).t(), bf(T, H).half()])
+def test_d_out(d_out):
+    a = layer()
+    refused(a, ready(a), "train_backward: d_out ", d_out=d_out)
+
+
+@pytest.mark.parametrize("logits", [torch.zeros(T, E + 1), torch.zeros(T - 1, E), bf(T, E), torch.zeros(E, T).t(),
+                                    torch.zeros(T, E, device="meta"), unaligned(T, E)])
+def test_logits(logits):
+    a = layer(renormalize=False)
+    refused(a, ready(a), "train_backward: logits ", logits=logits)
+
+
+def test_logits_that_are_not_read():
+    """With renormalised weights the logits are not an operand, whatever is passed: the step goes on to its first call."""
+    a = layer()
+    with pytest.raises(ValueError, match="HIP device"):
+        a.train_backward(bf(T, H), bf(T, H), ready(a), torch.zeros(1), grads=sums(), accumulate=True)
+
+
+@pytest.mark.parametrize("which", range(3))
+def test_grads_of_another_device_or_alignment(which):
+    a = layer()
+    for wrong in (torch.zeros(sums()[which].shape, device="meta"), unaligned(*sums()[which].shape)):
+        g = sums()
+        g[which] = wrong
+        refused(a, ready(a), "grads", grads=g)
+
+
+@pytest.mark.parametrize("name", ["gate", "up", "down"])
+def test_weights(name):
+    """Weights that another type or shape took the place of after the forward."""
+    a = layer()
+    b = ready(a)
+    w = getattr(a, name)
+    for other in (bf(E, I, H + 8), torch.zeros(w.shape), bf(*w.shape, device="meta")):
+        setattr(a, name, m.Bf16Weight(other))
+        refused(a, b, "grads|weights")
+    setattr(a, name, m.Fp8Weight(torch.zeros(w.shape, dtype=torch.uint8), torch.zeros(w.shape[:2])))
+    refused(a, b, "bf16 weights")
