@@ -104,12 +104,24 @@ class TrainBuffers:
     forward_done: bool = False
 
 
-def _operand(t: torch.Tensor, name: str, shape, dtypes, device) -> None:
-    """Refuses what a call that takes ``t`` would refuse it for."""
+def _memory(t: torch.Tensor) -> Tuple[int, int]:
+    at = t.data_ptr()
+    return at, at + t.numel() * t.element_size()
+
+
+def _apart(who: str, name: str, memory: Tuple[int, int], others, what: str) -> None:
+    for lo, hi in others:
+        if memory[0] < hi and lo < memory[1]:
+            raise ValueError(f"{who}: {name} lies over {what}")
+
+
+def _operand(t: torch.Tensor, name: str, shape, dtypes, device) -> Tuple[int, int]:
+    """Refuses what a call that takes ``t`` would refuse it for; the memory of ``t``."""
     if t.shape != shape or t.dtype not in dtypes or t.device != device or not t.is_contiguous() or t.data_ptr() % 16:
         types = " or ".join(str(d).removeprefix("torch.") for d in dtypes)
         raise ValueError(f"train_backward: {name} must be contiguous {types} {tuple(shape)} on {device}, 16-byte aligned; got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return _memory(t)
 
 
 class MoeLayer:
@@ -428,6 +440,8 @@ class MoeLayer:
     def train_forward(self, logits: torch.Tensor, x: torch.Tensor, b: TrainBuffers) -> torch.Tensor:
         """The layer's output (``b.out``) for x [T, H], keeping in the buffers what ``train_backward`` needs.
         Gate and up are rounded to bf16 before SiLU * up, as on the gate/up LoRA path."""
+        _apart("train_forward", "x", _memory(x), map(_memory, (b.g, b.u, b.h, b.ys, b.out)),
+               "a buffer that the step replaces before its backward reads x")
         b.forward_done = False
         moe_route_align(logits, self.top_k, self.renormalize, self.bs, b.ids, b.w, b.routing)
         moe_grouped_gemm(MOE_OP_GATHER, x, self.gate, None, b.routing, out=b.g, workspace=b.ws)
@@ -447,7 +461,8 @@ class MoeLayer:
 
         Returns (d_x [T, H] bf16 and d_logits [T, E] fp32, of the buffers, and (d_gate, d_up, d_down)).
         ``grads``: where the weight gradients go, bf16 or fp32 [E, I, H], [E, I, H] and [E, H, I] (allocated
-        in bf16 without); with ``accumulate`` they are added to what is there."""
+        in bf16 without), each in memory of its own; with ``accumulate`` they are added to what is there.
+        ``d_out`` may be ``b.out``."""
         if not b.forward_done:
             raise ValueError("train_backward needs a train_forward on these buffers, once for each backward")
         if not self.renormalize and logits is None:
@@ -456,21 +471,27 @@ class MoeLayer:
             raise ValueError("train_backward: accumulate needs grads")
         bf, f32, device = (torch.bfloat16,), (torch.float32,), b.out.device
         # every operand before anything is added or replaced: a step that ends halfway could not be made again
-        _operand(d_out, "d_out", b.out.shape, bf, device)
-        _operand(x, "x", b.out.shape, bf, device)
+        d_out_at, x_at = _operand(d_out, "d_out", b.out.shape, bf, device), _operand(x, "x", b.out.shape, bf, device)
         if not self.renormalize:
             _operand(logits, "logits", b.d_logits.shape, f32, device)
         weights = self.gate, self.up, self.down
         shapes = (self.E, self.I, self.H), (self.E, self.I, self.H), (self.E, self.H, self.I)
+        read = [d_out_at, x_at]
         for w, shape in zip(weights, shapes):
             if not isinstance(w, Bf16Weight):
                 raise ValueError("train_backward: gradients go through bf16 weights only")
-            _operand(w.w, "one of the weights", shape, bf, device)
+            read.append(_operand(w.w, "one of the weights", shape, bf, device))
+        kept = [_memory(t) for t in (b.g, b.u, b.h, b.ys, b.out)]
+        _apart("train_backward", "d_out", d_out_at, kept[:3], "a buffer that is replaced before its last use")
+        _apart("train_backward", "x", x_at, kept, "a buffer that the step replaces before it reads x")
         if grads is None:
             grads = tuple(torch.empty_like(w.w) for w in weights)
         dg, du, dd = grads
         for t, shape in zip(grads, shapes):
-            _operand(t, "one of grads", shape, bf + f32, device)
+            at = _operand(t, "one of grads", shape, bf + f32, device)
+            _apart("train_backward", "one of grads", at, read, "another one or an operand")
+            _apart("train_backward", "one of grads", at, kept, "one of the step's buffers")
+            read.append(at)
         base = lambda t: t if accumulate else None
         r = b.routing
         b.forward_done = False

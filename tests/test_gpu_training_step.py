@@ -47,3 +47,31 @@ def test_refused_calls_add_nothing(m):
     d_x, d_l, _ = layer.train_backward(d_out, x, b, logits, grads=total, accumulate=True)
     assert torch.equal(d_x, want_x) and torch.equal(d_l, want_l)
     assert all(torch.equal(p, q) for p, q in zip(total, want))
+
+
+@pytest.mark.parametrize("place", ["out", "d_x"])
+def test_gradient_in_place_of_a_result(m, place):
+    """d_out in the memory of the output, or of the gradient of x, gives what it gives in memory of its own."""
+    T, H, I, E, k = 50, 264, 72, 6, 2
+    layer, logits, x, d_out = make(m, T, H, I, E, k)
+    b = layer.train_plan(T, "cuda", dropout=0.2, seed=4)
+    layer.train_forward(logits, x, b)
+    want_x, want_l, want = layer.train_backward(d_out, x, b)
+    want_x, want_l = want_x.clone(), want_l.clone()
+    layer.train_forward(logits, x, b)
+    there = getattr(b, place).copy_(d_out)
+    d_x, d_l, grads = layer.train_backward(there, x, b)
+    assert torch.equal(d_x, want_x) and torch.equal(d_l, want_l) and all(torch.equal(p, q) for p, q in zip(grads, want))
+
+
+def test_one_tensor_for_two_gradients_is_refused(m):
+    layer, logits, x, d_out = make(m, 20, 72, 40, 4, 2)
+    b = layer.train_plan(20, "cuda")
+    layer.train_forward(logits, x, b)
+    g = sums(layer, 0.5)
+    with pytest.raises(ValueError, match="grads"):
+        layer.train_backward(d_out, x, b, grads=(g[0], g[0], g[2]), accumulate=True)
+    with pytest.raises(ValueError, match="x lies over"):
+        layer.train_forward(logits, b.out, b)
+    assert all((t == 0.5).all() for t in g)
+    layer.train_backward(d_out, x, b, grads=g, accumulate=True)

@@ -91,3 +91,64 @@ def test_weights(name):
         refused(a, b, "grads|weights")
     setattr(a, name, m.Fp8Weight(torch.zeros(w.shape, dtype=torch.uint8), torch.zeros(w.shape[:2])))
     refused(a, b, "bf16 weights")
+
+
+# ------------------------------------------------------------------ memory that a step writes before it has read it all
+def at(t, shape, dtype=torch.bfloat16, byte=0):
+    """A tensor over ``t``'s memory from ``byte`` on."""
+    size = torch.Size(shape).numel() * torch.empty(0, dtype=dtype).element_size()
+    return t.view(-1).view(torch.uint8)[byte:byte + size].view(dtype).view(shape)
+
+
+def test_grads_over_each_other():
+    """gate and up have one shape: one tensor for both would hold their sum, or the later one."""
+    a = layer()
+    g = sums()
+    refused(a, ready(a), "grads", grads=[g[0], g[0], g[2]])
+    both = torch.full((E * I * H + 64,), 3.0)
+    refused(a, ready(a), "grads", grads=[both[:-64].view(E, I, H), both[64:].view(E, I, H), g[2]])
+
+
+@pytest.mark.parametrize("name", ["gate", "up", "down"])
+def test_grads_over_operands(name):
+    a = layer()
+    b = ready(a)
+    which = ["gate", "up", "down"].index(name)
+    g = sums()
+    g[which] = getattr(a, name).w
+    refused(a, b, "grads", grads=g)
+    room = bf(E * I * H)
+    g[which] = room.view(g[which].shape)
+    refused(a, b, "grads", grads=g, x=at(room, (T, H), byte=16))
+    refused(a, b, "grads", grads=g, d_out=at(room, (T, H), byte=room.numel() * 2 - T * H * 2))
+
+
+@pytest.mark.parametrize("name", ["g", "u", "h", "ys"])
+def test_operands_over_buffers(name):
+    a = layer()
+    b = ready(a)
+    over = at(getattr(b, name), (T, H), byte=16)
+    refused(a, b, "train_backward: x ", x=over)
+    with pytest.raises(ValueError, match="train_forward: x "):
+        a.train_forward(torch.zeros(T, E), over, b)
+    assert b.forward_done
+    if name != "ys":
+        refused(a, b, "train_backward: d_out ", d_out=over)
+
+
+def test_x_over_the_output():
+    """A layer's output in the buffers is replaced by the next forward on them: not its x as well."""
+    a = layer()
+    b = ready(a)
+    with pytest.raises(ValueError, match="train_forward: x "):
+        a.train_forward(torch.zeros(T, E), b.out, b)
+    refused(a, b, "train_backward: x ", x=b.out)
+
+
+@pytest.mark.parametrize("name", ["out", "d_x", "ys"])
+def test_gradients_in_place_of_results(name):
+    """d_out in the place of the output, of the gradient of x or of the experts' outputs is read before those are written."""
+    a = layer()
+    b = ready(a)
+    with pytest.raises(ValueError, match="HIP device"):
+        a.train_backward(at(getattr(b, name), (T, H)), bf(T, H), b, grads=sums())
