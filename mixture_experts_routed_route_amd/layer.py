@@ -102,6 +102,7 @@ class TrainBuffers:
     ones: torch.Tensor     # weights of the sum of the pairs' gradients of x
     ws: torch.Tensor
     forward_done: bool = False
+    forward_of: Optional["MoeLayer"] = None   # the layer whose forward they hold
 
 
 def _memory(t: torch.Tensor) -> Tuple[int, int]:
@@ -449,14 +450,15 @@ class MoeLayer:
         moe_silu_mul_dropout(b.g, b.u, b.routing, b.dropout, b.rng, out=b.h)
         moe_grouped_gemm(MOE_OP_DOWN, b.h, self.down, None, b.routing, out=b.ys, workspace=b.ws)
         moe_combine(b.ys, b.routing.inv_sorted, b.w, out=b.out)
-        b.forward_done = True
+        b.forward_done, b.forward_of = True, self
         return b.out
 
     def train_backward(self, d_out: torch.Tensor, x: torch.Tensor, b: TrainBuffers,
                        logits: Optional[torch.Tensor] = None, grads: Optional[Tuple[torch.Tensor, ...]] = None,
                        accumulate: bool = False):
-        """Gradients from that of the layer's output, ``d_out`` [T, H] bf16, after ``train_forward`` of the same x
-        on the same buffers (once: it replaces what the forward kept).  A layer that does not renormalise its
+        """Gradients from that of the layer's output, ``d_out`` [T, H] bf16, after this layer's ``train_forward`` of the
+        same x on the same buffers (once: it replaces what the forward kept; layers may share buffers where each one's
+        backward comes before the next one's forward).  A layer that does not renormalise its
         routing weights needs the ``logits`` again.
 
         Returns (d_x [T, H] bf16 and d_logits [T, E] fp32, of the buffers, and (d_gate, d_up, d_down)).
@@ -492,6 +494,10 @@ class MoeLayer:
             _apart("train_backward", "one of grads", at, read, "another one or an operand")
             _apart("train_backward", "one of grads", at, kept, "one of the step's buffers")
             read.append(at)
+        other = b.forward_of  # (another layer object over the same weights is the same layer)
+        if other is not self and (other is None or other.renormalize != self.renormalize or any(
+                v.w.data_ptr() != w.w.data_ptr() for v, w in zip((other.gate, other.up, other.down), weights))):
+            raise ValueError("train_backward: the buffers hold the forward of another layer")
         base = lambda t: t if accumulate else None
         r = b.routing
         b.forward_done = False

@@ -75,3 +75,24 @@ def test_one_tensor_for_two_gradients_is_refused(m):
         layer.train_forward(logits, b.out, b)
     assert all((t == 0.5).all() for t in g)
     layer.train_backward(d_out, x, b, grads=g, accumulate=True)
+
+
+def test_layers_that_share_buffers(m):
+    """In turn they may; a backward after the other one's forward is refused and takes nothing from it."""
+    T, H, I, E, k = 30, 72, 40, 4, 2
+    (a, logits, x, d_out), (c, *_) = make(m, T, H, I, E, k), make(m, T, H, I, E, k, seed=1)
+    b = a.train_plan(T, "cuda", dropout=0.2, seed=4)
+    want = []
+    for one in (a, c):
+        one.train_forward(logits, x, b)
+        want.append(one.train_backward(d_out, x, b)[2])
+    a.train_forward(logits, x, b)
+    c.train_forward(logits, x, b)
+    with pytest.raises(ValueError, match="another layer"):
+        a.train_backward(d_out, x, b)
+    got = c.train_backward(d_out, x, b)[2]
+    assert all(torch.equal(p, q) for p, q in zip(got, want[1]))
+    a.train_forward(logits, x, b)
+    again = m.MoeLayer(E, H, I, k, 16, a.gate, a.up, a.down)   # the same weights
+    got = again.train_backward(d_out, x, b)[2]
+    assert all(torch.equal(p, q) for p, q in zip(got, want[0]))

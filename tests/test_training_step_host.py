@@ -152,3 +152,20 @@ def test_gradients_in_place_of_results(name):
     b = ready(a)
     with pytest.raises(ValueError, match="HIP device"):
         a.train_backward(at(getattr(b, name), (T, H)), bf(T, H), b, grads=sums())
+
+
+# ------------------------------------------------------------------ whose forward the buffers hold
+def test_backward_of_another_layer():
+    """Layers that share buffers: a backward after another layer's forward would take that one's activations."""
+    a, c = layer(), layer()
+    b = ready(a)
+    refused(c, b, "another layer")
+    b.forward_of = None
+    refused(a, b, "another layer")
+    same = m.MoeLayer(E, H, I, K, BS, *(m.Bf16Weight(w.w.view_as(w.w)) for w in (a.gate, a.up, a.down)))
+    b.forward_of = a
+    with pytest.raises(ValueError, match="HIP device"):   # past the checks
+        same.train_backward(bf(T, H), bf(T, H), b, grads=sums())
+    b.forward_done = True
+    other = m.MoeLayer(E, H, I, K, BS, a.gate, a.up, a.down, renormalize=False)
+    refused(other, b, "another layer", logits=torch.zeros(T, E))
