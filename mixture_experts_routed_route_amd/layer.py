@@ -415,13 +415,16 @@ class MoeLayer:
         return self.combine(b)
 
     # ------------------------------------------------------------------ training
+    def _check_trains(self) -> None:
+        if not all(isinstance(w, Bf16Weight) for w in (self.gate, self.up, self.down)):
+            raise ValueError("training needs bf16 weights of the experts")
+        if self._tables():
+            raise ValueError("training does not take LoRA tables")
+
     def train_plan(self, T: int, device, dropout: float = 0.0, seed: int = 0, wait: bool = True) -> TrainBuffers:
         """Buffers of a training step of T tokens: one forward and its backward at a time.  ``dropout``: the
         probability that a hidden activation (SiLU(gate) * up) is dropped.  ``wait``: as for ``plan``."""
-        if not all(isinstance(w, Bf16Weight) for w in (self.gate, self.up, self.down)):
-            raise ValueError("training needs bf16 expert weights")
-        if self._tables():
-            raise ValueError("training does not take LoRA tables")
+        self._check_trains()
         if not 0.0 <= dropout < 1.0:
             raise ValueError(f"dropout is {dropout}; needs [0, 1)")
         r = Routing.allocate(T * self.top_k, self.top_k, self.E, self.bs, device)
@@ -441,6 +444,7 @@ class MoeLayer:
     def train_forward(self, logits: torch.Tensor, x: torch.Tensor, b: TrainBuffers) -> torch.Tensor:
         """The layer's output (``b.out``) for x [T, H], keeping in the buffers what ``train_backward`` needs.
         Gate and up are rounded to bf16 before SiLU * up, as on the gate/up LoRA path."""
+        self._check_trains()
         _apart("train_forward", "x", _memory(x), map(_memory, (b.g, b.u, b.h, b.ys, b.out)),
                "a buffer that the step replaces before its backward reads x")
         b.forward_done = False
@@ -471,6 +475,7 @@ class MoeLayer:
             raise ValueError("train_backward: without renormalised routing weights the logits are needed")
         if accumulate and grads is None:
             raise ValueError("train_backward: accumulate needs grads")
+        self._check_trains()
         bf, f32, device = (torch.bfloat16,), (torch.float32,), b.out.device
         # every operand before anything is added or replaced: a step that ends halfway could not be made again
         d_out_at, x_at = _operand(d_out, "d_out", b.out.shape, bf, device), _operand(x, "x", b.out.shape, bf, device)
@@ -480,8 +485,6 @@ class MoeLayer:
         shapes = (self.E, self.I, self.H), (self.E, self.I, self.H), (self.E, self.H, self.I)
         read = [d_out_at, x_at]
         for w, shape in zip(weights, shapes):
-            if not isinstance(w, Bf16Weight):
-                raise ValueError("train_backward: gradients go through bf16 weights only")
             read.append(_operand(w.w, "one of the weights", shape, bf, device))
         kept = [_memory(t) for t in (b.g, b.u, b.h, b.ys, b.out)]
         _apart("train_backward", "d_out", d_out_at, kept[:3], "a buffer that is replaced before its last use")

@@ -169,3 +169,26 @@ def test_backward_of_another_layer():
     b.forward_done = True
     other = m.MoeLayer(E, H, I, K, BS, a.gate, a.up, a.down, renormalize=False)
     refused(other, b, "another layer", logits=torch.zeros(T, E))
+
+
+@pytest.mark.parametrize("name", ["lora", "lora_gate", "lora_up"])
+def test_tables(name):
+    """LoRA tables are refused at every step, not by the plan alone: the buffers may be another layer's, and tables may come
+    after the plan.  Left out silently, the output would be the base layer's."""
+    b = layer().train_plan(T, "cpu")
+    a = layer(**{name: object()})
+    with pytest.raises(ValueError, match="LoRA"):
+        a.train_forward(torch.zeros(T, E), bf(T, H), b)
+    assert not b.forward_done
+    a = layer()
+    b = ready(a)
+    setattr(a, name, object())
+    refused(a, b, "LoRA")
+
+
+def test_forward_of_other_weights():
+    a = layer()
+    b = a.train_plan(T, "cpu")
+    a.up = m.Fp8Weight(torch.zeros((E, I, H), dtype=torch.uint8), torch.zeros((E, I)))
+    with pytest.raises(ValueError, match="bf16 weights"):
+        a.train_forward(torch.zeros(T, E), bf(T, H), b)
