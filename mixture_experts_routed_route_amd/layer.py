@@ -105,24 +105,31 @@ class TrainBuffers:
     forward_of: Optional["MoeLayer"] = None   # the layer whose forward they hold
 
 
+def _elsewhere(t: torch.Tensor) -> bool:
+    """Whether ``t`` is on another GPU than the current one, which launches would go to."""
+    return t.is_cuda and t.get_device() != torch.cuda.current_device()
+
+
 def _memory(t: torch.Tensor) -> Tuple[int, int]:
     at = t.data_ptr()
-    return at, at + t.numel() * t.element_size()
+    return at, at + t.nbytes
 
 
 def _apart(who: str, name: str, memory: Tuple[int, int], others, what: str) -> None:
+    first, end = memory
     for lo, hi in others:
-        if memory[0] < hi and lo < memory[1]:
+        if first < hi and lo < end:
             raise ValueError(f"{who}: {name} lies over {what}")
 
 
 def _operand(t: torch.Tensor, name: str, shape, dtypes, device) -> Tuple[int, int]:
     """Refuses what a call that takes ``t`` would refuse it for; the memory of ``t``."""
-    if t.shape != shape or t.dtype not in dtypes or t.device != device or not t.is_contiguous() or t.data_ptr() % 16:
+    at = t.data_ptr()
+    if t.shape != shape or t.dtype not in dtypes or t.device != device or not t.is_contiguous() or at % 16:
         types = " or ".join(str(d).removeprefix("torch.") for d in dtypes)
         raise ValueError(f"train_backward: {name} must be contiguous {types} {tuple(shape)} on {device}, 16-byte aligned; got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
-    return _memory(t)
+    return at, at + t.nbytes
 
 
 class MoeLayer:
@@ -444,7 +451,14 @@ class MoeLayer:
     def train_forward(self, logits: torch.Tensor, x: torch.Tensor, b: TrainBuffers) -> torch.Tensor:
         """The layer's output (``b.out``) for x [T, H], keeping in the buffers what ``train_backward`` needs.
         Gate and up are rounded to bf16 before SiLU * up, as on the gate/up LoRA path."""
+        if _elsewhere(b.out):
+            with torch.cuda.device(b.out.device):
+                return self.train_forward(logits, x, b)
         self._check_trains()
+        index = b.out.get_device()
+        for t, name in ((logits, "logits"), (x, "x"), (self.gate.w, "gate"), (self.up.w, "up"), (self.down.w, "down")):
+            if t.get_device() != index:
+                raise ValueError(f"train_forward: {name} is on {t.device}, the buffers on {b.out.device}")
         _apart("train_forward", "x", _memory(x), map(_memory, (b.g, b.u, b.h, b.ys, b.out)),
                "a buffer that the step replaces before its backward reads x")
         b.forward_done = False
@@ -462,13 +476,16 @@ class MoeLayer:
                        accumulate: bool = False):
         """Gradients from that of the layer's output, ``d_out`` [T, H] bf16, after this layer's ``train_forward`` of the
         same x on the same buffers (once: it replaces what the forward kept; layers may share buffers where each one's
-        backward comes before the next one's forward).  A layer that does not renormalise its
-        routing weights needs the ``logits`` again.
+        backward comes before the next one's forward).  A layer that does not renormalise its routing weights needs
+        the ``logits`` again.
 
         Returns (d_x [T, H] bf16 and d_logits [T, E] fp32, of the buffers, and (d_gate, d_up, d_down)).
         ``grads``: where the weight gradients go, bf16 or fp32 [E, I, H], [E, I, H] and [E, H, I] (allocated
         in bf16 without), each in memory of its own; with ``accumulate`` they are added to what is there.
         ``d_out`` may be ``b.out``."""
+        if _elsewhere(b.out):
+            with torch.cuda.device(b.out.device):
+                return self.train_backward(d_out, x, b, logits, grads, accumulate)
         if not b.forward_done:
             raise ValueError("train_backward needs a train_forward on these buffers, once for each backward")
         if not self.renormalize and logits is None:
@@ -499,7 +516,8 @@ class MoeLayer:
             read.append(at)
         other = b.forward_of  # (another layer object over the same weights is the same layer)
         if other is not self and (other is None or other.renormalize != self.renormalize or any(
-                v.w.data_ptr() != w.w.data_ptr() for v, w in zip((other.gate, other.up, other.down), weights))):
+                not isinstance(v, Bf16Weight) or v.w.data_ptr() != w.w.data_ptr()
+                for v, w in zip((other.gate, other.up, other.down), weights))):
             raise ValueError("train_backward: the buffers hold the forward of another layer")
         base = lambda t: t if accumulate else None
         r = b.routing

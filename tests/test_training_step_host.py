@@ -192,3 +192,80 @@ def test_forward_of_other_weights():
     a.up = m.Fp8Weight(torch.zeros((E, I, H), dtype=torch.uint8), torch.zeros((E, I)))
     with pytest.raises(ValueError, match="bf16 weights"):
         a.train_forward(torch.zeros(T, E), bf(T, H), b)
+
+
+# ------------------------------------------------------------------ another device than the current one
+class OnGpu1(torch.Tensor):
+    """A CPU tensor that says it is on GPU 1."""
+    is_cuda = True
+
+    @property
+    def device(self):
+        return torch.device("cuda", 1)
+
+    def get_device(self):
+        return 1
+
+
+OPS = ["moe_route_align", "moe_grouped_gemm", "moe_silu_mul_dropout", "moe_combine", "moe_grouped_gemm_dgrad",
+       "moe_silu_mul_backward", "moe_grouped_gemm_wgrad", "moe_route_backward"]
+
+
+@pytest.fixture
+def launches(monkeypatch):
+    """The current device of every call of an operator, with GPU 0 current outside; no call is made."""
+    import mixture_experts_routed_route_amd.layer as module
+    current, seen = [0], []
+
+    class Device:
+        def __init__(self, device):
+            self.index = torch.device(device).index
+
+        def __enter__(self):
+            current.append(self.index)
+
+        def __exit__(self, *_):
+            current.pop()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[-1])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    for name in OPS:
+        monkeypatch.setattr(module, name, lambda *args, _name=name, **kw: seen.append((_name, current[-1])))
+    return seen
+
+
+def on_gpu1():
+    a = layer()
+    b = a.train_plan(T, "cpu")
+    for w in (a.gate, a.up, a.down):
+        w.w = w.w.as_subclass(OnGpu1)
+    for name, t in vars(b).items():
+        if isinstance(t, torch.Tensor):
+            setattr(b, name, t.as_subclass(OnGpu1))
+    return a, b
+
+
+def test_step_on_another_device(launches):
+    """Every launch of a step goes to the buffers' device, whichever is current."""
+    a, b = on_gpu1()
+    gpu = lambda t: t.as_subclass(OnGpu1)
+    a.train_forward(gpu(torch.zeros(T, E)), gpu(bf(T, H)), b)
+    assert len(launches) == 6 and {d for _, d in launches} == {1}
+    launches.clear()
+    a.train_backward(gpu(bf(T, H)), gpu(bf(T, H)), b, grads=[gpu(g) for g in sums()])
+    assert len(launches) == 8 and {d for _, d in launches} == {1}
+    assert {n for n, _ in launches} == set(OPS) - {"moe_route_align", "moe_grouped_gemm", "moe_silu_mul_dropout"}
+
+
+@pytest.mark.parametrize("name", ["logits", "x", "gate", "up", "down"])
+def test_forward_over_two_devices(launches, name):
+    """An operand of another device than the buffers' would be read through its address on the wrong one."""
+    a, b = on_gpu1()
+    gpu = lambda t: t.as_subclass(OnGpu1)
+    args = {"logits": gpu(torch.zeros(T, E)), "x": gpu(bf(T, H))}
+    if name in args:
+        args[name] = args[name].as_subclass(torch.Tensor)
+    else:
+        setattr(a, name, m.Bf16Weight(getattr(a, name).w.as_subclass(torch.Tensor)))
+    with pytest.raises(ValueError, match=f"train_forward: {name} is on"):
+        a.train_forward(args["logits"], args["x"], b)
+    assert not launches
