@@ -76,7 +76,7 @@ moe_status moe_silu_mul_backward(const uint16_t* gate, const uint16_t* up, const
  * e: the gradient of the input of y = x W^T.  Exact bf16 products, fp32 sums, one rounding to bf16.
  *   dy0, dy1   bf16 [max_pad, N] by sorted row, or (by_token) [num_pairs / top_k, N] by token
  *   w0, w1     MOE_W_BF16 weights [E, N, K]; w1 and dy1 are NULL without a second pair
- *   dx         bf16 [max_pad, K], no operand's buffer; sentinel and padding rows are not written
+ *   dx         bf16 [max_pad, K], apart from every operand; sentinel and padding rows are not written
  * N and K multiples of 8, up to 2^20, num_experts <= 256, max_pad < 2^31 - 1024 (MOE_EUNSUPPORTED above).
  * workspace: NULL, or one of moe_grouped_gemm (the same buffer, zero-filled before its first use; every call
  * leaves its counters at zero; calls that share one must not overlap).  With it, launches of few tiles divide
@@ -91,8 +91,8 @@ moe_status moe_grouped_gemm_dgrad(const uint16_t* dy0, const moe_weight* w0, con
  * the weights of y = x W^T.  Exact bf16 products, fp32 sums.  Experts without rows get base, or zeros.
  *   dy         bf16 [max_pad, N] by sorted row, or (dy_by_token) [num_pairs / top_k, N] by token
  *   x          bf16 [max_pad, K] by sorted row, or (x_by_token) [num_pairs / top_k, K] by token
- *   dw         [E, N, K], bf16 (one rounding, after base is added) or, with dw_fp32, fp32; not dy's or x's buffer
- *   base       NULL, or of dw's type and shape; may be dw (gradients summed over batches)
+ *   dw         [E, N, K], bf16 (one rounding, after base is added) or, with dw_fp32, fp32; apart from dy and x
+ *   base       NULL, or of dw's type and shape; dw (gradients summed over batches), or apart from it
  * N and K multiples of 8, up to 2^20, num_experts <= 256, max_pad < 2^31 - 1024 (MOE_EUNSUPPORTED above).  workspace: as for
  * moe_grouped_gemm_dgrad; with it, launches of few tiles divide long sums over rows among workgroups.
  * num_pairs == 0 writes base or zeros. */

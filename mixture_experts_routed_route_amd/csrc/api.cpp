@@ -932,6 +932,12 @@ uint32_t dropped_below(double p) {
     return v >= 65535.0 ? 65535u : static_cast<uint32_t>(v);
 }
 
+// whether two arrays have memory in common
+bool share(const void* a, int64_t bytes_a, const void* b, int64_t bytes_b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + static_cast<uintptr_t>(bytes_b) && y < x + static_cast<uintptr_t>(bytes_a);
+}
+
 // sizes that every grouped gradient call shares
 moe_status check_grad(const char* who, int64_t num_pairs, int32_t top_k, int32_t num_experts, int32_t n, int32_t k,
                       int32_t block_size, int64_t max_pad, const void* workspace, int64_t workspace_bytes) {
@@ -1036,8 +1042,12 @@ moe_status moe_grouped_gemm_dgrad(const uint16_t* dy0, const moe_weight* w0, con
         REQUIRE_PTR(who, dy1);
         REQUIRE_PTR(who, w1->data);
     }
-    // (rows are read for one tile after they were written for another)
-    REQUIRE(dx != dy0 && dx != dy1, "%s: dx is one buffer with an operand", who);
+    // (operands are read for one tile after another one was written)
+    const int64_t dy_bytes = 2 * n * (by_token ? num_pairs / top_k : max_pad), w_bytes = INT64_C(2) * num_experts * n * k;
+    const int64_t dx_bytes = 2 * max_pad * k;
+    REQUIRE(!share(dx, dx_bytes, dy0, dy_bytes) && !share(dx, dx_bytes, dy1, dy_bytes) &&
+                !share(dx, dx_bytes, w0->data, w_bytes) && !(w1 && share(dx, dx_bytes, w1->data, w_bytes)),
+            "%s: dx is one buffer with an operand", who);
     return launched(who, moe::launch_dgrad(dy0, static_cast<const uint16_t*>(w0->data), dy1,
                                            w1 ? static_cast<const uint16_t*>(w1->data) : nullptr, dx, sorted_ids,
                                            expert_offsets, static_cast<int>(num_pairs), top_k, num_experts, n, k,
@@ -1062,7 +1072,11 @@ moe_status moe_grouped_gemm_wgrad(const uint16_t* dy, const uint16_t* x, void* d
         REQUIRE_PTR(who, sorted_ids);
         REQUIRE_PTR(who, expert_offsets);
     }
-    REQUIRE(num_pairs == 0 || (dw != dy && dw != x), "%s: dw is one buffer with an operand", who);
+    const int64_t dw_bytes = INT64_C(1) * num_experts * n * k * (dw_fp32 ? 4 : 2);
+    const int64_t dy_rows = dy_by_token ? num_pairs / top_k : max_pad, x_rows = x_by_token ? num_pairs / top_k : max_pad;
+    REQUIRE(num_pairs == 0 || (!share(dw, dw_bytes, dy, 2 * n * dy_rows) && !share(dw, dw_bytes, x, 2 * k * x_rows)),
+            "%s: dw is one buffer with an operand", who);
+    REQUIRE(base == dw || !share(dw, dw_bytes, base, dw_bytes), "%s: base lies over a part of dw", who);
     return launched(who, moe::launch_wgrad(dy, x, dw, base, dw_fp32 != 0, sorted_ids, expert_offsets,
                                            static_cast<int>(num_pairs), top_k, num_experts, n, k,
                                            static_cast<int>(max_pad), dy_by_token ? 1 : 0, x_by_token ? 1 : 0, workspace,
