@@ -47,7 +47,7 @@ extern "C" {
 
 /* h[r] = bf16(SiLU(gate[r]) * up[r] * mask), in fp32, for the rows r with sorted_ids[r] in [0, num_pairs); other
  * rows are not written.  Without sorted_ids every row r is pair r.
- *   gate, up, out  bf16 [rows, n]; out may be gate or up
+ *   gate, up, out  bf16 [rows, n]; out may be gate or up, else it is apart from both
  *   p_drop         in [0, 1); rng may be NULL where it is 0
  * n % 8 == 0, rows * n up to 2^35 (MOE_EUNSUPPORTED above).  rows == 0, or num_pairs == 0 with sorted_ids,
  * enqueues nothing. */
@@ -63,7 +63,8 @@ moe_status moe_silu_mul_dropout(const uint16_t* gate, const uint16_t* up, uint16
  *   h_weighted = bf16(w * h)            the x of moe_grouped_gemm_wgrad for the down projection
  *   d_topk_w[p] = sum over columns of d * h, in fp32, h not rounded
  *   topk_w fp32 [num_pairs]; without sorted_ids every row r is pair r, and num_pairs >= rows.
- * Each of d_gate, d_up and h_weighted may be one of gate, up and d (not two of them the same buffer).
+ * Each of d_gate, d_up and h_weighted may be one of gate, up and d, else it is apart from them; the outputs are
+ * apart from each other.
  * Rows without a pair are not written, nor are the d_topk_w of pairs without a row (an expert id out of
  * range).  n % 8 == 0, rows below 2^24 (MOE_EUNSUPPORTED above).  rows == 0, or num_pairs == 0 with sorted_ids,
  * enqueues nothing. */
@@ -109,7 +110,8 @@ moe_status moe_grouped_gemm_wgrad(const uint16_t* dy, const uint16_t* x, void* d
  *     d_logits[t, e] = p_e * (sum of d_w_j with ids[t, j] == e - sum_i w_i d_w_i)
  *   topk_ids i32, topk_w and d_topk_w fp32 [T, top_k]; pairs with an id outside [0, E) count as d_w = 0, and
  *   their d_topk_w is not read
- *   d_logits fp32 [T, E], every entry written
+ *   d_logits fp32 [T, E], every entry written; apart from topk_ids, topk_w and d_topk_w (where top_k == E it may
+ *   be one of them), and logits or apart from it
  * num_experts and top_k <= 256 (MOE_EUNSUPPORTED above).  num_tokens == 0 enqueues nothing. */
 moe_status moe_route_backward(const int32_t* topk_ids, const float* topk_w, const float* d_topk_w,
                               const float* logits, int32_t num_tokens, int32_t num_experts, int32_t top_k,

@@ -926,16 +926,19 @@ moe_status moe_few_tokens(const float* logits, const uint16_t* x, const moe_weig
 // ------------------------------------------------------------------ training operators (moe_training.h)
 namespace {
 
-// 16-bit random numbers below this drop their value
-uint32_t dropped_below(double p) {
-    const double v = p * 65536.0 + 0.5;
-    return v >= 65535.0 ? 65535u : static_cast<uint32_t>(v);
-}
-
 // whether two arrays have memory in common
 bool share(const void* a, int64_t bytes_a, const void* b, int64_t bytes_b) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return a && b && x < y + static_cast<uintptr_t>(bytes_b) && y < x + static_cast<uintptr_t>(bytes_a);
+}
+
+// an elementwise result: one of the inputs, or apart from it
+bool shifted(const void* out, const void* in, int64_t bytes) { return out != in && share(out, bytes, in, bytes); }
+
+// 16-bit random numbers below this drop their value
+uint32_t dropped_below(double p) {
+    const double v = p * 65536.0 + 0.5;
+    return v >= 65535.0 ? 65535u : static_cast<uint32_t>(v);
 }
 
 // sizes that every grouped gradient call shares
@@ -982,6 +985,8 @@ moe_status moe_silu_mul_dropout(const uint16_t* gate, const uint16_t* up, uint16
     REQUIRE_PTR(who, up);
     REQUIRE_PTR(who, out);
     if (sorted_ids) REQUIRE_PTR(who, sorted_ids);
+    const int64_t bytes = 2 * rows * n;
+    REQUIRE(!shifted(out, gate, bytes) && !shifted(out, up, bytes), "%s: out lies over a part of an input", who);
     const uint32_t below = dropped_below(p_drop);
     if (below) REQUIRE_PTR(who, rng);
     return launched(who, moe::launch_silu_mul_dropout(gate, up, out, sorted_ids, static_cast<int>(num_pairs), rows, n,
@@ -1001,7 +1006,10 @@ moe_status moe_silu_mul_backward(const uint16_t* gate, const uint16_t* up, const
     REQUIRE(p_drop >= 0.0 && p_drop < 1.0, "%s: p_drop %g not in [0, 1)", who, p_drop);
     if (rows == 0 || (sorted_ids && num_pairs == 0)) return ok();
     if (rows >= (1 << 24)) return fail(MOE_EUNSUPPORTED, "%s: rows %lld >= 2^24", who, static_cast<long long>(rows));
-    REQUIRE(d_gate != d_up && d_gate != h_weighted && d_up != h_weighted, "%s: two outputs are one buffer", who);
+    const int64_t bytes = 2 * rows * n;
+    REQUIRE(!share(d_gate, bytes, d_up, bytes) && !share(d_gate, bytes, h_weighted, bytes) &&
+                !share(d_up, bytes, h_weighted, bytes),
+            "%s: two outputs are one buffer", who);
     REQUIRE_PTR(who, gate);
     REQUIRE_PTR(who, up);
     REQUIRE_PTR(who, d);
@@ -1013,6 +1021,14 @@ moe_status moe_silu_mul_backward(const uint16_t* gate, const uint16_t* up, const
     if (sorted_ids) REQUIRE_PTR(who, sorted_ids);
     const uint32_t below = dropped_below(p_drop);
     if (below) REQUIRE_PTR(who, rng);
+    for (const void* out : {d_gate, d_up, h_weighted}) {
+        REQUIRE(!shifted(out, gate, bytes) && !shifted(out, up, bytes) && !shifted(out, d, bytes),
+                "%s: an output lies over a part of an input", who);
+        REQUIRE(!share(out, bytes, topk_w, 4 * num_pairs) && !share(out, bytes, d_topk_w, 4 * num_pairs),
+                "%s: an output lies over topk_w or d_topk_w", who);
+    }
+    for (const void* in : {gate, up, d})
+        REQUIRE(!share(in, bytes, d_topk_w, 4 * num_pairs), "%s: d_topk_w lies over an input", who);
     return launched(who, moe::launch_silu_mul_backward(gate, up, d, topk_w, sorted_ids, static_cast<int>(num_pairs), rows,
                                                        n, below, rng, d_gate, d_up, h_weighted, d_topk_w,
                                                        static_cast<hipStream_t>(stream)));
@@ -1099,6 +1115,12 @@ moe_status moe_route_backward(const int32_t* topk_ids, const float* topk_w, cons
     REQUIRE_PTR(who, d_topk_w);
     REQUIRE_PTR(who, d_logits);
     if (logits) REQUIRE_PTR(who, logits);
+    // (a token's wave reads all it needs before it writes)
+    const int64_t out_bytes = INT64_C(4) * num_tokens * num_experts, in_bytes = INT64_C(4) * num_tokens * top_k;
+    REQUIRE(!shifted(d_logits, logits, out_bytes), "%s: d_logits lies over a part of logits", who);
+    for (const void* in : {static_cast<const void*>(topk_ids), static_cast<const void*>(topk_w), static_cast<const void*>(d_topk_w)})
+        REQUIRE((in == d_logits && top_k == num_experts) || !share(d_logits, out_bytes, in, in_bytes),
+                "%s: d_logits lies over topk_ids, topk_w or d_topk_w", who);
     return launched(who, moe::launch_route_backward(topk_ids, topk_w, d_topk_w, logits, num_tokens, num_experts, top_k,
                                                     d_logits, static_cast<hipStream_t>(stream)));
 }

@@ -65,3 +65,51 @@ def test_wgrad(L, call):
 def test_base(L, call):
     """base may be dw: each value is read by the thread that writes it.  Shifted, another tile writes it first."""
     refused(L, call, "base lies over a part of dw")
+
+
+# ------------------------------------------------------------------ row kernels
+ROWS, COLS = 40, 64
+SIZE, PAIRS = ROWS * COLS * 2, ROWS * 4
+
+
+def drop(out, gate=MB, up=2 * MB):
+    return "moe_silu_mul_dropout", (gate, up, out, None, ROWS, ROWS, COLS, 0.0, None, None)
+
+
+def back(dg=11 * MB, du=12 * MB, hw=13 * MB, dw=14 * MB, gate=MB, up=2 * MB, d=3 * MB, w=4 * MB):
+    return "moe_silu_mul_backward", (gate, up, d, w, None, ROWS, ROWS, COLS, 0.0, None, dg, du, hw, dw, None)
+
+
+@pytest.mark.parametrize("call", [drop(MB + 16), drop(MB - 16), drop(2 * MB + SIZE - 16), drop(2 * MB, gate=2 * MB + 128)])
+def test_shifted_result(L, call):
+    """out may be gate or up: a thread loads what it replaces.  Shifted by a row or a chunk, another thread replaces it."""
+    refused(L, call, "out lies over a part of an input")
+
+
+@pytest.mark.parametrize("call", [back(dg=MB + 16), back(du=2 * MB - 128), back(hw=3 * MB + SIZE - 16), back(dg=3 * MB - SIZE + 16)])
+def test_shifted_gradients(L, call):
+    refused(L, call, "an output lies over a part of an input")
+
+
+@pytest.mark.parametrize("call", [back(dg=12 * MB + 16), back(du=13 * MB - 16), back(hw=11 * MB + SIZE - 16)])
+def test_gradients_over_each_other(L, call):
+    refused(L, call, "two outputs are one buffer")
+
+
+@pytest.mark.parametrize("call", [back(dg=4 * MB), back(hw=4 * MB + PAIRS - 16), back(du=14 * MB - SIZE + 16), back(dw=MB),
+                                  back(dw=3 * MB + SIZE - 16)])
+def test_gradients_over_weights_of_rows(L, call):
+    refused(L, call, "topk_w")
+
+
+def rback(out, ids=MB, w=2 * MB, dw=3 * MB, logits=None, T=40, experts=8, k=2):
+    return "moe_route_backward", (ids, w, dw, logits, T, experts, k, out, None)
+
+
+@pytest.mark.parametrize("call,what", [
+    (rback(MB), "topk_ids"), (rback(2 * MB), "topk_w"), (rback(3 * MB), "d_topk_w"), (rback(3 * MB - 40 * 8 * 4 + 16), "d_topk_w"),
+    (rback(2 * MB + 40 * 2 * 4 - 16), "topk_w"), (rback(3 * MB + 16, k=8), "d_topk_w"),
+    (rback(4 * MB + 32, logits=4 * MB), "a part of logits"), (rback(4 * MB - 16, logits=4 * MB), "a part of logits")])
+def test_route_backward(L, call, what):
+    """A token's row of d_logits over other tokens' operands, which their waves may not have read."""
+    refused(L, call, what)
