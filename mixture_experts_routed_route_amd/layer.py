@@ -430,7 +430,9 @@ class MoeLayer:
 
     def train_plan(self, T: int, device, dropout: float = 0.0, seed: int = 0, wait: bool = True) -> TrainBuffers:
         """Buffers of a training step of T tokens: one forward and its backward at a time.  ``dropout``: the
-        probability that a hidden activation (SiLU(gate) * up) is dropped.  ``wait``: as for ``plan``."""
+        probability that a hidden activation (SiLU(gate) * up) is dropped.  ``seed``, with offset 0, goes to ``b.rng``,
+        of which the masks are a function: layers of a model need seeds of their own (the same seed is the same
+        masks), and every step another offset, which the steps do not advance.  ``wait``: as for ``plan``."""
         self._check_trains()
         if not 0.0 <= dropout < 1.0:
             raise ValueError(f"dropout is {dropout}; needs [0, 1)")
@@ -450,7 +452,9 @@ class MoeLayer:
 
     def train_forward(self, logits: torch.Tensor, x: torch.Tensor, b: TrainBuffers) -> torch.Tensor:
         """The layer's output (``b.out``) for x [T, H], keeping in the buffers what ``train_backward`` needs.
-        Gate and up are rounded to bf16 before SiLU * up, as on the gate/up LoRA path."""
+        Gate and up are rounded to bf16 before SiLU * up, as on the gate/up LoRA path.  With dropout the masks are those
+        of ``b.rng`` as it stands: change the offset before the next forward (``b.rng[1] += 1``), or it drops the same
+        values again; left as it is, a forward can be made again for its backward (recomputation)."""
         if _elsewhere(b.out):
             with torch.cuda.device(b.out.device):
                 return self.train_forward(logits, x, b)

@@ -96,3 +96,18 @@ def test_layers_that_share_buffers(m):
     again = m.MoeLayer(E, H, I, k, 16, a.gate, a.up, a.down)   # the same weights
     got = again.train_backward(d_out, x, b)[2]
     assert all(torch.equal(p, q) for p, q in zip(got, want[0]))
+
+
+def test_masks_follow_rng_alone(m):
+    """The steps leave seed and offset as they are: the same masks until the caller changes one of them."""
+    T = 30
+    layer, logits, x, d_out = make(m, T, 72, 104, 4, 2)
+    b = layer.train_plan(T, "cuda", dropout=0.5, seed=4)
+    first = layer.train_forward(logits, x, b).clone()
+    layer.train_backward(d_out, x, b)
+    assert b.rng.tolist() == [4, 0]
+    assert torch.equal(layer.train_forward(logits, x, b), first)
+    assert torch.equal(layer.train_forward(logits, x, layer.train_plan(T, "cuda", dropout=0.5, seed=4)), first)
+    b.rng[1] += 1
+    assert not torch.equal(layer.train_forward(logits, x, b), first)
+    assert not torch.equal(layer.train_forward(logits, x, layer.train_plan(T, "cuda", dropout=0.5, seed=5)), first)
