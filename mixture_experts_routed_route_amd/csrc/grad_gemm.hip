@@ -100,6 +100,8 @@ struct __attribute__((aligned(16))) Tile {
     int en;          // expert | column tile << 8; < 0: no more tiles
 };
 
+// ---- Lists of tiles and addresses in LDS: whole numbers alone, so that a test compiles these for the CPU as they stand.
+
 // wgrad: the tiles of an expert that go to one XCD together, and how many such units it has
 __host__ __device__ __forceinline__ void units_of(int tiles_e, int tiles, int& unit, int& units_e) {
     units_e = (tiles_e + 31) / 32;
@@ -111,6 +113,55 @@ __host__ __device__ __forceinline__ void units_of(int tiles_e, int tiles, int& u
     }
     unit = (tiles_e + units_e - 1) / units_e;
 }
+
+// the expert's unit that XCD xcd gets in round v: back and forth over the XCDs
+__host__ __device__ __forceinline__ int unit_of_round(int v, int xcd) { return v * 8 + ((v & 1) ? 7 - xcd : xcd); }
+
+// row and column tile of tile idx: bands of kBand row tiles, row tiles fastest, so that tiles that run together share
+// operands in L2
+__host__ __device__ __forceinline__ void tile_of(int idx, int row_tiles, int n_tiles, int& m_t, int& n_t) {
+    const int band = idx / (kBand * n_tiles);
+    const int at = idx - band * kBand * n_tiles;
+    const int left = row_tiles - band * kBand, rows = left < kBand ? left : kBand;
+    n_t = at / rows;
+    m_t = band * kBand + at - n_t * rows;
+}
+
+// pieces of a tile where a launch of `grid` workgroups with a workspace has T of them, the longest of `most` halves
+__host__ __device__ __forceinline__ int pieces_of(int T, int grid, int most) {
+    if (T <= 0 || 2 * T > grid) return 1;
+    int n = (grid < kMaxPieces ? grid : kMaxPieces) / T;
+    n = n < kMaxSplit ? n : kMaxSplit;
+    n = n < most / kMinPiece ? n : most / kMinPiece;
+    return n > 1 ? n : 1;
+}
+
+// workgroups per XCD for `tiles` tiles, of which an XCD's list has at most `entries`
+__host__ __device__ __forceinline__ int64_t per_xcd_for(int64_t tiles, int64_t entries, bool ws, int cus) {
+    const int64_t most = cus / 8 > 1 ? cus / 8 : 1, want = (tiles + 7) / 8;
+    const int64_t n = ws || want > most ? most : want;
+    return entries > n * kTab ? (entries + kTab - 1) / kTab : n;
+}
+
+// Operands read by columns.  First of the eight columns that load q of `wave` puts where its lane's 16 bytes go; and the
+// bytes from a slot's start to what `lane` reads of 16 columns from block * 16 (block < 8; 8 further on: + 256 bytes).
+__host__ __device__ __forceinline__ int column_loaded(int wave, int lane, int q) {
+    return ((lane & 31) ^ (((q * 2 + (lane >> 5)) << 2) | ((((wave >> 1) ^ (wave >> 2)) & 1) << 1))) * 8;
+}
+__host__ __device__ __forceinline__ int column_read(int lane, int block) {
+    const int i16 = lane & 15, gr = lane >> 4, row = gr * 8 + (i16 >> 2), bit = (gr ^ (gr >> 1)) & 1;
+    return row * 512 + (((((block >> 1) ^ (i16 >> 2)) << 2) | (((block & 1) ^ bit) << 1) | ((i16 & 3) >> 1)) << 4) + (i16 & 1) * 8;
+}
+// dy of dgrad: first contraction index of the lane's 16 bytes of a row, and where it reads row wm * 16 + lane % 16
+__host__ __device__ __forceinline__ int row_loaded(int lane) { return ((lane & 3) ^ ((lane >> 4) & 3)) * 8; }
+__host__ __device__ __forceinline__ int row_read(int lane, int wm) {
+    const int i16 = lane & 15, gr = lane >> 4;
+    return (wm * 16 + i16) * 64 + ((gr ^ (i16 >> 2)) << 4);
+}
+// results on their way out: 16-byte chunk `chunk` of row `row` in the wave's 1 KB
+__host__ __device__ __forceinline__ int staged(int row, int chunk) { return row * 64 + (chunk ^ (row >> 2 & 3)) * 16; }
+
+// ---- (end)
 
 // DGRAD: bf16 out; else wgrad with bf16 (F32 false) or fp32 results
 template <bool DGRAD, bool F32>
@@ -174,8 +225,7 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     int pieces = 1;
     if (g.part && T > 0 && 2 * T <= static_cast<int>(gridDim.x)) {
         const int most = DGRAD ? (g.r1 ? 2 * nkh : nkh) : halves_of(s_order[0]);
-        pieces = min(min(min(static_cast<int>(gridDim.x), kMaxPieces) / T, kMaxSplit), most / kMinPiece);
-        pieces = max(__builtin_amdgcn_readfirstlane(pieces), 1);
+        pieces = __builtin_amdgcn_readfirstlane(pieces_of(T, gridDim.x, most));
     }
 
     // ---- this workgroup's list of tiles.  An XCD's tiles are dealt to its workgroups in turn, entries slot,
@@ -186,16 +236,10 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     if constexpr (!DGRAD) units_of(tiles_e, T, unit, units_e);
     const int units = E * units_e, xcd_units = (units + 7) / 8;
     const int l_n = DGRAD ? static_cast<int>(static_cast<long long>(T) * (xcd + 1) / 8) - l_lo : xcd_units * unit;
-    auto unit_at = [&](int v) __attribute__((always_inline)) { return v * 8 + ((v & 1) ? 7 - xcd : xcd); };
     // tile idx (dgrad: of all; wgrad: of expert e)
     auto tile_at = [&](int idx, int e) __attribute__((always_inline)) {
-        // bands of kBand row tiles, row tiles fastest: tiles that run together share operands in L2
-        const int m_lim = DGRAD ? m_real : r_tiles;
-        const int band = idx / (kBand * n_tiles);
-        const int at = idx - band * kBand * n_tiles;
-        const int rows = min(kBand, m_lim - band * kBand);
-        const int n_t = at / rows;
-        const int m_t = band * kBand + at - n_t * rows;
+        int m_t, n_t;
+        tile_of(idx, DGRAD ? m_real : r_tiles, n_tiles, m_t, n_t);
         Tile s;
         if constexpr (DGRAD) {
             int hi = E - 1;  // e: the largest expert whose first row tile is <= m_t
@@ -238,7 +282,7 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
         if constexpr (DGRAD) {
             s = tile_at(l_lo + i, 0);
         } else {
-            const int u = unit_at(i / unit), idx = (u % units_e) * unit + i % unit;
+            const int u = unit_of_round(i / unit, xcd), idx = (u % units_e) * unit + i % unit;
             if (u >= units || idx >= tiles_e) return false;
             s = tile_at(idx, s_order[u / units_e]);
         }
@@ -316,10 +360,10 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     int at[2], chunk_c[2], col_r[2], col_c[2];
     uint32_t lane_c[2];         // dgrad: bytes from a half's first row of W to this lane's
 #pragma unroll
-    for (int q = 0; q < 2; ++q) chunk_c[q] = ((lane & 31) ^ (((q * 2 + half) << 2) | ((((wave >> 1) ^ (wave >> 2)) & 1) << 1))) * 8;
+    for (int q = 0; q < 2; ++q) chunk_c[q] = column_loaded(wave, lane, q);
 #pragma unroll
     for (int q = 0; q < 2; ++q) lane_c[q] = static_cast<uint32_t>(wave * 4 + q * 2 + half) * (static_cast<uint32_t>(K) * 2);
-    const int k_r = ((lane & 3) ^ ((lane >> 4) & 3)) * 8;   // dgrad: first n of this lane's chunk of a row of dy
+    const int k_r = row_loaded(lane);   // dgrad: first n of this lane's chunk of a row of dy
     const ulonglong2* row_p = s_ptr;   // wgrad: the row addresses of the coming half
     // what can be issued from half i_h of the segment on
     auto move = [&](bool first) __attribute__((always_inline)) {
@@ -459,16 +503,11 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     // Fragment offsets in bytes within a slot.  A lane of the 16x16x32 MFMA holds 8 contraction indices from
     // 8 * (lane / 16) of row or column lane % 16.  Transposed reads: lane i16 of group gr of 16 lanes reads 8 bytes of
     // contraction row gr * 8 + i16 / 4 (+ 4 in the second read), columns (i16 % 4) * 4.
-    const int i16 = lane & 15, gr = lane >> 4;
-    auto tr_off = [&](int block) __attribute__((always_inline)) {   // 16 columns from block * 16, block < 8
-        const int row = gr * 8 + (i16 >> 2), bit = (gr ^ (gr >> 1)) & 1;
-        return row * 512 + (((((block >> 1) ^ (i16 >> 2)) << 2) | (((block & 1) ^ bit) << 1) | ((i16 & 3) >> 1)) << 4) + (i16 & 1) * 8;
-    };
     int c_off[4], r_off[2];      // blocks 8 further on lie 256 bytes further on
 #pragma unroll
-    for (int j = 0; j < 4; ++j) c_off[j] = kPartB + tr_off((j >> 1) * 4 + wn * 2 + (j & 1));
+    for (int j = 0; j < 4; ++j) c_off[j] = kPartB + column_read(lane, (j >> 1) * 4 + wn * 2 + (j & 1));
 #pragma unroll
-    for (int i = 0; i < 2; ++i) r_off[i] = DGRAD ? (wm * 16 + i16) * 64 + ((gr ^ (i16 >> 2)) << 4) : tr_off(i * 4 + wm);
+    for (int i = 0; i < 2; ++i) r_off[i] = DGRAD ? row_read(lane, wm) : column_read(lane, i * 4 + wm);
 
     f32x4 acc[4][8];
     bf16x8 fa[4], fb[8];
@@ -565,9 +604,9 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
         asm volatile("" : "+v"(ln), "+s"(wv));
         const int em = wv >> 1, en = wv & 1, sr = ln >> 2;   // the row of this lane's pieces
         char* const stage = s_stage + wv * 1024;
-        char* const mine = stage + sr * 64 + ((ln & 3) ^ (sr >> 2 & 3)) * 16;
+        char* const mine = stage + staged(sr, ln & 3);
         const int br = ln & 15, bg = ln >> 4;                // row and columns of its values of a block
-        auto of_block = [&](int chunk) __attribute__((always_inline)) { return stage + br * 64 + (chunk ^ (br >> 2)) * 16; };
+        auto of_block = [&](int chunk) __attribute__((always_inline)) { return stage + staged(br, chunk); };
         uint32_t ok = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -784,10 +823,7 @@ hipError_t grid_for(int64_t tiles, int64_t entries, bool ws, int& grid) {
     int cus = 0;
     const hipError_t err = device_cus(cus);
     if (err != hipSuccess) return err;
-    const int64_t most = cus / 8 > 1 ? cus / 8 : 1, want = (tiles + 7) / 8;   // per XCD
-    int64_t n = ws || want > most ? most : want;
-    if (entries > n * kTab) n = (entries + kTab - 1) / kTab;
-    grid = static_cast<int>(n * 8);
+    grid = static_cast<int>(per_xcd_for(tiles, entries, ws, cus) * 8);
     return hipSuccess;
 }
 
