@@ -21,13 +21,19 @@
 // against 1812.
 //
 // What bounds it: at 8 x (1024 x 4096 x 14336), 0.96 TFLOP, dgrad takes 887 us (1.08 PFLOP/s) and
-// wgrad 864 us (1.11); eight library products of these layouts take 798 to 849 and 1020 us.  Matrix
-// cores are busy for 59% of the cycles at a clock that falls to 1.7 GHz under the load; bank conflicts take 2 to 8%
-// of the cycles.  The loads' path is what the rest waits for: without the loads in the
-// main loop the same products take 618 and 820 us.  Their average latency is 450 cycles, far less than
-// they are issued ahead; dgrad's rows of dy come in pieces of 64 bytes, half a line each.  Tiles of few halves are bound
-// by their ends (wgrad of 64 experts of 192 rows, 1408 x 4096: 263 us, 3.0 TB/s): an epilogue is 3000 cycles per group,
-// as much as two halves, and moving the loads to the next tile as much again.
+// wgrad 868 us (1.11); eight library products of these layouts take 798 to 849 and 1020 us.  Matrix
+// cores are busy for 60 and 56% of the cycles at a clock that falls to 1.6 to 1.9 GHz under the load; bank conflicts take
+// 8 and 2% of the cycles.  The loads' path is what the rest waits for: without the loads in the
+// main loop the same products take 618 and 820 us.  Their average latency is 400 cycles, far less than
+// they are issued ahead; the address unit is busy for 77 and 57% of the cycles, since dgrad's rows of dy come in pieces
+// of 64 bytes, half a line each.  A tile of few rows is loaded as a whole one (copies of a row that is there), so what
+// counts of skewed experts' row tiles is how full they are: 73% (128 of them, 768 x 2048, two pairs: 456 us).
+// Tiles of few halves are bound by that and by their ends (wgrad of 64 experts of 192 rows, 1408 x 4096: 263 us, 3.0
+// TB/s): of 19 to 20 thousand cycles a tile its 7 halves take 14, 1400 to 1500 each where nothing waits and 1000 to 2000
+// more in three of them, which wait for loads queued behind the stores of the last tile; an epilogue takes 4200 to 5400,
+// and the way to the next tile's first half 700 to 950.  With sums to add to (2048 x 768 fp32, 501 us) an epilogue takes
+// 27 to 42 thousand, and workgroups end 105 us before the last one on average: the busiest expert's tiles are as long as
+// 250 halves.
 //
 // Tried and slower: two workgroups of 4 waves per CU with tiles of 128 x 256 and three slots, so that one's
 // epilogue runs beside the other's products (dgrad 1000 to 1085 us, wgrad 1030, ragged 277; half as many
@@ -106,7 +112,10 @@ struct __attribute__((aligned(16))) Tile {
 __host__ __device__ __forceinline__ void units_of(int tiles_e, int tiles, int& unit, int& units_e) {
     units_e = (tiles_e + 31) / 32;
     if (tiles < 2048) {
-        // few tiles: an expert's go to all XCDs (16 skewed experts, 2048 x 1024: 84 us, else 88)
+        // Few tiles: an expert's go to all XCDs, so that a busy expert's long tiles do not stay in one (us with and without:
+        // 8 skewed experts of 4096 x 1024 180 and 198, of 1408 x 4096 165 and 172, 16 of 2048 x 1024 145 and 150; 40, 64 and
+        // 128 skewed ones level; equal ones 67 and 66, 50 and 50, 128 and 126).  It costs where short last units add a round:
+        // 2 skewed experts of 4096 x 4096 215 and 209, 3 of 8192 x 2048 443 and 332.
         const int per = tiles < 128 ? 1 : tiles / 64;
         units_e = tiles_e / per > units_e ? tiles_e / per : units_e;
         units_e = units_e < tiles_e ? units_e : tiles_e;
@@ -219,9 +228,9 @@ __global__ __launch_bounds__(kNT, 1) void grad_gemm_kernel(GradArgs g) {
     auto halves_of = [&](int e) __attribute__((always_inline)) { return (s_hi[e] - s_lo[e] + kBK - 1) / kBK; };
 
     // ---- Few tiles (and a workspace): each is cut along the contraction into `pieces`, one per workgroup, which meet
-    // through fp32 partial tiles in the workspace (dgrad of 64 rows, 14336 x 4096: 165 -> 56 us; wgrad of 8192 rows,
-    // 1024 x 1024: 164 -> 57 us).  Meeting costs 5 to 20 us, so pieces have 16 halves or more (300 rows, 520 x 264: whole
-    // 17 us, in pieces of 8 halves 22 us).
+    // through fp32 partial tiles in the workspace (dgrad of 64 rows, 14336 x 4096: 160 -> 54 us; wgrad of 8192 rows,
+    // 1024 x 1024: 167 -> 56 us).  Meeting costs 5 to 20 us, so pieces have 16 halves or more (300 rows, 520 x 264: whole
+    // 16 us, in pieces of 8 halves 21).  All tiles of a launch count, those of experts without rows among them.
     int pieces = 1;
     if (g.part && T > 0 && 2 * T <= static_cast<int>(gridDim.x)) {
         const int most = DGRAD ? (g.r1 ? 2 * nkh : nkh) : halves_of(s_order[0]);
