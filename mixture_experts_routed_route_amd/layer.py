@@ -463,8 +463,7 @@ class MoeLayer:
         for t, name in ((logits, "logits"), (x, "x"), (self.gate.w, "gate"), (self.up.w, "up"), (self.down.w, "down")):
             if t.get_device() != index:
                 raise ValueError(f"train_forward: {name} is on {t.device}, the buffers on {b.out.device}")
-        _apart("train_forward", "x", _memory(x), map(_memory, (b.g, b.u, b.h, b.ys, b.out)),
-               "a buffer that the step replaces before its backward reads x")
+        _apart("train_forward", "x", _memory(x), (_memory(b.g), _memory(b.u)), "a buffer that is replaced before its last use")
         b.forward_done = False
         moe_route_align(logits, self.top_k, self.renormalize, self.bs, b.ids, b.w, b.routing)
         moe_grouped_gemm(MOE_OP_GATHER, x, self.gate, None, b.routing, out=b.g, workspace=b.ws)
@@ -509,14 +508,14 @@ class MoeLayer:
             read.append(_operand(w.w, "one of the weights", shape, bf, device))
         kept = [_memory(t) for t in (b.g, b.u, b.h, b.ys, b.out)]
         _apart("train_backward", "d_out", d_out_at, kept[:3], "a buffer that is replaced before its last use")
-        _apart("train_backward", "x", x_at, kept, "a buffer that the step replaces before it reads x")
+        _apart("train_backward", "x", x_at, kept, "a buffer that the step has replaced")
         if grads is None:
             grads = tuple(torch.empty_like(w.w) for w in weights)
         dg, du, dd = grads
         for t, shape in zip(grads, shapes):
             at = _operand(t, "one of grads", shape, bf + f32, device)
             _apart("train_backward", "one of grads", at, read, "another one or an operand")
-            _apart("train_backward", "one of grads", at, kept, "one of the step's buffers")
+            _apart("train_backward", "one of grads", at, kept[:4], "one of the step's buffers")
             read.append(at)
         other = b.forward_of  # (another layer object over the same weights is the same layer)
         if other is not self and (other is None or other.renormalize != self.renormalize or any(

@@ -71,8 +71,6 @@ def test_one_tensor_for_two_gradients_is_refused(m):
     g = sums(layer, 0.5)
     with pytest.raises(ValueError, match="grads"):
         layer.train_backward(d_out, x, b, grads=(g[0], g[0], g[2]), accumulate=True)
-    with pytest.raises(ValueError, match="x lies over"):
-        layer.train_forward(logits, b.out, b)
     assert all((t == 0.5).all() for t in g)
     layer.train_backward(d_out, x, b, grads=g, accumulate=True)
 
@@ -111,3 +109,17 @@ def test_masks_follow_rng_alone(m):
     b.rng[1] += 1
     assert not torch.equal(layer.train_forward(logits, x, b), first)
     assert not torch.equal(layer.train_forward(logits, x, layer.train_plan(T, "cuda", dropout=0.5, seed=5)), first)
+
+
+def test_forwards_over_one_output(m):
+    """Forward passes alone on shared buffers may hand the output on in place; a backward without its x is refused."""
+    T, H, I, E, k = 40, 72, 40, 4, 2
+    (a, logits, x, d_out), (c, *_) = make(m, T, H, I, E, k), make(m, T, H, I, E, k, seed=1)
+    b, other = a.train_plan(T, "cuda"), a.train_plan(T, "cuda")
+    between = a.train_forward(logits, x, b).clone()
+    want = c.train_forward(logits, between, other).clone()
+    assert torch.equal(c.train_forward(logits, b.out, b), want)
+    with pytest.raises(ValueError, match="x lies over"):
+        c.train_backward(d_out, b.out, b)
+    got, ref = c.train_backward(d_out, between, b)[2], c.train_backward(d_out, between, other)[2]
+    assert all(torch.equal(p, q) for p, q in zip(got, ref))

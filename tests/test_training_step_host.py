@@ -129,20 +129,21 @@ def test_operands_over_buffers(name):
     b = ready(a)
     over = at(getattr(b, name), (T, H), byte=16)
     refused(a, b, "train_backward: x ", x=over)
-    with pytest.raises(ValueError, match="train_forward: x "):
-        a.train_forward(torch.zeros(T, E), over, b)
-    assert b.forward_done
+    if name in ("g", "u"):   # h, ys and out are replaced after the forward's last use of x: a forward alone may take it there
+        with pytest.raises(ValueError, match="train_forward: x "):
+            a.train_forward(torch.zeros(T, E), over, b)
+        assert b.forward_done
     if name != "ys":
         refused(a, b, "train_backward: d_out ", d_out=over)
 
 
 def test_x_over_the_output():
-    """A layer's output in the buffers is replaced by the next forward on them: not its x as well."""
+    """The buffers' output may be the x of a forward, which replaces it at its end; its backward has no x there any more."""
     a = layer()
     b = ready(a)
-    with pytest.raises(ValueError, match="train_forward: x "):
-        a.train_forward(torch.zeros(T, E), b.out, b)
     refused(a, b, "train_backward: x ", x=b.out)
+    with pytest.raises(ValueError, match="HIP device"):   # past the checks
+        a.train_forward(torch.zeros(T, E), b.out, b)
 
 
 @pytest.mark.parametrize("name", ["out", "d_x", "ys"])
